@@ -356,6 +356,131 @@ void muon_adamw_hparams_default(muon_adamw_hparams *hp);
 int muon_adamw_step(muon_ctx *ctx, const muon_adamw_tensor *tensors, int count,
                     const muon_adamw_hparams *hp, void *stream);
 
+/* ---- What a training step runs before the updates ----
+ * The gated feed-forward block, whose three matrices are the gate / up / down entries of a
+ * decoder's Muon list (its backward writes or accumulates the G arrays muon_step reads),
+ * and two losses over vocabulary logits, each with its gradient. Conventions as above, and:
+ *   - matrices are row-major with unit column stride and the given row strides (ld, in
+ *     elements), at any element alignment; 16-byte aligned rows are read in place, others
+ *     are first copied into the workspace (the feed-forward block) or read as they are
+ *     (the losses);
+ *   - the calls only read the context: several threads may make them on one context;
+ *   - results do not change from run to run (no atomics; fixed summation orders).
+ * These operators are not on the pages the update is built from; the formulas are given. */
+#define MUON_ACT_SILU 0       /* act(g) = g / (1 + exp(-g)) */
+#define MUON_ACT_GELU_TANH 1  /* act(g) = g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+
+/* g = x w_gate^T, u = x w_up^T, h = act(g) * u (element-wise), y = h w_down^T.
+ * x: tokens x dim; w_gate, w_up: hidden x dim; w_down: dim x hidden, all in `dtype`.
+ * tokens in [0, 2^24], dim and hidden in [1, 2^20], row strides up to 2^21.
+ * MUON_BF16: products accumulate in fp32 on the bf16 matrix instructions; h (and in the
+ * backward dg, du) are rounded to bf16 once, as operands of the next product; g and u are
+ * saved for the backward in fp32. MUON_F32: fp32 throughout. */
+typedef struct muon_ffn {
+  const void *x, *w_gate, *w_up, *w_down;
+  int64_t ld_x, ld_gate, ld_up, ld_down;
+  int64_t tokens, dim, hidden;
+  int32_t dtype;       /* MUON_F32 or MUON_BF16: x, weights, y, dy, dx */
+  int32_t activation;  /* MUON_ACT_* */
+} muon_ffn;
+
+/* Operands of the backward: dy and dx are tokens x dim in the block's dtype; the weight
+ * gradients have the weights' shapes, in g_dtype. dx and each of g_gate, g_up, g_down may be
+ * null (not wanted). accumulate != 0 adds to the weight gradients (in fp32, then rounded to
+ * g_dtype) instead of overwriting them. `saved` is what muon_ffn_forward wrote. */
+typedef struct muon_ffn_grads {
+  const void *dy;
+  const void *saved;
+  void *dx, *g_gate, *g_up, *g_down;
+  int64_t ld_dy, ld_dx, ld_g_gate, ld_g_up, ld_g_down;
+  int32_t g_dtype;
+  int32_t accumulate;
+} muon_ffn_grads;
+
+/* Bytes of workspace (256-byte aligned) muon_ffn_forward (g null) or muon_ffn_backward (g
+ * given) needs, and bytes of the `saved` buffer (16-byte aligned) a forward for training
+ * fills: 8 per token and hidden column, hidden rounded up to 64. Either output pointer may be
+ * null. Depends on the sizes, strides, dtype and the alignment of the array pointers (null:
+ * aligned) and on which gradients are wanted. */
+int muon_ffn_workspace_size(muon_ctx *ctx, const muon_ffn *f, const muon_ffn_grads *g, size_t *workspace,
+                            size_t *saved);
+
+/* y (tokens x dim), enqueued on `stream`. saved: null, or the buffer that receives g and u
+ * for muon_ffn_backward. No tokens: a no-op. y must not overlap the inputs. */
+int muon_ffn_forward(muon_ctx *ctx, const muon_ffn *f, void *y, int64_t ld_y, void *saved, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* The gradients named by g for the same f as the forward (its x and weights unchanged):
+ *   dh = dy w_down, du = dh act(g), dg = dh u act'(g), dx = dg w_gate + du w_up,
+ *   g_gate = dg^T x, g_up = du^T x, g_down = dy^T h.
+ * No tokens: the weight gradients become zero (accumulate: stay). Outputs must not overlap
+ * the inputs or each other. */
+int muon_ffn_backward(muon_ctx *ctx, const muon_ffn *f, const muon_ffn_grads *g, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Logits (rows x vocab, in `dtype`; vocab up to 2^28) and what every loss does with them: with
+ * z = logits / temperature, loss[r] = weights[r] l_r and
+ * dlogits = d(sum_r grad_rows[r] loss[r]) / dlogits, rounded once to `dtype`; computed in
+ * fp32. A row of weight 0 takes no part: its logits are not read, its loss is 0 and its
+ * gradient row is written as zeros. dlogits null: no gradient. dlogits may be `logits` itself
+ * (same stride; the gradient replaces the logits), else must not overlap it. With lse_given
+ * the normaliser is read from lse instead of computed (one pass less): a backward after a
+ * forward that kept it. Without a gradient and with lse given only the rows' own entries are
+ * read. */
+typedef struct muon_logits {
+  const void *logits;
+  void *dlogits;
+  const float *weights;    /* rows, or null: 1 */
+  const float *grad_rows;  /* rows, or null: 1 */
+  float *loss;             /* rows, or null */
+  float *lse;              /* rows: log sum exp z (0 for rows that take no part), or null */
+  int64_t ld, ld_d;
+  int64_t rows, vocab;
+  float temperature;       /* finite, > 0 */
+  int32_t dtype;           /* MUON_F32 or MUON_BF16 */
+  int32_t lse_given;       /* 0 or 1 */
+} muon_logits;
+
+/* Clipped policy loss with a KL term. Row r with target t, lp = z_t - lse,
+ * rho = exp(lp - old_logp), A the advantage:
+ *   l = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A)
+ *       + kl_coef (exp(ref_logp - lp) - (ref_logp - lp) - 1)
+ * The gradient of the first term is that of -rho A where rho A is the smaller (or equal),
+ * else 0. A target outside [0, vocab) takes no part, like a row of weight 0. */
+typedef struct muon_policy {
+  const int64_t *targets;   /* rows */
+  const float *old_logp;    /* rows */
+  const float *advantages;  /* rows */
+  const float *ref_logp;    /* rows; may be null when kl_coef is 0 */
+  float *logp;              /* rows: lp (0 for rows that take no part), or null */
+  float clip_low, clip_high;  /* 0 <= clip_low <= 1, clip_high >= 0 */
+  float kl_coef;
+} muon_policy;
+
+int muon_policy_loss(muon_ctx *ctx, const muon_logits *l, const muon_policy *t, void *stream);
+
+/* Distillation from a teacher's `top` kept logits per row (entry j: logit t_j at column
+ * i_j), p_j = exp(t_j / temperature - L) with L = top_lse[r], the teacher's log sum exp of its
+ * logits / temperature over its whole vocabulary (the p_j then sum to less than 1), or, with
+ * top_lse null, over the kept entries:
+ *   l = sum_j p_j (log p_j - (z_{i_j} - lse))
+ * An entry whose column is outside [0, vocab) or whose logit is -inf is absent (p_j = 0);
+ * entries that name one column twice both count. */
+#define MUON_I32 2
+#define MUON_I64 3
+#define MUON_MAX_TOP 1024
+typedef struct muon_distill {
+  const void *top_logits;  /* rows x top, in top_dtype */
+  const void *top_ids;     /* rows x top, in id_dtype */
+  const float *top_lse;    /* rows, or null */
+  int64_t ld_top, ld_ids;
+  int32_t top;             /* 1..MUON_MAX_TOP */
+  int32_t top_dtype;       /* MUON_F32 or MUON_BF16 */
+  int32_t id_dtype;        /* MUON_I32 or MUON_I64 */
+} muon_distill;
+
+int muon_distill_loss(muon_ctx *ctx, const muon_logits *l, const muon_distill *t, void *stream);
+
 /* ---- Owner assignment: which rank updates which matrix ----
  * DMuon summary (gist.science), section 2.3 (compute-aware load balancing): the update
  * cost varies strongly with the matrix shape, so each matrix is given one owner rank to

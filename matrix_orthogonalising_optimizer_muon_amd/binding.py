@@ -93,6 +93,48 @@ class muon_adamw_hparams(ctypes.Structure):
                 ("w_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32)]
 
 
+MUON_ACT_SILU, MUON_ACT_GELU_TANH = 0, 1
+MUON_I32, MUON_I64 = 2, 3
+MUON_MAX_TOP = 1024
+ACTIVATIONS = {"silu": MUON_ACT_SILU, "gelu_tanh": MUON_ACT_GELU_TANH}
+
+
+class muon_ffn(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
+                ("w_down", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("ld_gate", ctypes.c_int64),
+                ("ld_up", ctypes.c_int64), ("ld_down", ctypes.c_int64), ("tokens", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("hidden", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
+
+
+class muon_ffn_grads(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("saved", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("g_gate", ctypes.c_void_p), ("g_up", ctypes.c_void_p), ("g_down", ctypes.c_void_p),
+                ("ld_dy", ctypes.c_int64), ("ld_dx", ctypes.c_int64), ("ld_g_gate", ctypes.c_int64),
+                ("ld_g_up", ctypes.c_int64), ("ld_g_down", ctypes.c_int64), ("g_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
+class muon_logits(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dlogits", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("grad_rows", ctypes.c_void_p), ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("ld", ctypes.c_int64), ("ld_d", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("temperature", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("lse_given", ctypes.c_int32)]
+
+
+class muon_policy(ctypes.Structure):
+    _fields_ = [("targets", ctypes.c_void_p), ("old_logp", ctypes.c_void_p), ("advantages", ctypes.c_void_p),
+                ("ref_logp", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("clip_low", ctypes.c_float),
+                ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float)]
+
+
+class muon_distill(ctypes.Structure):
+    _fields_ = [("top_logits", ctypes.c_void_p), ("top_ids", ctypes.c_void_p), ("top_lse", ctypes.c_void_p),
+                ("ld_top", ctypes.c_int64), ("ld_ids", ctypes.c_int64), ("top", ctypes.c_int32),
+                ("top_dtype", ctypes.c_int32), ("id_dtype", ctypes.c_int32)]
+
+
 MUON_MAX_COST_POINTS = 16
 MUON_MAX_PLAN_RANKS = 4096
 MUON_PLAN_GREEDY = 1
@@ -151,6 +193,18 @@ _lib.muon_adamw_hparams_default.restype = None
 _lib.muon_adamw_step.argtypes = [_P, ctypes.POINTER(muon_adamw_tensor), ctypes.c_int,
                                  ctypes.POINTER(muon_adamw_hparams), _P]
 _lib.muon_adamw_step.restype = ctypes.c_int
+_lib.muon_ffn_workspace_size.argtypes = [_P, ctypes.POINTER(muon_ffn), ctypes.POINTER(muon_ffn_grads),
+                                         ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)]
+_lib.muon_ffn_workspace_size.restype = ctypes.c_int
+_lib.muon_ffn_forward.argtypes = [_P, ctypes.POINTER(muon_ffn), _P, ctypes.c_int64, _P, _P, ctypes.c_size_t, _P]
+_lib.muon_ffn_forward.restype = ctypes.c_int
+_lib.muon_ffn_backward.argtypes = [_P, ctypes.POINTER(muon_ffn), ctypes.POINTER(muon_ffn_grads), _P,
+                                   ctypes.c_size_t, _P]
+_lib.muon_ffn_backward.restype = ctypes.c_int
+_lib.muon_policy_loss.argtypes = [_P, ctypes.POINTER(muon_logits), ctypes.POINTER(muon_policy), _P]
+_lib.muon_policy_loss.restype = ctypes.c_int
+_lib.muon_distill_loss.argtypes = [_P, ctypes.POINTER(muon_logits), ctypes.POINTER(muon_distill), _P]
+_lib.muon_distill_loss.restype = ctypes.c_int
 _lib.muon_destroy.argtypes = [_P]
 _lib.muon_destroy.restype = ctypes.c_int
 _lib.muon_status_str.argtypes = [ctypes.c_int]
@@ -402,6 +456,32 @@ def muon_adamw_step(ctx, tensors, hp: muon_adamw_hparams, stream_ptr=None, count
     return _lib.muon_adamw_step(ctx, arr, n, ctypes.byref(hp), stream_ptr)
 
 
+def muon_ffn_workspace_size(ctx, f: muon_ffn, g: muon_ffn_grads | None = None) -> tuple:
+    """(workspace bytes of the forward, or of the backward when ``g`` is given; bytes of the
+    ``saved`` buffer)."""
+    ws, saved = ctypes.c_size_t(), ctypes.c_size_t()
+    check(_lib.muon_ffn_workspace_size(ctx, f, g, ws, saved), "muon_ffn_workspace_size")
+    return ws.value, saved.value
+
+
+def muon_ffn_forward(ctx, f: muon_ffn, y: int, ld_y: int, saved: int | None, workspace: int | None,
+                     workspace_bytes: int, stream_ptr: int | None) -> int:
+    return _lib.muon_ffn_forward(ctx, f, y, ld_y, saved, workspace, workspace_bytes, stream_ptr)
+
+
+def muon_ffn_backward(ctx, f: muon_ffn, g: muon_ffn_grads, workspace: int | None, workspace_bytes: int,
+                      stream_ptr: int | None) -> int:
+    return _lib.muon_ffn_backward(ctx, f, g, workspace, workspace_bytes, stream_ptr)
+
+
+def muon_policy_loss(ctx, l: muon_logits, t: muon_policy, stream_ptr: int | None) -> int:
+    return _lib.muon_policy_loss(ctx, l, t, stream_ptr)
+
+
+def muon_distill_loss(ctx, l: muon_logits, t: muon_distill, stream_ptr: int | None) -> int:
+    return _lib.muon_distill_loss(ctx, l, t, stream_ptr)
+
+
 def shape_cost(points) -> muon_shape_cost:
     """A ``muon_shape_cost`` from [(batch, ms), ...] measured points."""
     c = muon_shape_cost()
@@ -440,5 +520,6 @@ def exported_symbols() -> list:
     return [n for n in ("muon_hparams_default", "muon_init", "muon_workspace_size", "muon_step", "muon_step_static", "muon_prepare",
                         "muon_plan_info", "muon_debug_gemm", "muon_debug_stage", "muon_profile_read", "muon_tune_save",
                         "muon_tune_load", "muon_adamw_hparams_default", "muon_adamw_step",
-                        "muon_destroy", "muon_status_str", "muon_owner_plan")
+                        "muon_destroy", "muon_status_str", "muon_owner_plan", "muon_ffn_workspace_size",
+                        "muon_ffn_forward", "muon_ffn_backward", "muon_policy_loss", "muon_distill_loss")
             if hasattr(_lib, n)]

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build", "muon_amd")
 LIB = os.path.join(PKG, "libmuon_amd.so")
-SOURCES = ["api.cpp", "gemm.hip", "elementwise.hip", "small.hip", "adamw.hip", "planner.cpp"]
+SOURCES = ["api.cpp", "gemm.hip", "elementwise.hip", "small.hip", "adamw.hip", "planner.cpp",
+           "train_api.cpp", "ffn.hip", "losses.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -66,7 +67,7 @@ def build(verbose: bool = False) -> str:
 # the regular build are reused when they are newer than their sources.
 SAN_OBJ = os.path.join(ROOT, "_build", "asan")
 SAN_LIB = os.path.join(SAN_OBJ, "libmuon_amd_asan.so")
-SAN_SOURCES = ["api.cpp", "planner.cpp"]
+SAN_SOURCES = ["api.cpp", "planner.cpp", "train_api.cpp"]
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=all"]
 

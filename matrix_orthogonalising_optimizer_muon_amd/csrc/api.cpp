@@ -52,6 +52,10 @@ struct muon_ctx {
 };
 
 namespace muon {
+
+int ctx_device(const muon_ctx* ctx) { return ctx->device; }
+int ctx_cus(const muon_ctx* ctx) { return ctx->cu_count; }
+
 namespace {
 
 constexpr int64_t kPad = 64;          // canonical dims are padded to multiples of 64
@@ -600,11 +604,6 @@ hipError_t apply(const Group& g, const StepEnv& env, const void* Q, const void* 
   return e;
 }
 
-#define MUON_HIP(call)                       \
-  do {                                       \
-    if ((call) != hipSuccess) return MUON_ERR_HIP; \
-  } while (0)
-
 // True when every GEMM stage the group will launch already has a measured tile (or the
 // context does not measure): such a group makes no host synchronisation and may run on
 // a stream of its own next to other groups.
@@ -788,18 +787,6 @@ int run_group(const Group& g, const StepEnv& env, MatDesc* table, const MatDesc*
   }
   return MUON_OK;
 }
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) == hipSuccess && hipSetDevice(dev) == hipSuccess) ok = true;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) (void)hipSetDevice(prev);
-  }
-};
-
 
 // File-scope scratch for muon_step_static (callers that cannot allocate device memory).
 // Each device holds its own copy; host code uses only the per-device address that

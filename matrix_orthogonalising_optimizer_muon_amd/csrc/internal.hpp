@@ -4,7 +4,27 @@
 #include <hip/hip_runtime.h>
 #include <cstdint>
 
+struct muon_ctx;
+
 namespace muon {
+
+// Front-end helpers shared by api.cpp and train_api.cpp.
+#define MUON_HIP(call)                       \
+  do {                                       \
+    if ((call) != hipSuccess) return MUON_ERR_HIP; \
+  } while (0)
+int ctx_device(const muon_ctx* ctx);  // -1: host-only
+int ctx_cus(const muon_ctx* ctx);
+struct DeviceGuard {
+  int prev = -1;
+  bool ok = false;
+  explicit DeviceGuard(int dev) {
+    if (hipGetDevice(&prev) == hipSuccess && hipSetDevice(dev) == hipSuccess) ok = true;
+  }
+  ~DeviceGuard() {
+    if (prev >= 0) (void)hipSetDevice(prev);
+  }
+};
 
 // Per-matrix descriptor, written into the workspace at the start of every step.
 struct MatDesc {
@@ -227,6 +247,71 @@ struct AdamChunk {
 };
 int64_t adam_blocks(int64_t numel);
 hipError_t launch_adamw(const AdamChunk& c, int64_t blocks, hipStream_t st);
+
+// Gated feed-forward block (ffn.hip): one product kernel, out(m, n) = sum_k A(m, k) B(n, k).
+constexpr int kActSilu = 0, kActGeluTanh = 1;
+enum FfnEpi : int { FFN_STORE = 0, FFN_GATE = 1, FFN_DGATE = 2 };
+enum FfnStage : int {
+  FFN_STAGE_GATE = 0,   // h = act(x Wg^T) (x Wu^T); x, Wg, Wu K-contiguous
+  FFN_STAGE_DOWN = 1,   // y = h Wd^T; both K-contiguous
+  FFN_STAGE_DGATE = 2,  // dh = dy Wd, then dg, du, h; Wd K-strided
+  FFN_STAGE_DX = 3,     // dx = [dg du] [Wg; Wu]; weights K-strided, two K segments
+  FFN_STAGE_DW = 4,     // A^T B over the tokens; both K-strided
+};
+enum FfnTile : int { FFN_TILE_64x128 = 0, FFN_TILE_128 = 1, FFN_TILE_256 = 2, FFN_TILE_COUNT = 3 };
+struct FfnGemm {
+  const void* A[2];       // operand of K segment 0 / 1, or of batch entry 0 / 1 (batched)
+  const void* B[2];       // operand of K segment 0 / 1, or Wg / Wu (FFN_GATE)
+  int64_t lda, ldb, ldb1; // row strides in elements (ldb1: of B[1]); rows 16-byte aligned
+  int32_t M, N;           // output rows and columns (FFN_GATE: columns of one of g, u)
+  int64_t K;              // valid k of a segment (rows of a K-strided operand)
+  int64_t KA;             // valid k of A's rows when A is K-contiguous (K, or its zero-padded size)
+  int32_t tail;           // K mod BK of the last slice's K-contiguous operands, 0: whole
+  int32_t slices0;        // slices of K segment 0
+  int32_t slices;         // slices of all segments
+  int32_t slices_per_split, splits;
+  int32_t tiles_m, tiles_n, tiles;
+  int32_t batched;        // A and C indexed by batch entry
+  void* C[3];             // FFN_STORE: outputs by batch entry; FFN_GATE: h; FFN_DGATE: dg, du, h
+  int64_t ldc;
+  int64_t Np;             // row stride of the padded intermediates (h, g, u, dg, du, partials)
+  float* gu;              // saved g, then u gu_stride elements later; null: not saved
+  int64_t gu_stride;
+  float* part;            // fp32 partial products [batch][split][M][Np]; null: one split
+  int32_t act;
+  int32_t c_bf16, c_vec, accumulate;
+};
+hipError_t launch_ffn(FfnStage stage, bool f32, int tile, const FfnGemm& p, int batches, hipStream_t st);
+hipError_t launch_ffn_align(const void* src, int64_t ld, void* dst, int64_t ldd, int64_t rows, int cols, bool f32,
+                            hipStream_t st);
+hipError_t launch_ffn_zero(void* out, int64_t ld, int64_t rows, int64_t cols, bool bf16, hipStream_t st);
+
+// Losses over vocabulary logits (losses.hip): one workgroup per row.
+enum LossKind : int { LOSS_POLICY = 0, LOSS_DISTILL = 1 };
+constexpr int kMaxTop = 1024;  // kept teacher entries per row
+struct LossParams {
+  const void* logits; int64_t ld;
+  void* dlogits; int64_t ld_d;      // null: no gradient
+  int64_t rows;
+  int32_t vocab;
+  float inv_temperature;
+  const float* weights;             // null: 1
+  const float* grad_rows;           // null: 1
+  float* loss;                      // null: not written
+  float* lse;                       // written, or read with lse_given; may be null otherwise
+  int32_t lse_given;
+  // policy
+  const int64_t* targets;
+  const float* old_logp; const float* advantages; const float* ref_logp;
+  float clip_low, clip_high, kl_coef;
+  float* logp;
+  // distill
+  const void* top_logits; int64_t ld_top;
+  const void* ids; int64_t ld_ids;
+  const float* top_lse;             // null: normalised over the kept entries
+  int32_t top, top_bf16, ids64;
+};
+hipError_t launch_loss(int loss, bool bf16, const LossParams& p, hipStream_t st);
 
 hipError_t launch_write_table(const TableChunk& c, MatDesc* dst, hipStream_t st);
 

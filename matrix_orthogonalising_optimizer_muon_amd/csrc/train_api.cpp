@@ -1,0 +1,441 @@
+// C-ABI front end of the training operators beside the updates: argument validation, the
+// workspace plan and the launches of the gated feed-forward block (forward, backward) and
+// of the losses over vocabulary logits. The calls only read the context, so several
+// threads may make them on one context at once.
+#include "../../include/muon.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "internal.hpp"
+
+namespace muon {
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t{1} << 24;
+constexpr int64_t kMaxDim = int64_t{1} << 20;
+constexpr int64_t kMaxLd = int64_t{1} << 21;   // a tile's 256 rows stay within 32-bit byte offsets
+constexpr size_t kAlign = 256;
+
+inline int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+inline int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
+inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+inline bool dtype_ok(int d) { return d == MUON_F32 || d == MUON_BF16; }
+inline int64_t size_of(int d) { return d == MUON_F32 ? 4 : 2; }
+inline bool aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// ---- gated feed-forward block ----
+
+int validate(const muon_ffn* f, bool need_pointers) {
+  if (!f || !dtype_ok(f->dtype)) return MUON_ERR_ARG;
+  if (f->activation != MUON_ACT_SILU && f->activation != MUON_ACT_GELU_TANH) return MUON_ERR_ARG;
+  if (f->tokens < 0 || f->tokens > kMaxTokens) return MUON_ERR_ARG;
+  if (f->dim < 1 || f->dim > kMaxDim || f->hidden < 1 || f->hidden > kMaxDim) return MUON_ERR_ARG;
+  auto ld_ok = [](int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxLd; };
+  if (!ld_ok(f->ld_x, f->dim) || !ld_ok(f->ld_gate, f->dim) || !ld_ok(f->ld_up, f->dim) ||
+      !ld_ok(f->ld_down, f->hidden))
+    return MUON_ERR_ARG;
+  const int64_t es = size_of(f->dtype);
+  if (!aligned(f->x, es) || !aligned(f->w_gate, es) || !aligned(f->w_up, es) || !aligned(f->w_down, es))
+    return MUON_ERR_ARG;
+  if (need_pointers && ((f->tokens > 0 && !f->x) || !f->w_gate || !f->w_up || !f->w_down)) return MUON_ERR_ARG;
+  return MUON_OK;
+}
+
+int validate(const muon_ffn* f, const muon_ffn_grads* g, bool need_pointers) {
+  if (!dtype_ok(g->g_dtype) || (g->accumulate != 0 && g->accumulate != 1)) return MUON_ERR_ARG;
+  auto ld_ok = [](int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxLd; };
+  if (!ld_ok(g->ld_dy, f->dim) || (g->dx && !ld_ok(g->ld_dx, f->dim)) || (g->g_gate && !ld_ok(g->ld_g_gate, f->dim)) ||
+      (g->g_up && !ld_ok(g->ld_g_up, f->dim)) || (g->g_down && !ld_ok(g->ld_g_down, f->hidden)))
+    return MUON_ERR_ARG;
+  const int64_t es = size_of(f->dtype), gs = size_of(g->g_dtype);
+  if (!aligned(g->dy, es) || !aligned(g->dx, es) || !aligned(g->g_gate, gs) || !aligned(g->g_up, gs) ||
+      !aligned(g->g_down, gs) || !aligned(g->saved, 16))
+    return MUON_ERR_ARG;
+  if (need_pointers && f->tokens > 0 && (!g->dy || !g->saved)) return MUON_ERR_ARG;
+  return MUON_OK;
+}
+
+// Workspace, in order of use. Offsets are filled whether or not memory is there.
+struct Arena {
+  size_t at = 0;
+  size_t take(size_t bytes) {
+    const size_t here = at;
+    at = align_up(at + bytes);
+    return here;
+  }
+};
+
+// An operand as the product kernel reads it: the caller's array where its rows are 16-byte
+// aligned, else a copy in the workspace whose rows are.
+struct Operand {
+  const void* p = nullptr;
+  int64_t ld = 0;
+  bool copied = false;
+  size_t off = 0;
+  const void* src = nullptr;
+  int64_t src_ld = 0, rows = 0, cols = 0;
+};
+
+Operand operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t es, Arena& a) {
+  Operand o;
+  o.src = p; o.src_ld = ld; o.rows = rows; o.cols = cols;
+  o.p = p; o.ld = ld;
+  if (!aligned(p, 16) || ld * es % 16 != 0) {
+    o.copied = true;
+    o.ld = round_up(cols, 16 / es);
+    o.off = a.take(static_cast<size_t>(rows * o.ld * es));
+  }
+  return o;
+}
+
+// Tile and K split of one product. The 256 tile carries the most products per LDS byte and
+// is taken when its tiles fill the GPU; smaller tiles, and for plain outputs a split of K
+// joined by a second kernel, keep more CUs busy otherwise.
+struct Shape {
+  int tile = FFN_TILE_128, splits = 1;
+  int64_t slices = 0, per_split = 0;
+  int64_t tiles_m = 0, tiles_n = 0;
+};
+
+Shape choose(bool f32, int64_t M, int64_t cols, int64_t slices, int batches, bool may_split, int cus) {
+  static const int bm[FFN_TILE_COUNT] = {64, 128, 256}, bn[FFN_TILE_COUNT] = {128, 128, 256};
+  Shape s;
+  auto tiles = [&](int t) { return cdiv(M, bm[t]) * cdiv(cols, bn[t]) * batches; };
+  s.tile = FFN_TILE_64x128;
+  if (!f32 && tiles(FFN_TILE_256) >= cus * 3 / 4) s.tile = FFN_TILE_256;
+  else if (tiles(FFN_TILE_128) >= cus * 3 / 4) s.tile = FFN_TILE_128;
+  s.tiles_m = cdiv(M, bm[s.tile]);
+  s.tiles_n = cdiv(cols, bn[s.tile]);
+  s.slices = slices;
+  if (may_split && tiles(s.tile) < cus) {
+    // at least 8 slices to a split, at most 16 splits
+    const int64_t want = std::min<int64_t>({cdiv(cus, tiles(s.tile)), slices / 8, 16});
+    s.splits = static_cast<int>(std::max<int64_t>(1, want));
+  }
+  s.per_split = cdiv(slices, s.splits);
+  s.splits = static_cast<int>(cdiv(slices, s.per_split));
+  return s;
+}
+
+// Everything muon_ffn_forward / muon_ffn_backward launch, from the sizes and alignments.
+struct FfnPlan {
+  int64_t es = 2, bk = 64, Hp = 0;
+  Operand x, wg, wu, wd, dy;
+  size_t off_h = 0, off_dg = 0, off_du = 0, off_part = 0, bytes = 0;
+  Shape gate, down, dgate, dx, dgu, dwd;
+};
+
+size_t part_bytes(const Shape& s, int batches, int64_t M, int64_t N) {
+  return s.splits > 1 ? static_cast<size_t>(batches) * s.splits * M * round_up(N, 4) * 4 : 0;
+}
+
+FfnPlan plan_of(const muon_ffn* f, const muon_ffn_grads* g, int cus) {
+  FfnPlan p;
+  const bool f32 = f->dtype == MUON_F32;
+  p.es = size_of(f->dtype);
+  p.bk = 128 / p.es;
+  p.Hp = round_up(f->hidden, 64);
+  const int64_t T = f->tokens, D = f->dim, F = f->hidden;
+  if (T == 0) return p;  // nothing is launched on tiles
+  Arena a;
+  const size_t inter = static_cast<size_t>(T * p.Hp * p.es);
+  p.x = operand(f->x, f->ld_x, T, D, p.es, a);
+  p.wd = operand(f->w_down, f->ld_down, D, F, p.es, a);
+  p.wg = operand(f->w_gate, f->ld_gate, F, D, p.es, a);
+  p.wu = operand(f->w_up, f->ld_up, F, D, p.es, a);
+  p.off_h = a.take(inter);
+  size_t part = 0;
+  if (!g) {
+    p.gate = choose(f32, T, 2 * F, cdiv(D, p.bk), 1, false, cus);
+    p.down = choose(f32, T, D, cdiv(F, p.bk), 1, true, cus);
+    part = part_bytes(p.down, 1, T, D);
+  } else {
+    p.dy = operand(g->dy, g->ld_dy, T, D, p.es, a);
+    p.off_dg = a.take(inter);
+    p.off_du = a.take(inter);
+    const int n = (g->g_gate && g->g_up) ? 2 : 1;
+    p.dgate = choose(f32, T, F, cdiv(D, p.bk), 1, false, cus);
+    p.dx = choose(f32, T, D, 2 * (p.Hp / p.bk), 1, true, cus);
+    p.dgu = choose(f32, F, D, cdiv(T, p.bk), n, true, cus);
+    p.dwd = choose(f32, D, F, cdiv(T, p.bk), 1, true, cus);
+    if (g->dx) part = std::max(part, part_bytes(p.dx, 1, T, D));
+    if (g->g_gate || g->g_up) part = std::max(part, part_bytes(p.dgu, n, F, D));
+    if (g->g_down) part = std::max(part, part_bytes(p.dwd, 1, D, F));
+  }
+  p.off_part = a.take(part);
+  p.bytes = a.at;
+  return p;
+}
+
+hipError_t settle(Operand& o, char* ws, bool f32, hipStream_t st) {
+  if (!o.copied) return hipSuccess;
+  o.p = ws + o.off;
+  return launch_ffn_align(o.src, o.src_ld, ws + o.off, o.ld, o.rows, static_cast<int>(o.cols), f32, st);
+}
+
+FfnGemm product(const Shape& s, int64_t M, int64_t N, int64_t K, int act) {
+  FfnGemm q;
+  std::memset(&q, 0, sizeof(q));
+  q.M = static_cast<int32_t>(M);
+  q.N = static_cast<int32_t>(N);
+  q.K = q.KA = K;
+  q.slices0 = q.slices = static_cast<int32_t>(s.slices);
+  q.slices_per_split = static_cast<int32_t>(s.per_split);
+  q.splits = s.splits;
+  q.tiles_m = static_cast<int32_t>(s.tiles_m);
+  q.tiles_n = static_cast<int32_t>(s.tiles_n);
+  q.tiles = q.tiles_m * q.tiles_n;
+  q.act = act;
+  return q;
+}
+
+// A plain output: type, row stride, and whether 4 elements of a row are one aligned store.
+void output(FfnGemm& q, const Shape& s, char* part, bool bf16, int64_t ldc, bool accumulate) {
+  const int64_t es = bf16 ? 2 : 4;
+  q.c_bf16 = bf16;
+  q.ldc = ldc;
+  q.accumulate = accumulate;
+  q.c_vec = ldc % 4 == 0 && aligned(q.C[0], 4 * es) && (!q.C[1] || aligned(q.C[1], 4 * es));
+  if (s.splits > 1) {
+    q.part = reinterpret_cast<float*>(part);
+    q.Np = round_up(q.N, 4);
+  }
+}
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return MUON_OK;
+  return !ws || have < need || !aligned(ws, kAlign) ? MUON_ERR_WORKSPACE : MUON_OK;
+}
+
+// ---- losses ----
+
+int validate(const muon_logits* l) {
+  if (!l || !dtype_ok(l->dtype)) return MUON_ERR_ARG;
+  if (l->rows < 0 || l->rows > 0x7FFFFFFF || l->vocab < 1 || l->vocab > (int64_t{1} << 28)) return MUON_ERR_ARG;
+  if (l->ld < l->vocab || (l->dlogits && l->ld_d < l->vocab)) return MUON_ERR_ARG;
+  if (!std::isfinite(l->temperature) || !(l->temperature > 0.0f) || !std::isfinite(1.0f / l->temperature))
+    return MUON_ERR_ARG;
+  if (l->lse_given != 0 && l->lse_given != 1) return MUON_ERR_ARG;
+  const int64_t es = size_of(l->dtype);
+  if (!aligned(l->logits, es) || !aligned(l->dlogits, es)) return MUON_ERR_ARG;
+  if (l->rows > 0 && (!l->logits || (l->lse_given && !l->lse))) return MUON_ERR_ARG;
+  // in place only as a whole: the same rows
+  if (l->dlogits == l->logits && l->dlogits && l->ld_d != l->ld) return MUON_ERR_ARG;
+  return MUON_OK;
+}
+
+LossParams params(const muon_logits* l) {
+  LossParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.logits = l->logits; p.ld = l->ld;
+  p.dlogits = l->dlogits; p.ld_d = l->ld_d;
+  p.rows = l->rows;
+  p.vocab = static_cast<int32_t>(l->vocab);
+  p.inv_temperature = 1.0f / l->temperature;
+  p.weights = l->weights; p.grad_rows = l->grad_rows;
+  p.loss = l->loss; p.lse = l->lse; p.lse_given = l->lse_given;
+  return p;
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+int muon_ffn_workspace_size(muon_ctx* ctx, const muon_ffn* f, const muon_ffn_grads* g, size_t* workspace,
+                            size_t* saved) {
+  try {
+    if (!ctx || (!workspace && !saved)) return MUON_ERR_ARG;
+    int rc = validate(f, false);
+    if (rc == MUON_OK && g) rc = validate(f, g, false);
+    if (rc != MUON_OK) return rc;
+    const FfnPlan p = plan_of(f, g, ctx_cus(ctx));
+    if (workspace) *workspace = p.bytes;
+    if (saved) *saved = static_cast<size_t>(2 * f->tokens * p.Hp * 4);
+    return MUON_OK;
+  } catch (...) {
+    return MUON_ERR_HIP;
+  }
+}
+
+int muon_ffn_forward(muon_ctx* ctx, const muon_ffn* f, void* y, int64_t ld_y, void* saved, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  try {
+    if (!ctx) return MUON_ERR_ARG;
+    int rc = validate(f, true);
+    if (rc != MUON_OK) return rc;
+    if (ld_y < f->dim || ld_y > kMaxLd || !aligned(y, size_of(f->dtype)) || !aligned(saved, 16)) return MUON_ERR_ARG;
+    if (f->tokens == 0) return MUON_OK;
+    if (!y) return MUON_ERR_ARG;
+    FfnPlan p = plan_of(f, nullptr, ctx_cus(ctx));
+    rc = check_workspace(workspace, workspace_bytes, p.bytes);
+    if (rc != MUON_OK) return rc;
+    if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
+    DeviceGuard dg(ctx_device(ctx));
+    if (!dg.ok) return MUON_ERR_HIP;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    const bool f32 = f->dtype == MUON_F32;
+    for (Operand* o : {&p.x, &p.wg, &p.wu, &p.wd}) MUON_HIP(settle(*o, ws, f32, st));
+    const int64_t T = f->tokens, D = f->dim, F = f->hidden;
+
+    FfnGemm q = product(p.gate, T, F, D, f->activation);
+    q.A[0] = p.x.p; q.lda = p.x.ld;
+    q.B[0] = p.wg.p; q.ldb = p.wg.ld;
+    q.B[1] = p.wu.p; q.ldb1 = p.wu.ld;
+    q.tail = static_cast<int32_t>(D % p.bk);
+    q.C[0] = ws + p.off_h;
+    q.Np = p.Hp;
+    q.gu = static_cast<float*>(saved);
+    q.gu_stride = T * p.Hp;
+    MUON_HIP(launch_ffn(FFN_STAGE_GATE, f32, p.gate.tile, q, 1, st));
+
+    q = product(p.down, T, D, F, f->activation);
+    q.A[0] = ws + p.off_h; q.lda = p.Hp;
+    q.B[0] = p.wd.p; q.ldb = p.wd.ld;
+    q.tail = static_cast<int32_t>(F % p.bk);
+    q.C[0] = y;
+    output(q, p.down, ws + p.off_part, !f32, ld_y, false);
+    MUON_HIP(launch_ffn(FFN_STAGE_DOWN, f32, p.down.tile, q, 1, st));
+    return MUON_OK;
+  } catch (...) {
+    return MUON_ERR_HIP;
+  }
+}
+
+int muon_ffn_backward(muon_ctx* ctx, const muon_ffn* f, const muon_ffn_grads* g, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  try {
+    if (!ctx || !g) return MUON_ERR_ARG;
+    int rc = validate(f, true);
+    if (rc == MUON_OK) rc = validate(f, g, true);
+    if (rc != MUON_OK) return rc;
+    FfnPlan p = plan_of(f, g, ctx_cus(ctx));
+    rc = f->tokens > 0 ? check_workspace(workspace, workspace_bytes, p.bytes) : MUON_OK;
+    if (rc != MUON_OK) return rc;
+    if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
+    DeviceGuard dg(ctx_device(ctx));
+    if (!dg.ok) return MUON_ERR_HIP;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool f32 = f->dtype == MUON_F32, gb = g->g_dtype == MUON_BF16;
+    const int64_t T = f->tokens, D = f->dim, F = f->hidden;
+    if (T == 0) {  // no tokens: the weight gradients are zero, or stay as they are
+      if (g->accumulate) return MUON_OK;
+      if (g->g_gate) MUON_HIP(launch_ffn_zero(g->g_gate, g->ld_g_gate, F, D, gb, st));
+      if (g->g_up) MUON_HIP(launch_ffn_zero(g->g_up, g->ld_g_up, F, D, gb, st));
+      if (g->g_down) MUON_HIP(launch_ffn_zero(g->g_down, g->ld_g_down, D, F, gb, st));
+      return MUON_OK;
+    }
+    char* ws = static_cast<char*>(workspace);
+    for (Operand* o : {&p.x, &p.wg, &p.wu, &p.wd, &p.dy}) MUON_HIP(settle(*o, ws, f32, st));
+    char *h = ws + p.off_h, *dgp = ws + p.off_dg, *dup = ws + p.off_du, *part = ws + p.off_part;
+
+    FfnGemm q = product(p.dgate, T, F, D, f->activation);
+    q.A[0] = p.dy.p; q.lda = p.dy.ld;
+    q.B[0] = p.wd.p; q.ldb = p.wd.ld;
+    q.tail = static_cast<int32_t>(D % p.bk);
+    q.C[0] = dgp; q.C[1] = dup; q.C[2] = h;
+    q.Np = p.Hp;
+    q.gu = const_cast<float*>(static_cast<const float*>(g->saved));
+    q.gu_stride = T * p.Hp;
+    MUON_HIP(launch_ffn(FFN_STAGE_DGATE, f32, p.dgate.tile, q, 1, st));
+
+    if (g->dx) {
+      q = product(p.dx, T, D, F, f->activation);
+      q.slices0 = static_cast<int32_t>(p.Hp / p.bk);
+      q.A[0] = dgp; q.A[1] = dup; q.lda = p.Hp; q.KA = p.Hp;
+      q.B[0] = p.wg.p; q.ldb = p.wg.ld;
+      q.B[1] = p.wu.p; q.ldb1 = p.wu.ld;
+      q.C[0] = g->dx;
+      output(q, p.dx, part, !f32, g->ld_dx, false);
+      MUON_HIP(launch_ffn(FFN_STAGE_DX, f32, p.dx.tile, q, 1, st));
+    }
+    if (g->g_gate || g->g_up) {
+      // both in one launch where they share a row stride, else one after the other
+      const bool both = g->g_gate && g->g_up;
+      const bool one_launch = both && g->ld_g_gate == g->ld_g_up;
+      for (int i = 0; i < 2; ++i) {
+        void* out = i ? g->g_up : g->g_gate;
+        if (!out || (one_launch && i)) continue;
+        q = product(p.dgu, F, D, T, f->activation);
+        q.A[0] = i ? dup : dgp; q.A[1] = dup; q.lda = p.Hp;
+        q.B[0] = p.x.p; q.ldb = p.x.ld;
+        q.C[0] = out;
+        q.C[1] = one_launch ? g->g_up : nullptr;
+        q.batched = one_launch;
+        output(q, p.dgu, part, gb, i ? g->ld_g_up : g->ld_g_gate, g->accumulate);
+        MUON_HIP(launch_ffn(FFN_STAGE_DW, f32, p.dgu.tile, q, one_launch ? 2 : 1, st));
+      }
+    }
+    if (g->g_down) {
+      q = product(p.dwd, D, F, T, f->activation);
+      q.A[0] = p.dy.p; q.lda = p.dy.ld;
+      q.B[0] = h; q.ldb = p.Hp;
+      q.C[0] = g->g_down;
+      output(q, p.dwd, part, gb, g->ld_g_down, g->accumulate);
+      MUON_HIP(launch_ffn(FFN_STAGE_DW, f32, p.dwd.tile, q, 1, st));
+    }
+    return MUON_OK;
+  } catch (...) {
+    return MUON_ERR_HIP;
+  }
+}
+
+int muon_policy_loss(muon_ctx* ctx, const muon_logits* l, const muon_policy* t, void* stream) {
+  try {
+    if (!ctx || !t) return MUON_ERR_ARG;
+    const int rc = validate(l);
+    if (rc != MUON_OK) return rc;
+    if (!std::isfinite(t->clip_low) || !std::isfinite(t->clip_high) || !std::isfinite(t->kl_coef) ||
+        t->clip_low < 0.0f || t->clip_high < 0.0f || t->clip_low > 1.0f)
+      return MUON_ERR_ARG;
+    if (t->kl_coef != 0.0f && l->rows > 0 && !t->ref_logp) return MUON_ERR_ARG;
+    if (l->rows > 0 && (!t->targets || !t->old_logp || !t->advantages)) return MUON_ERR_ARG;
+    if (l->rows == 0) return MUON_OK;
+    if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
+    DeviceGuard dg(ctx_device(ctx));
+    if (!dg.ok) return MUON_ERR_HIP;
+    LossParams p = params(l);
+    p.targets = t->targets;
+    p.old_logp = t->old_logp; p.advantages = t->advantages;
+    p.ref_logp = t->kl_coef != 0.0f ? t->ref_logp : nullptr;
+    p.clip_low = t->clip_low; p.clip_high = t->clip_high; p.kl_coef = t->kl_coef;
+    p.logp = t->logp;
+    MUON_HIP(launch_loss(LOSS_POLICY, l->dtype == MUON_BF16, p, static_cast<hipStream_t>(stream)));
+    return MUON_OK;
+  } catch (...) {
+    return MUON_ERR_HIP;
+  }
+}
+
+int muon_distill_loss(muon_ctx* ctx, const muon_logits* l, const muon_distill* t, void* stream) {
+  try {
+    if (!ctx || !t) return MUON_ERR_ARG;
+    const int rc = validate(l);
+    if (rc != MUON_OK) return rc;
+    if (t->top < 1 || t->top > MUON_MAX_TOP || t->ld_top < t->top || t->ld_ids < t->top) return MUON_ERR_ARG;
+    if (!dtype_ok(t->top_dtype) || (t->id_dtype != MUON_I32 && t->id_dtype != MUON_I64)) return MUON_ERR_ARG;
+    if (l->rows > 0 && (!t->top_logits || !t->top_ids)) return MUON_ERR_ARG;
+    if (l->rows == 0) return MUON_OK;
+    if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
+    DeviceGuard dg(ctx_device(ctx));
+    if (!dg.ok) return MUON_ERR_HIP;
+    LossParams p = params(l);
+    p.top_logits = t->top_logits; p.ld_top = t->ld_top;
+    p.ids = t->top_ids; p.ld_ids = t->ld_ids;
+    p.top_lse = t->top_lse;
+    p.top = t->top; p.top_bf16 = t->top_dtype == MUON_BF16; p.ids64 = t->id_dtype == MUON_I64;
+    MUON_HIP(launch_loss(LOSS_DISTILL, l->dtype == MUON_BF16, p, static_cast<hipStream_t>(stream)));
+    return MUON_OK;
+  } catch (...) {
+    return MUON_ERR_HIP;
+  }
+}
+
+}  // extern "C"

@@ -1,0 +1,324 @@
+"""The vocabulary losses (muon_policy_loss, muon_distill_loss) against the float64 oracle,
+element by element, within the errors the oracle derives for fp32 arithmetic and the
+gradient's one rounding."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+from oracle import losses as ol  # noqa: E402
+from tests.gpu_util import TORCH_DT, to_np  # noqa: E402
+
+HALF_STEP = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def S():
+    from matrix_orthogonalising_optimizer_muon_amd import losses
+    return losses
+
+
+def cuda(a, dtype=torch.float32):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda().to(dtype)
+
+
+def inside(got, ref, bound, what):
+    err = np.abs(to_np(got) - ref)
+    bad = ~(err <= bound)
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:3].tolist(), to_np(got)[bad][:3], ref[bad][:3], bound[bad][:3])
+
+
+def policy_inputs(n, V, dtype, seed=0, scale=2.5):
+    rng = np.random.default_rng([seed, n, V])
+    z = cuda(scale * rng.standard_normal((n, V)), TORCH_DT[dtype])
+    t = rng.integers(0, V, n)
+    zz = to_np(z)
+    lp = np.array([zz[r, t[r]] - zz[r].max() - np.log(np.exp(zz[r] - zz[r].max()).sum()) for r in range(n)])
+    # ratios on both sides of the clip range, none within 1e-2 of a border
+    d = rng.choice([-0.5, -0.1, 0.0, 0.1, 0.5], n) + 0.03 * rng.uniform(-1, 1, n)
+    return z, cuda(t, torch.int64), cuda(lp - d), cuda(rng.standard_normal(n)), cuda(lp + 0.3 * rng.standard_normal(n))
+
+
+def check_policy(S, ins, dtype, weights=None, temperature=1.0, kl=0.1, grad_rows=None, in_place=False):
+    z, t, old, adv, ref = ins
+    kw = dict(clip_low=0.2, clip_high=0.28, kl_coef=kl, temperature=temperature)
+    want = ol.policy(to_np(z), t.cpu().numpy(), to_np(old), to_np(adv), to_np(ref), None if weights is None else to_np(weights),
+                     **kw, half_step=HALF_STEP[dtype])
+    # log ratios: the oracle's clip branch must not hang on the kernel's rounding
+    d = (want["logp"] - to_np(old))[want["err_logp"] > 0]
+    assert all(np.abs(np.exp(d) - b).min() > 1e-3 for b in (0.8, 1.28))
+    z_in = z.clone() if in_place else z
+    loss, logp, grad = S.policy_loss(z_in, t, old, adv, ref_logp=ref if kl else None, weights=weights,
+                                     out=z_in if in_place else None, **kw)
+    inside(loss, want["loss"], want["err_loss"], "loss")
+    inside(logp, want["logp"], want["err_logp"], "logp")
+    inside(grad, want["grad"], want["err_grad"], "grad")
+    # automatic differentiation: the backward from the kept normaliser
+    up = torch.linspace(-1.0, 2.0, z.shape[0], device="cuda")
+    want = ol.policy(to_np(z), t.cpu().numpy(), to_np(old), to_np(adv), to_np(ref), None if weights is None else to_np(weights),
+                     to_np(up), **kw, half_step=HALF_STEP[dtype], lse_given=True)
+    leaf = z.detach().requires_grad_(True)
+    loss2, logp2 = S.policy_loss_rows(leaf, t, old, adv, ref_logp=ref if kl else None, weights=weights, **kw)
+    assert torch.equal(loss2, loss) and torch.equal(logp2, logp)
+    inside(torch.autograd.grad((loss2 * up).sum(), leaf)[0], want["grad"], want["err_grad"], "autograd")
+    return loss, logp, grad
+
+
+VOCABS = [1, 2, 7, 8, 9, 63, 255, 1000, 1024, 2049, 4097, 16384, 16391]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", VOCABS)
+def test_policy_parity(S, V, dtype):
+    check_policy(S, policy_inputs(9, V, dtype), dtype, temperature=0.7)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [32003, 65536, 77825, 152064, 155649, 262147])
+def test_policy_parity_large_vocabulary(S, V, dtype):
+    check_policy(S, policy_inputs(3, V, dtype), dtype, weights=cuda([0.5, 0.0, 2.0]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_policy_rows_that_take_no_part(S, dtype):
+    """Weight 0 or no target: NaN and infinities there are not read; everything is written."""
+    ins = list(policy_inputs(8, 515, dtype))
+    w = cuda([1.0, 0.0, 0.25, 0.0, 1.0, 1.0, 1.0, 1.0])
+    ins[0][1], ins[0][3] = float("nan"), float("inf")
+    ins[1][5], ins[1][6] = -100, 515
+    ins[0][5:7] = float("nan")
+    ins[2][1] = float("nan")
+    check_policy(S, ins, dtype, weights=w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [100, 20000, 152064])
+def test_policy_in_place(S, V, dtype):
+    check_policy(S, policy_inputs(4, V, dtype), dtype, in_place=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("off,extra", [(0, 1), (1, 0), (8, 24), (3, 5)])
+def test_policy_strided(S, dtype, off, extra):
+    """Logits and gradient inside wider buffers: NaN around them is neither read nor overwritten."""
+    V = 1003
+    ins = list(policy_inputs(6, V, dtype))
+    plain = check_policy(S, ins, dtype)
+    wide = torch.full((8, off + V + extra), float("nan"), dtype=ins[0].dtype, device="cuda")
+    wide[1:-1, off:off + V] = ins[0]
+    ins[0] = wide[1:-1, off:off + V]
+    out = torch.full((8, off + V + extra), float("nan"), dtype=ins[0].dtype, device="cuda")
+    view = out[1:-1, off:off + V]
+    got = S.policy_loss(ins[0], *ins[1:4], ref_logp=ins[4], clip_low=0.2, clip_high=0.28, kl_coef=0.1, out=view)
+    for a, b in zip(got, plain):
+        assert torch.equal(a, b)
+    frame = torch.isnan(out)
+    frame[1:-1, off:off + V] = True
+    assert bool(frame.all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_policy_masked_columns(S, dtype):
+    """Columns masked with -inf or the type's lowest value take no probability and no gradient;
+    a row of nothing but the lowest value is uniform; one of -inf is NaN."""
+    V = 700
+    ins = list(policy_inputs(4, V, dtype))
+    lowest = torch.finfo(TORCH_DT[dtype]).min
+    t = ins[1]
+    z = ins[0]
+    mask = torch.rand(4, V, device="cuda", generator=torch.Generator("cuda").manual_seed(1)) < 0.5
+    mask[torch.arange(4), t] = False
+    z[0][mask[0]] = float("-inf")
+    z[1][mask[1]] = lowest
+    z[2] = lowest
+    z[3] = float("-inf")
+    zz = to_np(z)[:3]
+    lp = np.array([zz[r, int(t[r])] - zz[r].max() - np.log(np.exp(zz[r] - zz[r].max()).sum()) for r in range(3)])
+    ins[2][:3] = cuda(lp - 0.05)
+    loss, logp, grad = S.policy_loss(z, t, ins[2], ins[3], clip_low=0.2, clip_high=0.28)
+    want = ol.policy(zz, t.cpu().numpy()[:3], to_np(ins[2])[:3], to_np(ins[3])[:3], clip_low=0.2, clip_high=0.28, kl_coef=0.0,
+                     temperature=1.0, half_step=HALF_STEP[dtype])
+    # the lowest value in the log-probability cancels exactly: only its differences count
+    bound = want["err_logp"]
+    bound[2] = ol.U * 100
+    inside(logp[:3], want["logp"], bound, "logp")
+    for r in (0, 1):
+        inside(grad[r], want["grad"][r], want["err_grad"][r], "grad")
+        assert bool((grad[r][mask[r]] == 0).all())
+    assert np.allclose(to_np(grad[2]), want["grad"][2], rtol=2 * HALF_STEP[dtype] + 1e-5, atol=0)
+    assert bool(torch.isnan(loss[3])) and bool(torch.isnan(grad[3]).all())
+
+
+def test_policy_wild_values(S):
+    """NaN and +inf logits make their row NaN and leave the others alone."""
+    ins = list(policy_inputs(5, 999, "f32"))
+    base = S.policy_loss(*ins[:4])
+    ins[0] = ins[0].clone()
+    ins[0][1, 998] = float("nan")
+    ins[0][3, 4] = float("inf")
+    got = S.policy_loss(*ins[:4])
+    for a, b in zip(base, got):
+        assert torch.equal(a[[0, 2, 4]], b[[0, 2, 4]])
+        assert bool(torch.isnan(b[[1, 3]]).all())
+
+
+def test_policy_at_the_clip_border(S):
+    """rho A equal to the clipped product takes the gradient: with rho = 1 and no clip range."""
+    z = torch.zeros(4, 8, device="cuda")
+    t = torch.zeros(4, dtype=torch.int64, device="cuda")
+    old = torch.full((4,), float(-np.log(8.0)), device="cuda")
+    adv = cuda([1.0, -1.0, 0.0, 2.0])
+    loss, logp, grad = S.policy_loss(z, t, old, adv, clip_low=0.0, clip_high=0.0)
+    rho = torch.exp(logp - old)
+    kept = rho * adv <= rho.clamp(1.0, 1.0) * adv
+    hot = torch.zeros(8, device="cuda")
+    hot[0] = 1.0
+    want = torch.where(kept, -rho * adv, torch.zeros_like(adv))[:, None] * (hot - 0.125)
+    assert torch.allclose(grad, want, rtol=1e-5, atol=1e-6)
+
+
+def distill_inputs(n, V, K, dtype, seed=0, top_dtype=torch.float32, id_dtype=torch.int64):
+    rng = np.random.default_rng([seed, n, V, K])
+    z = cuda(2.5 * rng.standard_normal((n, V)), TORCH_DT[dtype])
+    ids = np.stack([rng.permutation(V)[:K] if K <= V else rng.integers(0, V, K) for _ in range(n)])
+    return z, cuda(2.0 * rng.standard_normal((n, K)) + 5.0, top_dtype), cuda(ids, id_dtype)
+
+
+def check_distill(S, ins, dtype, top_lse=None, weights=None, temperature=1.0, in_place=False):
+    z, top, ids = ins
+    opt = lambda t: None if t is None else to_np(t)  # noqa: E731
+    run = lambda **kw: ol.distill(to_np(z), to_np(top), ids.cpu().numpy(), opt(top_lse), opt(weights),  # noqa: E731
+                                  temperature=temperature, half_step=HALF_STEP[dtype], **kw)
+    want = run()
+    z_in = z.clone() if in_place else z
+    loss, grad = S.distill_loss(z_in, top, ids, top_lse=top_lse, weights=weights, temperature=temperature,
+                                out=z_in if in_place else None)
+    inside(loss, want["loss"], want["err_loss"], "loss")
+    inside(grad, want["grad"], want["err_grad"], "grad")
+    up = torch.linspace(-1.0, 2.0, z.shape[0], device="cuda")
+    want = run(grad_rows=to_np(up), lse_given=True)
+    leaf = z.detach().requires_grad_(True)
+    loss2 = S.distill_loss_rows(leaf, top, ids, top_lse=top_lse, weights=weights, temperature=temperature)
+    assert torch.equal(loss2, loss)
+    inside(torch.autograd.grad((loss2 * up).sum(), leaf)[0], want["grad"], want["err_grad"], "autograd")
+    return loss, grad
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,K", [(1, 1), (5, 5), (9, 3), (1000, 1), (1003, 64), (4099, 300), (16391, 64), (2000, 1024)])
+def test_distill_parity(S, V, K, dtype):
+    check_distill(S, distill_inputs(7, V, K, dtype), dtype, temperature=2.0)
+
+
+@pytest.mark.parametrize("V", [32003, 152064, 155655])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distill_parity_large_vocabulary(S, V, dtype):
+    ins = distill_inputs(3, V, 100, dtype, top_dtype=torch.bfloat16, id_dtype=torch.int32)
+    lse = cuda([9.0, 10.0, 11.0])
+    check_distill(S, ins, dtype, top_lse=lse, weights=cuda([1.0, 0.0, 0.5]), in_place=True)
+
+
+@pytest.mark.parametrize("id_dtype", [torch.int64, torch.int32])
+def test_distill_absent_and_repeated_entries(S, id_dtype):
+    """Ids outside the vocabulary, teacher logits of -inf, one column named several times, a row
+    that keeps nothing."""
+    V, K = 300, 40
+    ins = distill_inputs(6, V, K, "f32", id_dtype=id_dtype)
+    ins[2][0, 5:20] = -1
+    ins[2][1, 3] = V
+    ins[2][2, :] = 17
+    ins[2][3, 1::2] = ins[2][3, ::2]
+    ins[2][4, :] = -7
+    ins[1][5, :30] = float("-inf")
+    ins[1][4, 0] = float("nan")   # absent by its id: its logit does not count
+    want_none = check_distill(S, (ins[0], torch.nan_to_num(ins[1], nan=0.0, neginf=float("-inf")), ins[2]), "f32")
+    got = S.distill_loss(*ins)
+    assert torch.equal(got[0], want_none[0]) and torch.equal(got[1], want_none[1])
+    assert float(got[0][4]) == 0.0 and bool((got[1][4] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distill_rows_that_take_no_part(S, dtype):
+    ins = distill_inputs(5, 2051, 9, dtype)
+    ins[0][2] = float("nan")
+    ins[1][2] = float("nan")
+    w = cuda([1.0, 1.0, 0.0, 3.0, 0.0])
+    z, top = ins[0].clone(), ins[1].clone()
+    z[2], top[2] = 0.0, 0.0
+    a = check_distill(S, (z, top, ins[2]), dtype, weights=w)
+    b = S.distill_loss(*ins, weights=w)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_losses_offsets_past_32_bits(S):
+    """Rows a wide stride apart: element offsets past 2^32."""
+    n, V, ld = 4200, 130, 1 << 20   # 8.8 GB of buffer
+    z, t, old, adv, ref = policy_inputs(n, V, "bf16")
+    wide = torch.empty(n, ld, dtype=torch.bfloat16, device="cuda")
+    wide[:, :V] = z
+    a = S.policy_loss(z, t, old, adv)
+    b = S.policy_loss(wide[:, :V], t, old, adv, out=wide[:, :V])
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    want = ol.policy(to_np(z[-3:]), t.cpu().numpy()[-3:], to_np(old)[-3:], to_np(adv)[-3:], clip_low=0.2, clip_high=0.2,
+                     kl_coef=0.0, temperature=1.0, half_step=2.0 ** -8)
+    inside(b[2][-3:], want["grad"], want["err_grad"], "grad")
+
+
+def test_losses_evaluation_only_and_leading_dimensions(S):
+    z, t, old, adv, _ = policy_inputs(12, 333, "bf16")
+    loss, logp, grad = S.policy_loss(z, t, old, adv)
+    l3, p3, none = S.policy_loss(z.view(3, 4, 333), t.view(3, 4), old.view(3, 4), adv.view(3, 4), grad=False)
+    assert none is None and l3.shape == (3, 4) and torch.equal(l3.flatten(), loss) and torch.equal(p3.flatten(), logp)
+    _, _, g3 = S.policy_loss(z.view(3, 4, 333), t.view(3, 4), old.view(3, 4), adv.view(3, 4))
+    assert torch.equal(g3.view(12, 333), grad)
+    empty = S.policy_loss(z[:0], t[:0], old[:0], adv[:0])
+    assert empty[0].shape == (0,) and empty[2].shape == (0, 333)
+
+
+def test_losses_graph_and_stream(S):
+    """Captured and replayed with other eager work between the replays, and on a side stream."""
+    z, t, old, adv, _ = policy_inputs(40, 5003, "bf16")
+    zd, top, ids = distill_inputs(40, 5003, 16, "bf16")
+    hold, hold_d = z.clone(), zd.clone()
+
+    def step():
+        return (*S.policy_loss(hold, t, old, adv), *S.distill_loss(hold_d, top, ids, temperature=2.0))
+    eager = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(eager, got))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = step()
+    for k in range(4):
+        hold.copy_(z.roll(k, 0))
+        hold_d.copy_(zd.roll(k, 1))
+        g.replay()
+        torch.randn(1 << 20, device="cuda").mul_(2.0)
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, held)), k
+
+
+def test_losses_refusals(S):
+    z, t, old, adv, ref = policy_inputs(4, 64, "bf16")
+    bad = [dict(targets=t.int()), dict(targets=t[:3]), dict(old_logp=old.double()), dict(advantages=adv.cpu()),
+           dict(weights=torch.ones(3, device="cuda")), dict(kl_coef=0.1), dict(temperature=0.0), dict(clip_low=-1.0),
+           dict(out=torch.empty(4, 64, device="cuda")), dict(out=torch.empty(4, 63, dtype=torch.bfloat16, device="cuda")),
+           dict(logits=z.T.contiguous().T)]
+    for kw in bad:
+        args = dict(dict(logits=z, targets=t, old_logp=old, advantages=adv), **kw)
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            S.policy_loss(**args)
+    z, top, ids = distill_inputs(4, 64, 8, "bf16")
+    bad = [dict(top_ids=ids.float()), dict(top_ids=ids[:, :7]), dict(top_logits=top[:3]), dict(top_logits=top.double()),
+           dict(top_lse=torch.ones(3, device="cuda")), dict(top_logits=torch.zeros(4, 1025, device="cuda"))]
+    for kw in bad:
+        args = dict(dict(logits=z, top_logits=top, top_ids=ids), **kw)
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            S.distill_loss(**args)
