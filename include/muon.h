@@ -399,7 +399,7 @@ typedef struct muon_ffn_grads {
 
 /* Bytes of workspace (256-byte aligned) muon_ffn_forward (g null) or muon_ffn_backward (g
  * given) needs, and bytes of the `saved` buffer (16-byte aligned) a forward for training
- * fills: 8 per token and hidden column, hidden rounded up to 64. Either output pointer may be
+ * fills: 8 per token and hidden column, tokens rounded up to 32 and hidden to 64. Either output pointer may be
  * null. Depends on the sizes, strides, dtype and the alignment of the array pointers (null:
  * aligned) and on which gradients are wanted. */
 int muon_ffn_workspace_size(muon_ctx *ctx, const muon_ffn *f, const muon_ffn_grads *g, size_t *workspace,

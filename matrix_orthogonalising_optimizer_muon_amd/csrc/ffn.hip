@@ -7,9 +7,10 @@
 // One product kernel serves every line: out(m, n) = sum_k A(m, k) B(n, k), fp32
 // accumulators, with either operand stored K-contiguous (rows of k) or K-strided (rows of
 // m or n), so that no operand is ever transposed in memory:
-//   gate    A = x,         B = Wg and Wu     both K-contiguous; 32 columns of g and the same
-//                                             32 of u alternate, so one wave holds both and
-//                                             its epilogue writes h (and g, u for training)
+//   gate    A = x,         B = Wg and Wu     both K-contiguous; 8 rows of Wg and the same 8
+//                                             of Wu alternate in a tile, so one lane holds g
+//                                             and u of an element and the epilogue writes h
+//                                             (and g, u for training)
 //   down    A = h,         B = Wd            both K-contiguous
 //   dgate   A = dy,        B = Wd            B K-strided; epilogue reads g and u, writes dg,
 //                                             du and h
@@ -24,6 +25,7 @@
 // operand's last row return zero (buffer bounds); a K tail of a K-contiguous operand is
 // cleared in LDS before the last slice is used.
 #include <type_traits>
+#include <utility>
 
 #include "internal.hpp"
 #include "mfma_util.hpp"
@@ -74,38 +76,74 @@ __device__ __forceinline__ void mma(f32x16& acc, const u32x4& a, const u32x4& b)
   }
 }
 
-// 4 consecutive elements at p, 16-bit or 32-bit; vec: p is aligned to 4 elements.
+// 16 bytes at element alignment (one instruction at any address).
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+
+// Row m of one 32 x 32 block leaves in pieces of 8 columns. A lane holds columns
+// 8 q + 4 (l / 32) .. + 3 for q = 0..3 of row l % 32. fp32: 16 bytes per q. bf16: lanes l
+// and l + 32 swap halves, after which the lower one holds columns 8 q .. + 7 of an even q
+// and the upper one of the odd q next to it: 16 bytes each.
+// n: columns from the block's first to the matrix' last (more than 32: whole block).
+// add: the values are added to what is there.
 template <int KIND>
-__device__ __forceinline__ void put4(void* base, int64_t at, const float (&v)[4], int n, bool vec) {
+__device__ __forceinline__ void store_block(void* row, const float (&v)[16], int n, int half, bool add) {
   if constexpr (KIND == KIND_F32) {
-    float* p = static_cast<float*>(base) + at;
-    if (vec && n >= 4) {
-      *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    } else {
+    float* p = static_cast<float*>(row) + half * 4;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < n) p[e] = v[e];
+    for (int q = 0; q < 4; ++q) {
+      const int left = n - q * 8 - half * 4;
+      if (left >= 4) {
+        f32x4 w{v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]};
+        if (add) w += __builtin_bit_cast(f32x4, static_cast<u32x4>(*reinterpret_cast<u32x4_a4*>(p + q * 8)));
+        *reinterpret_cast<u32x4_a4*>(p + q * 8) = __builtin_bit_cast(u32x4, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < left) p[q * 8 + e] = (add ? p[q * 8 + e] : 0.0f) + v[q * 4 + e];
+      }
     }
   } else {
-    unsigned short* p = static_cast<unsigned short*>(base) + at;
-    if (vec && n >= 4) {
-      *reinterpret_cast<u32x2*>(p) =
-          u32x2{to_bf16(v[0]) | (static_cast<unsigned int>(to_bf16(v[1])) << 16),
-                to_bf16(v[2]) | (static_cast<unsigned int>(to_bf16(v[3])) << 16)};
-    } else {
+    unsigned short* p = static_cast<unsigned short*>(row);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < n) p[e] = to_bf16(v[e]);
+    for (int q = 0; q < 4; q += 2) {
+      float t[8];  // this lane's columns of q and q + 1, with the old values where they are added
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = v[q * 4 + e];
+      if (add) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = q * 8 + (e >> 2) * 8 + half * 4 + (e & 3);
+          if (c < n) t[e] += from_bf16(p[c]);
+        }
+      }
+      unsigned int a[2], b[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        a[e] = to_bf16(t[2 * e]) | (static_cast<unsigned int>(to_bf16(t[2 * e + 1])) << 16);
+        b[e] = to_bf16(t[4 + 2 * e]) | (static_cast<unsigned int>(to_bf16(t[5 + 2 * e])) << 16);
+      }
+      const auto r0 = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+      const auto r1 = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+      const u32x4 w{static_cast<unsigned int>(r0[0]), static_cast<unsigned int>(r1[0]),
+                    static_cast<unsigned int>(r0[1]), static_cast<unsigned int>(r1[1])};
+      const int c = (q + half) * 8;
+      if (c + 8 <= n) {
+        *reinterpret_cast<u32x4_a2*>(p + c) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < n) p[c + e] = static_cast<unsigned short>(w[e / 2] >> (16 * (e & 1)));
+      }
     }
   }
 }
-template <int KIND>
-__device__ __forceinline__ void get4(const void* base, int64_t at, float (&v)[4], int n) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if constexpr (KIND == KIND_F32) v[e] = e < n ? static_cast<const float*>(base)[at + e] : 0.0f;
-    else v[e] = e < n ? from_bf16(static_cast<const unsigned short*>(base)[at + e]) : 0.0f;
-  }
+
+// Saved g and u: fp32, in the order the lanes hold them. For 32 rows (block mb) and 8
+// columns (group f8), 64 lanes x 4 values: lane l holds row l % 32, columns 4 (l / 32) .. + 3;
+// g first, then u. Both kernels then move whole kilobytes.
+__device__ __forceinline__ int64_t saved_at(int64_t mb, int64_t Hp, int f8, int which, int lane) {
+  return ((mb * (Hp >> 3) + f8) * 2 + which) * 256 + lane * 4;
 }
 
 // Where an operand's 16-byte chunk `c` of K-strided row `k` lies in LDS (rows of R
@@ -119,45 +157,22 @@ __device__ __forceinline__ int swz_strided(int k, int c) {
   else return c ^ (((k >> 1) & 1) << 2);
 }
 
-// The loads of one operand's slice: per-lane byte offsets of this wave's instructions.
-template <int KIND, int R, int CH, int I, bool STRIDED>
-struct Loader {
-  static constexpr int ES = KIND == KIND_F32 ? 4 : 2;
-  static constexpr int VEC = 16 / ES;
-  uint32_t off[I];
-  __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int rows_left) {
-#pragma unroll
-    for (int j = 0; j < I; ++j) {
-      const int at = (wave * I + j) * 64 + lane;  // chunk position in the stage
-      if constexpr (STRIDED) {
-        constexpr int CPR = R / VEC;
-        const int k = at / CPR;
-        const int c = swz_strided<KIND, R>(k, at % CPR);
-        off[j] = static_cast<uint32_t>((k * ld + c * VEC) * ES);
-      } else {
-        const int row = at / CH;
-        const int c = (at % CH) ^ swz_bits<CH>(row);
-        off[j] = static_cast<uint32_t>((min(row, rows_left - 1) * ld + c * VEC) * ES);
-      }
-    }
-  }
-};
-
-// A buffer over `elems` elements at `base` (64-bit count, clamped to what 32-bit offsets
-// reach; the host keeps a tile's rows under 2^31 bytes), rounded up to a whole 16-byte
-// chunk: bases and rows are 16-byte aligned, so such a chunk shares its page with a valid one.
-template <int ES>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int64_t elems) {
-  int64_t bytes = (elems * ES + 15) & ~int64_t{15};
-  bytes = bytes < 0 ? 0 : (bytes > 0x7FFFFFF0 ? 0x7FFFFFF0 : bytes);
-  return make_rsrc(base, static_cast<uint32_t>(bytes));
+// f(0), f(1), ..., f(N - 1) with constants.
+template <int N, typename F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  each_of<N>(f, std::make_integer_sequence<int, N>{});
 }
 
-// KIND: element type of x, weights and outputs. BM x BN output tile, WM x WN waves, NS LDS
-// stages of CH 16-byte chunks of K. AS / BS: A / B stored K-strided.
-template <int KIND, int BM, int BN, int WM, int WN, int NS, int CH, bool AS, bool BS, int EPI>
-__global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
-  constexpr int NW = WM * WN, NT = 64 * NW;
+// KIND: element type of x, weights and outputs. BM x BN output tile, WM x WN waves per
+// k-group, KS k-groups (each takes its share of every slice's k-steps; their sums are joined
+// through LDS), NS LDS stages of CH 16-byte chunks of K. AS / BS: A / B stored K-strided.
+template <int KIND, int BM, int BN, int WM, int WN, int KS, int NS, int CH, bool AS, bool BS, int EPI>
+__global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
+  constexpr int NWC = WM * WN, NW = NWC * KS, NT = 64 * NW;
   constexpr int ES = KIND == KIND_F32 ? 4 : 2;
   constexpr int VEC = 16 / ES;
   constexpr int BK = CH * VEC;
@@ -165,16 +180,20 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
   constexpr int FM = TWM / 32, FN = TWN / 32;
   constexpr int IA = BM * CH / (64 * NW), IB = BN * CH / (64 * NW);  // loads per wave and slice
   constexpr int STAGE = (BM + BN) * CH;
-  constexpr int KL = CH / 2;                                          // MFMA k-steps per slice
+  constexpr int KL = CH / 2 / KS;                                     // a wave's k-steps per slice
   constexpr int D = NS - 1;
   constexpr bool DUAL = EPI == FFN_GATE;
   static_assert(IA * 64 * NW == BM * CH && IB * 64 * NW == BN * CH, "whole instructions");
-  static_assert(!DUAL || (!AS && !BS && FN % 2 == 0), "gate: K-contiguous, column pairs");
+  static_assert(!DUAL || (!AS && !BS && CH == 8), "gate: K-contiguous, 8 rows an instruction");
+  static_assert(KL % 2 == 0, "fragment buffers alternate in pairs");
+  static_assert(KS == 1 || BM * BN * 4 <= NS * STAGE * 16, "the joined sums fit in LDS");
   __shared__ u32x4 lds[NS * STAGE];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
+  const int half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kgrp = wave / NWC, wloc = wave % NWC;
 
   // Workgroups are dealt round-robin to the 8 XCDs: give each XCD a contiguous run of the
   // logical sequence, walked in groups of 8 tile rows, so that neighbours share panels in
@@ -199,70 +218,115 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
   const int m0 = tm * BM;
   const int n0 = DUAL ? tn * (BN / 2) : tn * BN;
 
-  // Slices of this workgroup: [kt0, kt0 + nk) of the product's nk0 (+ nk1) slices.
+  // Slices of this workgroup: [kt0, kt0 + nk) of the product's.
   const int kt0 = split * p.slices_per_split;
   const int nk = min(p.slices - kt0, p.slices_per_split);
 
-  const char* A[2];
-  const char* Bp[2];
-  A[0] = static_cast<const char*>(p.A[p.batched ? batch : 0]);
-  A[1] = static_cast<const char*>(p.A[1]);
-  Bp[0] = static_cast<const char*>(p.B[0]);
-  Bp[1] = static_cast<const char*>(p.B[1]);
-
-  Loader<KIND, BM, CH, IA, AS> la;
-  la.init(wave, lane, p.lda, p.M - m0);
-  Loader<KIND, BN, CH, IB, BS> lb;
-  if constexpr (DUAL) {
-    // rows 64 t .. 64 t + 31 of the tile come from Wg, the next 32 from Wu (same columns)
+  // Per-lane byte offsets of this wave's load instructions: instruction j fills chunk
+  // positions (wave I + j) 64 + lane of the operand's part of a stage.
+  uint32_t a_off[IA], b_off[IB];
 #pragma unroll
-    for (int j = 0; j < IB; ++j) {
-      const int at = (wave * IB + j) * 64 + lane;
+  for (int j = 0; j < IA; ++j) {
+    const int at = (wave * IA + j) * 64 + lane;
+    if constexpr (AS) {
+      const int k = at / (BM / VEC);
+      a_off[j] = static_cast<uint32_t>((k * p.lda + swz_strided<KIND, BM>(k, at % (BM / VEC)) * VEC) * ES);
+    } else {
       const int row = at / CH;
-      const int c = (at % CH) ^ swz_bits<CH>(row);
-      const int f = min((row >> 6) * 32 + (row & 31), p.N - n0 - 1);
-      lb.off[j] = static_cast<uint32_t>((f * ((row & 32) ? p.ldb1 : p.ldb) + c * VEC) * ES);
+      a_off[j] = static_cast<uint32_t>((min(row, p.M - m0 - 1) * p.lda + ((at % CH) ^ swz_bits<CH>(row)) * VEC) * ES);
     }
-  } else {
-    lb.init(wave, lane, p.ldb, p.N - n0);
+  }
+#pragma unroll
+  for (int j = 0; j < IB; ++j) {
+    const int at = (wave * IB + j) * 64 + lane;
+    if constexpr (BS) {
+      const int k = at / (BN / VEC);
+      b_off[j] = static_cast<uint32_t>((k * p.ldb + swz_strided<KIND, BN>(k, at % (BN / VEC)) * VEC) * ES);
+    } else {
+      const int row = at / CH;
+      const int c = ((at % CH) ^ swz_bits<CH>(row)) * VEC;
+      if constexpr (DUAL) {
+        // rows 16 t .. 16 t + 7 of the tile come from Wg, the next 8 from Wu (same columns of g and u)
+        const int f = min((row >> 4) * 8 + (row & 7), p.N - n0 - 1);
+        b_off[j] = static_cast<uint32_t>((f * ((row & 8) ? p.ldb1 : p.ldb) + c) * ES);
+      } else {
+        b_off[j] = static_cast<uint32_t>((min(row, p.N - n0 - 1) * p.ldb + c) * ES);
+      }
+    }
   }
 
-  auto issue = [&](int stage, int kt) {
-    kt += kt0;
-    const int seg = kt >= p.slices0 ? 1 : 0;
-    const int64_t k0 = static_cast<int64_t>(kt - (seg ? p.slices0 : 0)) * BK;
-    u32x4* sa = lds + stage * STAGE;
-    u32x4* sb = sa + BM * CH;
-    const char* ab = seg ? A[1] : A[0];
-    const char* bb = seg ? Bp[1] : Bp[0];
-    if constexpr (AS) {
-      const auto r = rsrc_of<ES>(ab + (k0 * p.lda + m0) * ES, (p.K - k0 - 1) * p.lda + p.M - m0);
+  // Where the next slice starts. K-contiguous: a byte offset along the rows of one buffer;
+  // K-strided: a pointer, and how many rows are left. Slices are loaded in order, and up to
+  // NS - 1 past the last one: those land in stages that are not read, and past an operand's
+  // end they read zeros.
+  const char* a_ptr = static_cast<const char*>(p.A[p.batched ? batch : 0]);
+  const char* b_ptr = static_cast<const char*>(p.B[0]);
+  int a_k = 0, b_k = 0;      // K-contiguous: byte offset
+  int a_rows = 0, b_rows = 0;  // K-strided: rows left
+  int seg_left = 0x7FFFFFFF;   // K-strided B in two segments: slices until the second
+  if constexpr (AS) {
+    a_ptr += (static_cast<int64_t>(kt0) * BK * p.lda + m0) * ES;
+    a_rows = p.K - kt0 * BK;
+  } else {
+    a_ptr += m0 * p.lda * ES;
+    a_k = kt0 * BK * ES;
+  }
+  if constexpr (BS) {
+    const bool second = p.B[1] != nullptr && kt0 >= p.slices0;
+    const int s = second ? kt0 - p.slices0 : kt0;
+    b_ptr = second ? static_cast<const char*>(p.B[1]) : b_ptr;
+    b_ptr += (static_cast<int64_t>(s) * BK * p.ldb + n0) * ES;
+    b_rows = p.K - s * BK;
+    if (p.B[1] != nullptr && !second) seg_left = p.slices0 - kt0;
+  } else {
+    b_ptr += n0 * p.ldb * ES;
+    b_k = kt0 * BK * ES;
+  }
+  // Buffer bounds in bytes, rounded up to whole chunks: rows are 16-byte aligned, so such a
+  // chunk shares its page with a valid element.
+  auto bytes_of = [&](int rows, int64_t ld, int last) {
+    const int b = static_cast<int>(((rows - 1) * ld + last) * ES + 15) & ~15;
+    return rows > 0 ? b : 0;
+  };
+  const int a_bytes = AS ? 0 : bytes_of(min(p.M - m0, BM), p.lda, p.KA);
+  const int b_bytes = BS ? 0 : bytes_of(min(p.N - n0, DUAL ? BN / 2 : BN), p.ldb, p.K);
+  const auto rb1 = make_rsrc(DUAL ? static_cast<const char*>(p.B[1]) + n0 * p.ldb1 * ES : b_ptr,
+                             DUAL ? bytes_of(min(p.N - n0, BN / 2), p.ldb1, p.K) : 0);
+
+  auto issue = [&](int stage) {
+    u32x4* sa = lds + stage * STAGE + wave * IA * 64;
+    u32x4* sb = lds + stage * STAGE + BM * CH + wave * IB * 64;
+    {
+      const auto r = make_rsrc(a_ptr, AS ? bytes_of(min(a_rows, BK), p.lda, p.M - m0) : a_bytes);
 #pragma unroll
-      for (int j = 0; j < IA; ++j) buf_load_lds(r, sa + (wave * IA + j) * 64, la.off[j], 0);
-    } else {
-      const auto r = rsrc_of<ES>(ab + m0 * p.lda * ES, (min(p.M - m0, BM) - 1) * p.lda + p.KA);
-#pragma unroll
-      for (int j = 0; j < IA; ++j) buf_load_lds(r, sa + (wave * IA + j) * 64, la.off[j], static_cast<int>(k0 * ES));
+      for (int j = 0; j < IA; ++j) buf_load_lds(r, sa + j * 64, a_off[j], a_k);
+      if constexpr (AS) {
+        a_ptr += static_cast<int64_t>(BK * ES) * p.lda;
+        a_rows -= BK;
+      } else {
+        a_k += BK * ES;
+      }
     }
-    if constexpr (BS) {
-      const int64_t ld = seg ? p.ldb1 : p.ldb;
-      const auto r = rsrc_of<ES>(bb + (k0 * ld + n0) * ES, (p.K - k0 - 1) * ld + p.N - n0);
-#pragma unroll
-      for (int j = 0; j < IB; ++j) buf_load_lds(r, sb + (wave * IB + j) * 64, lb.off[j], 0);
-    } else if constexpr (DUAL) {
-      const int64_t last = min(p.N - n0, BN / 2) - 1;
-      const auto r0 = rsrc_of<ES>(Bp[0] + n0 * p.ldb * ES, last * p.ldb + p.K);
-      const auto r1 = rsrc_of<ES>(Bp[1] + n0 * p.ldb1 * ES, last * p.ldb1 + p.K);
+    const auto r = make_rsrc(b_ptr, BS ? bytes_of(min(b_rows, BK), p.ldb, p.N - n0) : b_bytes);
+    if constexpr (DUAL) {
 #pragma unroll
       for (int j = 0; j < IB; ++j) {
-        const bool up = ((wave * IB + j) * 64 / CH) & 32;  // one matrix per instruction (64 / CH rows)
-        if (up) buf_load_lds(r1, sb + (wave * IB + j) * 64, lb.off[j], static_cast<int>(k0 * ES));
-        else buf_load_lds(r0, sb + (wave * IB + j) * 64, lb.off[j], static_cast<int>(k0 * ES));
+        if ((wave * IB + j) & 1) buf_load_lds(rb1, sb + j * 64, b_off[j], b_k);
+        else buf_load_lds(r, sb + j * 64, b_off[j], b_k);
       }
     } else {
-      const auto r = rsrc_of<ES>(bb + n0 * p.ldb * ES, (min(p.N - n0, BN) - 1) * p.ldb + p.K);
 #pragma unroll
-      for (int j = 0; j < IB; ++j) buf_load_lds(r, sb + (wave * IB + j) * 64, lb.off[j], static_cast<int>(k0 * ES));
+      for (int j = 0; j < IB; ++j) buf_load_lds(r, sb + j * 64, b_off[j], b_k);
+    }
+    if constexpr (BS) {
+      b_ptr += static_cast<int64_t>(BK * ES) * p.ldb;
+      b_rows -= BK;
+      if (--seg_left == 0) {
+        b_ptr = static_cast<const char*>(p.B[1]) + static_cast<int64_t>(n0) * ES;
+        b_rows = p.K;
+      }
+    } else {
+      b_k += BK * ES;
     }
   };
 
@@ -274,8 +338,8 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  const int wm0 = (wave / WN) * TWM;
-  const int wn0 = (wave % WN) * TWN;
+  const int wm0 = (wloc / WN) * TWM;
+  const int wn0 = (wloc % WN) * TWN;
 
   // Fragment of 32 rows starting at r0 (tile coordinates) and k-step kk: 16 bytes per lane,
   // lane l holding row r0 + l % 32 and k = (2 kk + l / 32) VEC .. + VEC - 1.
@@ -283,12 +347,12 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
     constexpr bool STR = decltype(strided)::value;
     constexpr int R = decltype(rows_tag)::value;
     if constexpr (!STR) {
-      return s[swz_ch<CH>(r0 + (lane & 31), 2 * kk + (lane >> 5))];
+      return s[swz_ch<CH>(r0 + (lane & 31), 2 * kk + half)];
     } else if constexpr (KIND == KIND_F32) {
       u32x4 v;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int k = 8 * kk + 4 * (lane >> 5) + e;
+        const int k = 8 * kk + 4 * half + e;
         const int col = r0 + (lane & 31);
         v[e] = reinterpret_cast<const unsigned int*>(s)[(k * (R / VEC) + swz_strided<KIND, R>(k, col >> 2)) * 4 + (col & 3)];
       }
@@ -297,7 +361,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
       u32x2 h[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int k = 16 * kk + 8 * (lane >> 5) + 4 * t + ((lane & 15) >> 2);
+        const int k = 16 * kk + 8 * half + 4 * t + ((lane & 15) >> 2);
         const int col = r0 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
         const unsigned short* q =
             reinterpret_cast<const unsigned short*>(s) + (k * (R / VEC) + swz_strided<KIND, R>(k, col >> 3)) * 8 + (col & 7);
@@ -312,6 +376,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
   using RA = std::integral_constant<int, BM>;
   using RB = std::integral_constant<int, BN>;
   u32x4 fa[2][FM], fb[2][FN];
+  const int kk0 = kgrp * KL;
   auto load_frags = [&](int buf, const u32x4* sa, int kk) {
     const u32x4* sb = sa + BM * CH;
 #pragma unroll
@@ -320,19 +385,18 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
     for (int j = 0; j < FN; ++j) fb[buf][j] = frag(sb, TB{}, RB{}, wn0 + j * 32, kk);
   };
 
-  // Ring of NS stages as in gemm.hip: slice k computes while slices k + 1 .. k + NS - 1 are
-  // in flight; past the end the last slice is loaded again into a stage that is not read.
+  // Ring of NS stages as in gemm.hip: while slice k is computed, slices k + 1 .. k + NS - 1
+  // are in flight or landed.
 #pragma unroll
-  for (int s0 = 0; s0 < D; ++s0) issue(s0, min(s0, nk - 1));
+  for (int s0 = 0; s0 < D; ++s0) issue(s0);
   wait_vmcnt<(D - 1) * (IA + IB)>();
   __builtin_amdgcn_s_barrier();
-  issue(D, min(D, nk - 1));
-  load_frags(0, lds, 0);
+  issue(D);
+  load_frags(0, lds, kk0);
 
   constexpr int RDS = KIND == KIND_F32 ? 4 : 2;                       // LDS reads of a strided fragment
   constexpr int NRD = FM * (AS ? RDS : 1) + FN * (BS ? RDS : 1);      // LDS reads per k-step
   constexpr int NMF = (KIND == KIND_F32 ? 4 : 1) * FM * FN;           // MFMAs per k-step
-  static_assert(KL % 2 == 0, "fragment buffers alternate in pairs");
   auto slice = [&](int kt, auto next_tag) {
     constexpr bool NEXT = decltype(next_tag)::value;
     const u32x4* sa = lds + (kt % NS) * STAGE;
@@ -340,7 +404,7 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
     for (int kl = 0; kl < KL; ++kl) {
       const int cur = kl & 1;
       if (kl + 1 < KL) {
-        load_frags(cur ^ 1, sa, kl + 1);
+        load_frags(cur ^ 1, sa, kk0 + kl + 1);
       } else if constexpr (NEXT) {
 #pragma unroll
         for (int kk = 0; kk + 1 < KL; ++kk) {
@@ -351,8 +415,8 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
         __builtin_amdgcn_sched_barrier(0);
         wait_vmcnt_lgkm0<(D - 1) * (IA + IB)>();
         __builtin_amdgcn_s_barrier();
-        load_frags(cur ^ 1, lds + ((kt + 1) % NS) * STAGE, 0);
-        issue(kt % NS, min(kt + NS, nk - 1));
+        load_frags(cur ^ 1, lds + ((kt + 1) % NS) * STAGE, kk0);
+        issue(kt % NS);
       }
 #pragma unroll
       for (int i = 0; i < FM; ++i)
@@ -400,131 +464,175 @@ __global__ __launch_bounds__(64 * WM * WN) void ffn_gemm(const FfnGemm p) {
         s[at] = v;
       }
       __syncthreads();
-      load_frags(0, s, 0);
+      load_frags(0, s, kk0);
     }
   }
   slice(nk - 1, std::false_type{});
   wait_vmcnt<0>();
 
+  if constexpr (KS > 1) {
+    // The k-groups' sums, added in the order of the groups.
+    float* red = reinterpret_cast<float*>(lds);
+    for (int g = KS - 1; g >= 1; --g) {
+      __syncthreads();
+      if (kgrp == g) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) red[((i * FN + j) * 16 + e) * (64 * NWC) + wloc * 64 + lane] = acc[i][j][e];
+      }
+      __syncthreads();
+      if (kgrp == g - 1) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] += red[((i * FN + j) * 16 + e) * (64 * NWC) + wloc * 64 + lane];
+      }
+    }
+    if (kgrp != 0) return;
+  }
+
   // Epilogue. Lane l of block (i, j) holds row m = 32 i + l % 32 and, for q = 0..3, the four
-  // columns n = 32 j + 8 q + 4 (l / 32) .. + 3.
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
+  // columns n = 32 j + 8 q + 4 (l / 32) .. + 3. Lanes l and l + 32 share a row, so they take
+  // the same branches.
+  each<FM>([&](auto i_tag) {  // unrolled whatever its size: the accumulators stay in registers
+    constexpr int i = decltype(i_tag)::value;
     const int m = m0 + wm0 + i * 32 + (lane & 31);
-    if (m >= p.M) continue;
+    const int64_t mb = (m0 + wm0) / 32 + i;
     if constexpr (EPI == FFN_GATE) {
+      if (mb * 32 >= p.M) return;
+      // two blocks of 16 columns each make 32 columns of h where the wave has a pair
+      constexpr int PAIR = FN % 2 == 0 ? 2 : 1;
+      each<FN / PAIR>([&](auto j_tag) {
+        constexpr int j = decltype(j_tag)::value * PAIR;
+        const int f = n0 + (wn0 + j * 32) / 2;
+        if (f >= p.Np) return;
+        float h[16];
 #pragma unroll
-      for (int j = 0; j < FN; j += 2)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int f = n0 + (wn0 + j * 32) / 2 + q * 8 + (lane >> 5) * 4;
-          if (f >= p.Np) continue;
-          float g[4], u[4], h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool in = f + e < p.N;  // columns behind N are the padding: zero
-            g[e] = in ? acc[i][j][q * 4 + e] : 0.0f;
-            u[e] = in ? acc[i][j + 1][q * 4 + e] : 0.0f;
-            float slope;
-            activation(g[e], p.act, h[e], slope);
-            h[e] *= u[e];
-          }
-          const int64_t at = static_cast<int64_t>(m) * p.Np + f;
-          put4<KIND>(p.C[0], at, h, 4, true);
-          if (p.gu != nullptr) {
-            put4<KIND_F32>(p.gu, at, g, 4, true);
-            put4<KIND_F32>(p.gu + p.gu_stride, at, u, 4, true);
-          }
-        }
-    } else if constexpr (EPI == FFN_DGATE) {
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int f = n0 + wn0 + j * 32 + q * 8 + (lane >> 5) * 4;
-          if (f >= p.Np) continue;
-          const int64_t at = static_cast<int64_t>(m) * p.Np + f;
-          float g[4], u[4], dg[4], du[4], h[4];
-          get4<KIND_F32>(p.gu, at, g, 4);
-          get4<KIND_F32>(p.gu + p.gu_stride, at, u, 4);
+        for (int t = 0; t < 2 * PAIR; ++t) {  // groups of 8 columns
+          float g[4], u[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float dh = f + e < p.N ? acc[i][j][q * 4 + e] : 0.0f;
+            // columns behind N, and the saved rows behind M, are padding: zero
+            const bool in = f + t * 8 + half * 4 + e < p.N && m < p.M;
+            g[e] = in ? acc[i][j + t / 2][(t & 1) * 8 + e] : 0.0f;
+            u[e] = in ? acc[i][j + t / 2][(t & 1) * 8 + 4 + e] : 0.0f;
             float a, slope;
             activation(g[e], p.act, a, slope);
-            du[e] = dh * a;
-            dg[e] = dh * u[e] * slope;
-            h[e] = a * u[e];
+            h[t * 4 + e] = a * u[e];
           }
-          put4<KIND>(p.C[0], at, dg, 4, true);
-          put4<KIND>(p.C[1], at, du, 4, true);
-          put4<KIND>(p.C[2], at, h, 4, true);
+          if (p.gu != nullptr) {
+            const int64_t at = saved_at(mb, p.Np, (f >> 3) + t, 0, lane);
+            *reinterpret_cast<f32x4*>(p.gu + at) = f32x4{g[0], g[1], g[2], g[3]};
+            *reinterpret_cast<f32x4*>(p.gu + at + 256) = f32x4{u[0], u[1], u[2], u[3]};
+          }
         }
-    } else {
+        if constexpr (PAIR == 1) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
+          for (int e = 8; e < 16; ++e) h[e] = 0.0f;
+        }
+        if (m < p.M)
+          store_block<KIND>(static_cast<char*>(p.C[0]) + (static_cast<int64_t>(m) * p.ldc + f) * ES, h, 16 * PAIR, half, false);
+      });
+    } else if constexpr (EPI == FFN_DGATE) {
+      if (m >= p.M) return;
+      f32x4 g[FN][4], u[FN][4];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int f = n0 + wn0 + j * 32;
+        if (f >= p.Np) continue;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int n = n0 + wn0 + j * 32 + q * 8 + (lane >> 5) * 4;
-          if (n >= p.N) continue;
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][q * 4 + e];
-          if (p.part != nullptr) {
-            put4<KIND_F32>(p.part, (static_cast<int64_t>(z) * p.M + m) * p.Np + n, v, 4, true);
-            continue;
-          }
-          const int64_t at = static_cast<int64_t>(m) * p.ldc + n;
-          if (p.c_bf16) {
-            if (p.accumulate) {
-              float o[4];
-              get4<KIND_BF16>(p.C[batch], at, o, p.N - n);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] += o[e];
-            }
-            put4<KIND_BF16>(p.C[batch], at, v, p.N - n, p.c_vec);
-          } else {
-            if (p.accumulate) {
-              float o[4];
-              get4<KIND_F32>(p.C[batch], at, o, p.N - n);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] += o[e];
-            }
-            put4<KIND_F32>(p.C[batch], at, v, p.N - n, p.c_vec);
-          }
+          const int64_t at = saved_at(mb, p.Np, (f >> 3) + q, 0, lane);
+          g[j][q] = *reinterpret_cast<const f32x4*>(p.gu + at);
+          u[j][q] = *reinterpret_cast<const f32x4*>(p.gu + at + 256);
         }
+      }
+      each<FN>([&](auto j_tag) {
+        constexpr int j = decltype(j_tag)::value;
+        const int f = n0 + wn0 + j * 32;
+        if (f >= p.Np) return;
+        float dg[16], du[16], h[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float dh = f + q * 8 + half * 4 + e < p.N ? acc[i][j][q * 4 + e] : 0.0f;
+            float a, slope;
+            activation(g[j][q][e], p.act, a, slope);
+            du[q * 4 + e] = dh * a;
+            dg[q * 4 + e] = dh * u[j][q][e] * slope;
+            h[q * 4 + e] = a * u[j][q][e];
+          }
+        const int64_t at = (static_cast<int64_t>(m) * p.ldc + f) * ES;
+        store_block<KIND>(static_cast<char*>(p.C[0]) + at, dg, 32, half, false);
+        store_block<KIND>(static_cast<char*>(p.C[1]) + at, du, 32, half, false);
+        store_block<KIND>(static_cast<char*>(p.C[2]) + (static_cast<int64_t>(m) * p.Np + f) * ES, h, 32, half, false);
+      });
+    } else {
+      if (m >= p.M) return;
+      each<FN>([&](auto j_tag) {
+        constexpr int j = decltype(j_tag)::value;
+        const int n = n0 + wn0 + j * 32;
+        if (n >= p.N) return;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e];
+        if (p.part != nullptr)
+          store_block<KIND_F32>(p.part + (static_cast<int64_t>(z) * p.M + m) * p.Np + n, v, p.N - n, half, false);
+        else if (p.c_bf16)
+          store_block<KIND_BF16>(static_cast<unsigned short*>(p.C[batch]) + static_cast<int64_t>(m) * p.ldc + n, v, p.N - n, half, p.accumulate);
+        else
+          store_block<KIND_F32>(static_cast<float*>(p.C[batch]) + static_cast<int64_t>(m) * p.ldc + n, v, p.N - n, half, p.accumulate);
+      });
     }
-  }
+  });
 }
 
 // Sum of the K splits' fp32 partial products in split order, then the store: one thread per
-// 4 columns. HBM/L2-bound: splits x 4 bytes read per element.
-__global__ __launch_bounds__(256) void ffn_join(const FfnGemm p, int64_t quads) {
-  const int per_row = (p.N + 3) / 4;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < quads; i += static_cast<int64_t>(gridDim.x) * 256) {
+// 8 columns. Bound by the reads of the partials (splits x 4 bytes per element).
+__global__ __launch_bounds__(256) void ffn_join(const FfnGemm p, int64_t pieces) {
+  const int per_row = (p.N + 7) / 8;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t row = i / per_row;      // batch * M + m
-    const int n = static_cast<int>(i - row * per_row) * 4;
+    const int n = static_cast<int>(i - row * per_row) * 8;
     const int batch = static_cast<int>(row / p.M);
     const int64_t m = row - static_cast<int64_t>(batch) * p.M;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const float* src = p.part + (static_cast<int64_t>(batch) * p.splits * p.M + m) * p.Np + n;
+    const int64_t step = static_cast<int64_t>(p.M) * p.Np;
+    f32x4 lo{0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
     for (int s = 0; s < p.splits; ++s) {
-      const f32x4 w = *reinterpret_cast<const f32x4*>(
-          p.part + ((static_cast<int64_t>(batch) * p.splits + s) * p.M + m) * p.Np + n);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += w[e];
+      lo += *reinterpret_cast<const f32x4*>(src + s * step);
+      hi += *reinterpret_cast<const f32x4*>(src + s * step + 4);
     }
-    const int64_t at = m * p.ldc + n;
-    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    const int left = p.N - n;
     if (p.c_bf16) {
-      if (p.accumulate) get4<KIND_BF16>(p.C[batch], at, o, p.N - n);
+      unsigned short* c = static_cast<unsigned short*>(p.C[batch]) + m * p.ldc + n;
+      if (p.accumulate) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += o[e];
-      put4<KIND_BF16>(p.C[batch], at, v, p.N - n, p.c_vec);
+        for (int e = 0; e < 8; ++e)
+          if (e < left) v[e] += from_bf16(c[e]);
+      }
+      if (left >= 8) {
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = to_bf16(v[2 * e]) | (static_cast<unsigned int>(to_bf16(v[2 * e + 1])) << 16);
+        *reinterpret_cast<u32x4_a2*>(c) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < left) c[e] = to_bf16(v[e]);
+      }
     } else {
-      if (p.accumulate) get4<KIND_F32>(p.C[batch], at, o, p.N - n);
+      float* c = static_cast<float*>(p.C[batch]) + m * p.ldc + n;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += o[e];
-      put4<KIND_F32>(p.C[batch], at, v, p.N - n, p.c_vec);
+      for (int e = 0; e < 8; ++e)
+        if (e < left) c[e] = (p.accumulate ? c[e] : 0.0f) + v[e];
     }
   }
 }
@@ -556,22 +664,23 @@ __global__ __launch_bounds__(256) void ffn_zero(void* out, int64_t ld, int64_t r
   }
 }
 
-template <int KIND, int BM, int BN, int WM, int WN, int NS, int CH, bool AS, bool BS, int EPI>
+template <int KIND, int BM, int BN, int WM, int WN, int KS, int NS, int CH, bool AS, bool BS, int EPI>
 hipError_t launch(const FfnGemm& p, int batches, hipStream_t st) {
   const int64_t grid = static_cast<int64_t>(p.tiles) * p.splits * batches;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((ffn_gemm<KIND, BM, BN, WM, WN, NS, CH, AS, BS, EPI>), dim3(static_cast<unsigned int>(grid)),
-                     dim3(64 * WM * WN), 0, st, p);
+  hipLaunchKernelGGL((ffn_gemm<KIND, BM, BN, WM, WN, KS, NS, CH, AS, BS, EPI>), dim3(static_cast<unsigned int>(grid)),
+                     dim3(64 * WM * WN * KS), 0, st, p);
   return hipGetLastError();
 }
 
 template <int KIND, bool AS, bool BS, int EPI>
 hipError_t launch_tile(int tile, const FfnGemm& p, int batches, hipStream_t st) {
   switch (tile) {
-    case FFN_TILE_64x128: return launch<KIND, 64, 128, 2, 2, 3, 8, AS, BS, EPI>(p, batches, st);
-    case FFN_TILE_128: return launch<KIND, 128, 128, 2, 2, 4, 8, AS, BS, EPI>(p, batches, st);
+    case FFN_TILE_64: return launch<KIND, 64, 64, 2, 2, 2, 4, 8, AS, BS, EPI>(p, batches, st);
+    case FFN_TILE_64x128: return launch<KIND, 64, 128, 2, 2, 1, 3, 8, AS, BS, EPI>(p, batches, st);
+    case FFN_TILE_128: return launch<KIND, 128, 128, 2, 2, 1, 4, 8, AS, BS, EPI>(p, batches, st);
     case FFN_TILE_256:
-      if constexpr (KIND != KIND_F32) return launch<KIND, 256, 256, 2, 4, 2, 8, AS, BS, EPI>(p, batches, st);
+      if constexpr (KIND != KIND_F32) return launch<KIND, 256, 256, 2, 4, 1, 2, 8, AS, BS, EPI>(p, batches, st);
       return hipErrorInvalidValue;
   }
   return hipErrorInvalidValue;
@@ -595,9 +704,9 @@ hipError_t launch_ffn(FfnStage stage, bool f32, int tile, const FfnGemm& p, int 
   hipError_t e = f32 ? launch_kind<KIND_F32>(stage, tile, p, batches, st)
                      : launch_kind<KIND_BF16>(stage, tile, p, batches, st);
   if (e != hipSuccess || p.part == nullptr) return e;
-  const int64_t quads = static_cast<int64_t>(batches) * p.M * ((p.N + 3) / 4);
-  const int64_t blocks = (quads + 255) / 256;
-  hipLaunchKernelGGL(ffn_join, dim3(static_cast<unsigned int>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, p, quads);
+  const int64_t pieces = static_cast<int64_t>(batches) * p.M * ((p.N + 7) / 8);
+  const int64_t blocks = (pieces + 255) / 256;
+  hipLaunchKernelGGL(ffn_join, dim3(static_cast<unsigned int>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, p, pieces);
   return hipGetLastError();
 }
 

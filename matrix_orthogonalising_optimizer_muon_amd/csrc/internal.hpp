@@ -258,14 +258,20 @@ enum FfnStage : int {
   FFN_STAGE_DX = 3,     // dx = [dg du] [Wg; Wu]; weights K-strided, two K segments
   FFN_STAGE_DW = 4,     // A^T B over the tokens; both K-strided
 };
-enum FfnTile : int { FFN_TILE_64x128 = 0, FFN_TILE_128 = 1, FFN_TILE_256 = 2, FFN_TILE_COUNT = 3 };
+enum FfnTile : int {
+  FFN_TILE_64 = 0,      // 64 x 64, two k-groups of 4 waves
+  FFN_TILE_64x128 = 1,  // 4 waves
+  FFN_TILE_128 = 2,     // 128 x 128, 4 waves
+  FFN_TILE_256 = 3,     // 256 x 256, 8 waves; not fp32
+  FFN_TILE_COUNT = 4
+};
 struct FfnGemm {
-  const void* A[2];       // operand of K segment 0 / 1, or of batch entry 0 / 1 (batched)
-  const void* B[2];       // operand of K segment 0 / 1, or Wg / Wu (FFN_GATE)
-  int64_t lda, ldb, ldb1; // row strides in elements (ldb1: of B[1]); rows 16-byte aligned
+  const void* A[2];       // operand, or (batched) operand of batch entry 0 / 1
+  const void* B[2];       // operand; B[1]: Wu (FFN_GATE), or a second K segment (K-strided B)
+  int64_t lda, ldb, ldb1; // row strides in elements (ldb1: of Wu in FFN_GATE); rows 16-byte aligned
   int32_t M, N;           // output rows and columns (FFN_GATE: columns of one of g, u)
-  int64_t K;              // valid k of a segment (rows of a K-strided operand)
-  int64_t KA;             // valid k of A's rows when A is K-contiguous (K, or its zero-padded size)
+  int32_t K;              // valid k: of a K-contiguous row, or rows of a K-strided operand (of each segment)
+  int32_t KA;             // valid k of A's rows when A is K-contiguous (K, or its zero-padded size)
   int32_t tail;           // K mod BK of the last slice's K-contiguous operands, 0: whole
   int32_t slices0;        // slices of K segment 0
   int32_t slices;         // slices of all segments
@@ -273,13 +279,12 @@ struct FfnGemm {
   int32_t tiles_m, tiles_n, tiles;
   int32_t batched;        // A and C indexed by batch entry
   void* C[3];             // FFN_STORE: outputs by batch entry; FFN_GATE: h; FFN_DGATE: dg, du, h
-  int64_t ldc;
-  int64_t Np;             // row stride of the padded intermediates (h, g, u, dg, du, partials)
-  float* gu;              // saved g, then u gu_stride elements later; null: not saved
-  int64_t gu_stride;
+  int64_t ldc;            // row stride of C (FFN_DGATE: of dg and du)
+  int64_t Np;             // row stride of h, g and u; of the partial products
+  float* gu;              // saved g and u, 32 x 8 blocks (FFN_GATE: null: not saved)
   float* part;            // fp32 partial products [batch][split][M][Np]; null: one split
   int32_t act;
-  int32_t c_bf16, c_vec, accumulate;
+  int32_t c_bf16, accumulate;
 };
 hipError_t launch_ffn(FfnStage stage, bool f32, int tile, const FfnGemm& p, int batches, hipStream_t st);
 hipError_t launch_ffn_align(const void* src, int64_t ld, void* dst, int64_t ldd, int64_t rows, int cols, bool f32,

@@ -80,11 +80,11 @@ struct Operand {
   int64_t src_ld = 0, rows = 0, cols = 0;
 };
 
-Operand operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t es, Arena& a) {
+Operand operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t es, Arena& a, bool copy = false) {
   Operand o;
   o.src = p; o.src_ld = ld; o.rows = rows; o.cols = cols;
   o.p = p; o.ld = ld;
-  if (!aligned(p, 16) || ld * es % 16 != 0) {
+  if (copy || !aligned(p, 16) || ld * es % 16 != 0) {
     o.copied = true;
     o.ld = round_up(cols, 16 / es);
     o.off = a.take(static_cast<size_t>(rows * o.ld * es));
@@ -102,12 +102,13 @@ struct Shape {
 };
 
 Shape choose(bool f32, int64_t M, int64_t cols, int64_t slices, int batches, bool may_split, int cus) {
-  static const int bm[FFN_TILE_COUNT] = {64, 128, 256}, bn[FFN_TILE_COUNT] = {128, 128, 256};
+  static const int bm[FFN_TILE_COUNT] = {64, 64, 128, 256}, bn[FFN_TILE_COUNT] = {64, 128, 128, 256};
   Shape s;
   auto tiles = [&](int t) { return cdiv(M, bm[t]) * cdiv(cols, bn[t]) * batches; };
-  s.tile = FFN_TILE_64x128;
+  s.tile = FFN_TILE_64;
   if (!f32 && tiles(FFN_TILE_256) >= cus * 3 / 4) s.tile = FFN_TILE_256;
   else if (tiles(FFN_TILE_128) >= cus * 3 / 4) s.tile = FFN_TILE_128;
+  else if (tiles(FFN_TILE_64x128) >= cus * 3 / 4) s.tile = FFN_TILE_64x128;
   s.tiles_m = cdiv(M, bm[s.tile]);
   s.tiles_n = cdiv(cols, bn[s.tile]);
   s.slices = slices;
@@ -125,12 +126,12 @@ Shape choose(bool f32, int64_t M, int64_t cols, int64_t slices, int batches, boo
 struct FfnPlan {
   int64_t es = 2, bk = 64, Hp = 0;
   Operand x, wg, wu, wd, dy;
-  size_t off_h = 0, off_dg = 0, off_du = 0, off_part = 0, bytes = 0;
+  size_t off_h = 0, off_dg = 0, off_part = 0, bytes = 0;
   Shape gate, down, dgate, dx, dgu, dwd;
 };
 
 size_t part_bytes(const Shape& s, int batches, int64_t M, int64_t N) {
-  return s.splits > 1 ? static_cast<size_t>(batches) * s.splits * M * round_up(N, 4) * 4 : 0;
+  return s.splits > 1 ? static_cast<size_t>(batches) * s.splits * M * round_up(N, 8) * 4 : 0;
 }
 
 FfnPlan plan_of(const muon_ffn* f, const muon_ffn_grads* g, int cus) {
@@ -147,18 +148,22 @@ FfnPlan plan_of(const muon_ffn* f, const muon_ffn_grads* g, int cus) {
   p.wd = operand(f->w_down, f->ld_down, D, F, p.es, a);
   p.wg = operand(f->w_gate, f->ld_gate, F, D, p.es, a);
   p.wu = operand(f->w_up, f->ld_up, F, D, p.es, a);
+  if (g && g->dx && p.wg.ld != p.wu.ld) {
+    // dx reads them as the two K segments of one operand: one row stride
+    if (!p.wg.copied) p.wg = operand(f->w_gate, f->ld_gate, F, D, p.es, a, true);
+    if (!p.wu.copied) p.wu = operand(f->w_up, f->ld_up, F, D, p.es, a, true);
+  }
   p.off_h = a.take(inter);
   size_t part = 0;
   if (!g) {
-    p.gate = choose(f32, T, 2 * F, cdiv(D, p.bk), 1, false, cus);
+    p.gate = choose(f32, T, 2 * p.Hp, cdiv(D, p.bk), 1, false, cus);  // h's padding is written too
     p.down = choose(f32, T, D, cdiv(F, p.bk), 1, true, cus);
     part = part_bytes(p.down, 1, T, D);
   } else {
     p.dy = operand(g->dy, g->ld_dy, T, D, p.es, a);
-    p.off_dg = a.take(inter);
-    p.off_du = a.take(inter);
+    p.off_dg = a.take(2 * inter);  // dg and du side by side in each row: one operand of dx
     const int n = (g->g_gate && g->g_up) ? 2 : 1;
-    p.dgate = choose(f32, T, F, cdiv(D, p.bk), 1, false, cus);
+    p.dgate = choose(f32, T, p.Hp, cdiv(D, p.bk), 1, false, cus);
     p.dx = choose(f32, T, D, 2 * (p.Hp / p.bk), 1, true, cus);
     p.dgu = choose(f32, F, D, cdiv(T, p.bk), n, true, cus);
     p.dwd = choose(f32, D, F, cdiv(T, p.bk), 1, true, cus);
@@ -182,7 +187,7 @@ FfnGemm product(const Shape& s, int64_t M, int64_t N, int64_t K, int act) {
   std::memset(&q, 0, sizeof(q));
   q.M = static_cast<int32_t>(M);
   q.N = static_cast<int32_t>(N);
-  q.K = q.KA = K;
+  q.K = q.KA = static_cast<int32_t>(K);
   q.slices0 = q.slices = static_cast<int32_t>(s.slices);
   q.slices_per_split = static_cast<int32_t>(s.per_split);
   q.splits = s.splits;
@@ -193,16 +198,14 @@ FfnGemm product(const Shape& s, int64_t M, int64_t N, int64_t K, int act) {
   return q;
 }
 
-// A plain output: type, row stride, and whether 4 elements of a row are one aligned store.
+// A plain output: type, row stride, and where the partial products of a K split go.
 void output(FfnGemm& q, const Shape& s, char* part, bool bf16, int64_t ldc, bool accumulate) {
-  const int64_t es = bf16 ? 2 : 4;
   q.c_bf16 = bf16;
   q.ldc = ldc;
   q.accumulate = accumulate;
-  q.c_vec = ldc % 4 == 0 && aligned(q.C[0], 4 * es) && (!q.C[1] || aligned(q.C[1], 4 * es));
   if (s.splits > 1) {
     q.part = reinterpret_cast<float*>(part);
-    q.Np = round_up(q.N, 4);
+    q.Np = round_up(q.N, 8);
   }
 }
 
@@ -257,7 +260,7 @@ int muon_ffn_workspace_size(muon_ctx* ctx, const muon_ffn* f, const muon_ffn_gra
     if (rc != MUON_OK) return rc;
     const FfnPlan p = plan_of(f, g, ctx_cus(ctx));
     if (workspace) *workspace = p.bytes;
-    if (saved) *saved = static_cast<size_t>(2 * f->tokens * p.Hp * 4);
+    if (saved) *saved = static_cast<size_t>(2 * round_up(f->tokens, 32) * p.Hp * 4);
     return MUON_OK;
   } catch (...) {
     return MUON_ERR_HIP;
@@ -291,9 +294,8 @@ int muon_ffn_forward(muon_ctx* ctx, const muon_ffn* f, void* y, int64_t ld_y, vo
     q.B[1] = p.wu.p; q.ldb1 = p.wu.ld;
     q.tail = static_cast<int32_t>(D % p.bk);
     q.C[0] = ws + p.off_h;
-    q.Np = p.Hp;
+    q.ldc = q.Np = p.Hp;
     q.gu = static_cast<float*>(saved);
-    q.gu_stride = T * p.Hp;
     MUON_HIP(launch_ffn(FFN_STAGE_GATE, f32, p.gate.tile, q, 1, st));
 
     q = product(p.down, T, D, F, f->activation);
@@ -334,24 +336,24 @@ int muon_ffn_backward(muon_ctx* ctx, const muon_ffn* f, const muon_ffn_grads* g,
     }
     char* ws = static_cast<char*>(workspace);
     for (Operand* o : {&p.x, &p.wg, &p.wu, &p.wd, &p.dy}) MUON_HIP(settle(*o, ws, f32, st));
-    char *h = ws + p.off_h, *dgp = ws + p.off_dg, *dup = ws + p.off_du, *part = ws + p.off_part;
+    char *h = ws + p.off_h, *dgp = ws + p.off_dg, *dup = dgp + p.Hp * p.es, *part = ws + p.off_part;
 
     FfnGemm q = product(p.dgate, T, F, D, f->activation);
     q.A[0] = p.dy.p; q.lda = p.dy.ld;
     q.B[0] = p.wd.p; q.ldb = p.wd.ld;
     q.tail = static_cast<int32_t>(D % p.bk);
     q.C[0] = dgp; q.C[1] = dup; q.C[2] = h;
+    q.ldc = 2 * p.Hp;
     q.Np = p.Hp;
     q.gu = const_cast<float*>(static_cast<const float*>(g->saved));
-    q.gu_stride = T * p.Hp;
     MUON_HIP(launch_ffn(FFN_STAGE_DGATE, f32, p.dgate.tile, q, 1, st));
 
     if (g->dx) {
       q = product(p.dx, T, D, F, f->activation);
       q.slices0 = static_cast<int32_t>(p.Hp / p.bk);
-      q.A[0] = dgp; q.A[1] = dup; q.lda = p.Hp; q.KA = p.Hp;
+      q.A[0] = dgp; q.lda = 2 * p.Hp; q.KA = static_cast<int32_t>(2 * p.Hp);
       q.B[0] = p.wg.p; q.ldb = p.wg.ld;
-      q.B[1] = p.wu.p; q.ldb1 = p.wu.ld;
+      q.B[1] = p.wu.p;
       q.C[0] = g->dx;
       output(q, p.dx, part, !f32, g->ld_dx, false);
       MUON_HIP(launch_ffn(FFN_STAGE_DX, f32, p.dx.tile, q, 1, st));
@@ -364,7 +366,7 @@ int muon_ffn_backward(muon_ctx* ctx, const muon_ffn* f, const muon_ffn_grads* g,
         void* out = i ? g->g_up : g->g_gate;
         if (!out || (one_launch && i)) continue;
         q = product(p.dgu, F, D, T, f->activation);
-        q.A[0] = i ? dup : dgp; q.A[1] = dup; q.lda = p.Hp;
+        q.A[0] = i ? dup : dgp; q.A[1] = dup; q.lda = 2 * p.Hp;
         q.B[0] = p.x.p; q.ldb = p.x.ld;
         q.C[0] = out;
         q.C[1] = one_launch ? g->g_up : nullptr;

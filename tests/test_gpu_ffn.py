@@ -119,6 +119,24 @@ def test_ffn_strided_operands(L, dtype, off, extra):
         assert bool(frame.all())
 
 
+@pytest.mark.parametrize("gate_extra,up_extra", [(0, 8), (24, 0), (8, 3), (3, 5)])
+def test_ffn_weights_of_different_strides(L, gate_extra, up_extra):
+    """w_gate and w_up with row strides of their own, and gradient buffers likewise."""
+    T, D, F = 37, 72, 140
+    ops = list(block(T, D, F, "bf16"))
+    y0, out0 = check(L, ops, "silu", "bf16")
+    for k, extra in ((1, gate_extra), (2, up_extra)):
+        wide = torch.full((F, D + extra), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:, :D] = ops[k]
+        ops[k] = wide[:, :D]
+    x, wg, wu, wd, dy = ops
+    y, saved = L.ffn_forward(x, wg, wu, wd, save=True)
+    grads = (torch.empty(F, D + up_extra, dtype=torch.bfloat16, device="cuda")[:, :D],
+             torch.empty(F, D + gate_extra, dtype=torch.bfloat16, device="cuda")[:, :D], torch.empty_like(wd))
+    got = L.ffn_backward(dy, x, wg, wu, wd, saved, grads=grads)
+    assert torch.equal(y, y0) and all(torch.equal(a, b) for a, b in zip(got, out0))
+
+
 def test_ffn_nan_stays_in_its_row(L):
     """A NaN or infinity in one token reaches that token's results and the weight gradients' columns
     only through the formulas: other rows of y and dx are what they were."""
@@ -257,7 +275,7 @@ def test_ffn_two_calls_at_once(L):
 
 
 def test_ffn_refusals(L):
-    x, wg, wu, wd, dy = block(6, 16, 24, "bf16")
+    x, wg, wu, wd, dy = block(40, 16, 24, "bf16")   # saved holds whole blocks of 32 tokens
     y, saved = L.ffn_forward(x, wg, wu, wd, save=True)
     with pytest.raises(TypeError):
         L.ffn_forward(x, wg.float(), wu, wd)

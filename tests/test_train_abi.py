@@ -78,7 +78,7 @@ def test_ffn_forward_validation(hctx):
     assert call(ffn(), y=FAKE + 1) == B.MUON_ERR_ARG
     assert call(ffn(), saved=FAKE + 8) == B.MUON_ERR_ARG
     need, saved = B.muon_ffn_workspace_size(hctx, ffn())
-    assert need >= 10 * 128 * 2 and saved == 2 * 10 * 128 * 4
+    assert need >= 10 * 128 * 2 and saved == 2 * 32 * 128 * 4
     assert call(ffn(), n=need) == B.MUON_ERR_DEVICE
     assert call(ffn(), n=need - 1) == B.MUON_ERR_WORKSPACE
     assert call(ffn(), ws=None) == B.MUON_ERR_WORKSPACE
