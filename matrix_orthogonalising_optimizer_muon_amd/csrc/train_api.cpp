@@ -92,34 +92,69 @@ Operand operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t e
   return o;
 }
 
-// Tile and K split of one product. The 256 tile carries the most products per LDS byte and
-// is taken when its tiles fill the GPU; smaller tiles, and for plain outputs a split of K
-// joined by a second kernel, keep more CUs busy otherwise.
+// Tile and K split of one product: the cheapest by a model of measured parts. A workgroup
+// takes kSliceUs per slice of K (128 bytes a row), by operand layout, tile and how many
+// share a CU; the launch is as many rounds of resident workgroups as it takes; each round
+// adds the fill of the ring and an epilogue in proportion to the tile (larger where it
+// reads g and u); a split of K (plain outputs) adds the traffic of the fp32 partials and
+// the joining launch. Measured over 845 launches of 15 problems, 64 to 16384 tokens; on
+// these the model's choice takes 1.6% more than the best of all tiles and splits (mean),
+// against 20 to 110% for the largest tile that fills the GPU (2048 tokens, 2048 x 8192: dx
+// 292 us with 128 x 128 tiles, 130 us with 256 x 256 and four splits).
 struct Shape {
   int tile = FFN_TILE_128, splits = 1;
   int64_t slices = 0, per_split = 0;
   int64_t tiles_m = 0, tiles_n = 0;
 };
 
-Shape choose(bool f32, int64_t M, int64_t cols, int64_t slices, int batches, bool may_split, int cus) {
+enum Layout { BOTH_CONTIGUOUS = 0, B_STRIDED = 1, BOTH_STRIDED = 2 };
+// [fp32][layout][tile][two workgroups a CU, one]; the two large tiles always have one.
+constexpr float kSliceUs[2][3][FFN_TILE_COUNT][2] = {
+    {{{0.443f, 0.183f}, {0.694f, 0.335f}, {0.518f, 0.518f}, {1.070f, 1.070f}},
+     {{0.443f, 0.256f}, {0.681f, 0.386f}, {0.522f, 0.522f}, {1.136f, 1.136f}},
+     {{0.526f, 0.314f}, {0.679f, 0.414f}, {0.539f, 0.539f}, {1.179f, 1.179f}}},
+    {{{1.177f, 0.568f}, {2.228f, 1.105f}, {2.058f, 2.058f}, {1e9f, 1e9f}},
+     {{1.163f, 0.643f}, {2.009f, 1.117f}, {2.031f, 2.031f}, {1e9f, 1e9f}},
+     {{1.072f, 0.570f}, {2.001f, 1.047f}, {2.058f, 2.058f}, {1e9f, 1e9f}}}};
+constexpr double kFillUs = 1.5, kEpilogueUs = 8.4, kDgateEpilogueUs = 37.0;  // per round; epilogues per 256 x 256
+constexpr double kJoinUs = 2.0, kJoinBytesPerUs = 6.5e6;
+constexpr int64_t kMaxPartBytes = int64_t{1} << 28;
+constexpr int64_t kMinSplitSlices = 4;
+
+// cols: tile columns covered (twice the output's for the gate stage); dgate: its epilogue.
+Shape choose(bool f32, Layout layout, int64_t M, int64_t cols, int64_t slices, int batches, bool may_split, bool dgate,
+             int cus) {
   static const int bm[FFN_TILE_COUNT] = {64, 64, 128, 256}, bn[FFN_TILE_COUNT] = {64, 128, 128, 256};
-  Shape s;
-  auto tiles = [&](int t) { return cdiv(M, bm[t]) * cdiv(cols, bn[t]) * batches; };
-  s.tile = FFN_TILE_64;
-  if (!f32 && tiles(FFN_TILE_256) >= cus * 3 / 4) s.tile = FFN_TILE_256;
-  else if (tiles(FFN_TILE_128) >= cus * 3 / 4) s.tile = FFN_TILE_128;
-  else if (tiles(FFN_TILE_64x128) >= cus * 3 / 4) s.tile = FFN_TILE_64x128;
-  s.tiles_m = cdiv(M, bm[s.tile]);
-  s.tiles_n = cdiv(cols, bn[s.tile]);
-  s.slices = slices;
-  if (may_split && tiles(s.tile) < cus) {
-    // at least 8 slices to a split, at most 16 splits
-    const int64_t want = std::min<int64_t>({cdiv(cus, tiles(s.tile)), slices / 8, 16});
-    s.splits = static_cast<int>(std::max<int64_t>(1, want));
+  static const int per_cu[FFN_TILE_COUNT] = {2, 2, 1, 1};
+  static const int try_splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+  Shape best;
+  double best_us = 1e300;
+  for (int t = 0; t < FFN_TILE_COUNT; ++t) {
+    if (f32 && t == FFN_TILE_256) continue;
+    const int64_t tm = cdiv(M, bm[t]), tn = cdiv(cols, bn[t]);
+    const double area = bm[t] * bn[t] / 65536.0;
+    for (const int want : try_splits) {
+      if (want > 1 && (!may_split || slices / want < kMinSplitSlices)) break;
+      const int64_t per = cdiv(slices, want), splits = cdiv(slices, per);
+      const int64_t part = splits > 1 ? batches * splits * M * cols * 4 : 0;
+      if (part > kMaxPartBytes) break;
+      const int64_t wgs = tm * tn * batches * splits;
+      const int64_t slots = static_cast<int64_t>(cus) * per_cu[t];
+      const double us = cdiv(wgs, slots) * (per * static_cast<double>(kSliceUs[f32][layout][t][wgs <= cus]) + kFillUs +
+                                            area * (dgate ? kDgateEpilogueUs : kEpilogueUs)) +
+                        (part ? kJoinUs + 2.0 * part / kJoinBytesPerUs : 0.0);
+      if (us < best_us) {
+        best_us = us;
+        best.tile = t;
+        best.splits = static_cast<int>(splits);
+        best.slices = slices;
+        best.per_split = per;
+        best.tiles_m = tm;
+        best.tiles_n = tn;
+      }
+    }
   }
-  s.per_split = cdiv(slices, s.splits);
-  s.splits = static_cast<int>(cdiv(slices, s.per_split));
-  return s;
+  return best;
 }
 
 // Everything muon_ffn_forward / muon_ffn_backward launch, from the sizes and alignments.
@@ -156,17 +191,17 @@ FfnPlan plan_of(const muon_ffn* f, const muon_ffn_grads* g, int cus) {
   p.off_h = a.take(inter);
   size_t part = 0;
   if (!g) {
-    p.gate = choose(f32, T, 2 * p.Hp, cdiv(D, p.bk), 1, false, cus);  // h's padding is written too
-    p.down = choose(f32, T, D, cdiv(F, p.bk), 1, true, cus);
+    p.gate = choose(f32, BOTH_CONTIGUOUS, T, 2 * p.Hp, cdiv(D, p.bk), 1, false, false, cus);  // h's padding is written too
+    p.down = choose(f32, BOTH_CONTIGUOUS, T, D, cdiv(F, p.bk), 1, true, false, cus);
     part = part_bytes(p.down, 1, T, D);
   } else {
     p.dy = operand(g->dy, g->ld_dy, T, D, p.es, a);
     p.off_dg = a.take(2 * inter);  // dg and du side by side in each row: one operand of dx
     const int n = (g->g_gate && g->g_up) ? 2 : 1;
-    p.dgate = choose(f32, T, p.Hp, cdiv(D, p.bk), 1, false, cus);
-    p.dx = choose(f32, T, D, 2 * (p.Hp / p.bk), 1, true, cus);
-    p.dgu = choose(f32, F, D, cdiv(T, p.bk), n, true, cus);
-    p.dwd = choose(f32, D, F, cdiv(T, p.bk), 1, true, cus);
+    p.dgate = choose(f32, B_STRIDED, T, p.Hp, cdiv(D, p.bk), 1, false, true, cus);
+    p.dx = choose(f32, B_STRIDED, T, D, 2 * (p.Hp / p.bk), 1, true, false, cus);
+    p.dgu = choose(f32, BOTH_STRIDED, F, D, cdiv(T, p.bk), n, true, false, cus);
+    p.dwd = choose(f32, BOTH_STRIDED, D, F, cdiv(T, p.bk), 1, true, false, cus);
     if (g->dx) part = std::max(part, part_bytes(p.dx, 1, T, D));
     if (g->g_gate || g->g_up) part = std::max(part, part_bytes(p.dgu, n, F, D));
     if (g->g_down) part = std::max(part, part_bytes(p.dwd, 1, D, F));
