@@ -14,6 +14,8 @@
 // exp((z - m)) over its columns (one rescale per 16-byte vector), joined in a fixed order;
 // the second writes the gradient. All of it in fp32; exp((z - m) c) is formed from the
 // difference, so that rows of the type's lowest values stay exact, and q = e / s.
+#include <type_traits>
+
 #include "internal.hpp"
 #include "mfma_util.hpp"
 
@@ -121,14 +123,16 @@ struct Shared {
   float sum[16];
 };
 
-template <typename E, int LOSS, int THREADS>
+// NV > 0: the row stays in registers between the passes, NV 16-byte vectors a thread, and is
+// read once. NV == 0: the second pass reads it again (rows too long to hold).
+template <typename E, int LOSS, int THREADS, int NV>
 __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
   using R = Row<E>;
   constexpr int VEC = R::VEC;
+  constexpr int KT = LOSS == LOSS_DISTILL ? (kMaxTop + THREADS - 1) / THREADS : 1;  // kept entries a thread takes
   __shared__ Shared sh;
-  __shared__ float tz[LOSS == LOSS_DISTILL ? kMaxTop : 1];   // the kept entries' logits
-  __shared__ float tp[LOSS == LOSS_DISTILL ? kMaxTop : 1];   // their teacher probabilities
-  __shared__ int tid_of[LOSS == LOSS_DISTILL ? kMaxTop : 1]; // their columns, -1: absent
+  __shared__ __attribute__((aligned(16))) int col[LOSS == LOSS_DISTILL ? kMaxTop : 4];   // the kept entries' columns, -1: absent
+  __shared__ float mass_of[LOSS == LOSS_DISTILL ? kMaxTop : 1];                          // and teacher probabilities
 
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x;
@@ -159,22 +163,45 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     return;
   }
 
-  // The scalars of the row that lie in the logits, before a gradient may overwrite them.
+  // The teacher's entries first, then the row: loads return in order, so the columns are
+  // known (and their logits requested) while the row is still on its way.
+  float tt[KT], tz[KT];
+  int tc[KT];
+  if constexpr (LOSS == LOSS_DISTILL) {
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      const int j = k * THREADS + tid;
+      tc[k] = -1;
+      tt[k] = -INFINITY;
+      tz[k] = 0.0f;
+      if (j < p.top) {
+        const int64_t id = p.ids64 ? static_cast<const int64_t*>(p.ids)[r * p.ld_ids + j]
+                                   : static_cast<const int32_t*>(p.ids)[r * p.ld_ids + j];
+        const int64_t at = r * p.ld_top + j;
+        const float t = p.top_bf16 ? Row<unsigned short>::from(static_cast<const unsigned short*>(p.top_logits)[at])
+                                   : static_cast<const float*>(p.top_logits)[at];
+        if (id >= 0 && id < V) {
+          tc[k] = static_cast<int>(id);
+          tt[k] = t;
+        }
+      }
+    }
+  }
+  u32x4 row[NV > 0 ? NV : 1];
+  if constexpr (NV > 0) {
+    // past the row's last vector a thread loads that one again and leaves it out below
+    if (d || !p.lse_given)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) row[i] = R::load(z + static_cast<int64_t>(min(i * THREADS + tid, full - 1)) * VEC);
+  }
+  const float zl = tail < V ? R::from(z[tail]) : 0.0f;
   float zt = 0.0f;
   if constexpr (LOSS == LOSS_POLICY) {
     zt = R::from(z[target]);
   } else {
-    for (int j = tid; j < p.top; j += THREADS) {
-      const int64_t id = p.ids64 ? static_cast<const int64_t*>(p.ids)[r * p.ld_ids + j]
-                                 : static_cast<const int32_t*>(p.ids)[r * p.ld_ids + j];
-      const bool in = id >= 0 && id < V;
-      tid_of[j] = in ? static_cast<int>(id) : -1;
-      tz[j] = in ? R::from(z[id]) : 0.0f;
-      const int64_t at = r * p.ld_top + j;
-      const float t = p.top_bf16 ? Row<unsigned short>::from(static_cast<const unsigned short*>(p.top_logits)[at])
-                                 : static_cast<const float*>(p.top_logits)[at];
-      tp[j] = in ? t : -INFINITY;
-    }
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+      if (tc[k] >= 0) tz[k] = R::from(z[tc[k]]);
   }
 
   // m and s: q_v = exp2((z_v - m) c) / s, log2 of the normaliser (m c + log2 s).
@@ -185,22 +212,40 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     inv_s = 1.0f;
   } else {
     Stat st{-INFINITY, 0.0f};
-    for (int i = tid; i < full; i += THREADS) {
-      float v[VEC];
-      R::unpack(R::load(z + static_cast<int64_t>(i) * VEC), v);
-      float mx = st.m;
+    // one rescale of the running sum per G vectors
+    constexpr int G = NV == 0 ? 1 : 16 / VEC;
+    auto take = [&](const u32x4* vec, auto n_tag, int first) {
+      constexpr int N = decltype(n_tag)::value;
+      float v[N][VEC], mx = st.m;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) mx = fmaxf(mx, v[e]);
+      for (int g = 0; g < N; ++g) {
+        R::unpack(vec[g], v[g]);
+        const bool in = NV == 0 || (first + g) * THREADS + tid < full;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          v[g][e] = in ? v[g][e] : -INFINITY;
+          mx = fmaxf(mx, v[g][e]);
+        }
+      }
       const float at = base_of(mx);
       float s = st.s * __builtin_amdgcn_exp2f((st.m - at) * c);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s += __builtin_amdgcn_exp2f((v[e] - at) * c);
+      for (int g = 0; g < N; ++g)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s += __builtin_amdgcn_exp2f((v[g][e] - at) * c);
       st = {mx, s};
+    };
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int i = 0; i + G <= NV; i += G) take(row + i, std::integral_constant<int, G>{}, i);
+      if constexpr (NV % G != 0) take(row + NV / G * G, std::integral_constant<int, NV % G>{}, NV / G * G);
+    } else {
+      for (int i = tid; i < full; i += THREADS) {
+        const u32x4 v = R::load(z + static_cast<int64_t>(i) * VEC);
+        take(&v, std::integral_constant<int, 1>{}, 0);
+      }
     }
-    if (tail < V) {
-      const float v = R::from(z[tail]);
-      st = join(st, Stat{v, v == v ? 1.0f : v}, c);
-    }
+    if (tail < V) st = join(st, Stat{zl, zl == zl ? 1.0f : zl}, c);
     st = join_all<THREADS>(st, c, sh.stat);
     m = st.m;
     log2s = __builtin_amdgcn_logf(st.s);
@@ -211,6 +256,7 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
   const float up = p.grad_rows ? p.grad_rows[r] : 1.0f;
   const float scale = w * up * p.inv_temperature;
   float coef;  // dlogits_v = coef q_v, less the kept entries' part
+  float fix[KT];
   if constexpr (LOSS == LOSS_POLICY) {
     const float lp = ((zt - m) * c - log2s) * kLn2;
     const float adv = p.advantages[r];
@@ -232,86 +278,118 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     coef = -slope * scale;
   } else {
     // Teacher: p_j = exp((t_j - tm) c - log2 of the normaliser)
-    __syncthreads();
     float tm, tlog2;
     if (p.top_lse) {
       tm = 0.0f;
       tlog2 = p.top_lse[r] * kLog2e;
     } else {
       Stat st{-INFINITY, 0.0f};
-      for (int j = tid; j < p.top; j += THREADS) st = join(st, Stat{tp[j], tp[j] == -INFINITY ? 0.0f : 1.0f}, c);
+#pragma unroll
+      for (int k = 0; k < KT; ++k) st = join(st, Stat{tt[k], tt[k] == -INFINITY ? 0.0f : 1.0f}, c);
       st = join_all<THREADS>(st, c, sh.stat);
       tm = base_of(st.m);
       tlog2 = __builtin_amdgcn_logf(st.s);
     }
-    float mass = 0.0f, loss = 0.0f;
-    for (int j = tid; j < p.top; j += THREADS) {
-      const float lpj = (tp[j] - tm) * c - tlog2;        // log2 p_j
-      const float pj = tp[j] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lpj);
-      mass += pj;
-      if (pj != 0.0f) loss += pj * (lpj - ((tz[j] - m) * c - log2s));
-      tp[j] = pj;
+    float mass = 0.0f, loss = 0.0f, pj[KT];
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      const float lpj = (tt[k] - tm) * c - tlog2;        // log2 p_j
+      pj[k] = tt[k] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lpj);
+      mass += pj[k];
+      if (pj[k] != 0.0f) loss += pj[k] * (lpj - ((tz[k] - m) * c - log2s));
+      const int j = k * THREADS + tid;
+      if (j < kMaxTop) {
+        col[j] = tc[k];
+        mass_of[j] = pj[k];
+      }
     }
     mass = sum_all<THREADS>(mass, sh.sum);
     loss = sum_all<THREADS>(loss, sh.sum);
     if (tid == 0 && p.loss) p.loss[r] = loss * kLn2 * w;
     coef = mass * scale;
+    // A column that occurs more than once: its first entry carries the sum, the others nothing.
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      fix[k] = 0.0f;
+      const int j = k * THREADS + tid;
+      if (tc[k] < 0) continue;
+      for (int o = 0; o < p.top; o += 4) {
+        const int4 others = *reinterpret_cast<const int4*>(col + o);  // entries behind the last are -1
+        const int oc[4] = {others.x, others.y, others.z, others.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (oc[e] == tc[k]) {
+            if (o + e < j) tc[k] = -1;
+            else fix[k] += mass_of[o + e];
+          }
+        if (tc[k] < 0) break;
+      }
+      fix[k] *= scale;
+    }
   }
   if (!d) return;
 
-  // In place: every thread's logits of the row's scalars are read by now.
+  // In place: every thread has read the row's scalars by now (and, with the row in
+  // registers, the row); with a second pass a thread reads a vector before it writes it.
   __syncthreads();
   const float cq = coef * inv_s;
   const float shift = p.lse_given ? log2s : 0.0f;
-  for (int i = tid; i < full; i += THREADS) {
+  auto give = [&](const u32x4& vec, int i) {
     const int64_t at = static_cast<int64_t>(i) * VEC;
     float v[VEC];
-    R::unpack(R::load(z + at), v);
+    R::unpack(vec, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] = cq * __builtin_amdgcn_exp2f((v[e] - m) * c - shift);
     if constexpr (LOSS == LOSS_POLICY) {
-      const int64_t off = target - at;
+      const int off = static_cast<int>(target) - i * VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[e] = off == e ? v[e] - coef : v[e];
     }
     R::store(d + at, v);
+  };
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (i * THREADS + tid < full) give(row[i], i * THREADS + tid);
+  } else {
+    for (int i = tid; i < full; i += THREADS) give(R::load(z + static_cast<int64_t>(i) * VEC), i);
   }
   if (tail < V) {
-    float v = cq * __builtin_amdgcn_exp2f((R::from(z[tail]) - m) * c - shift);
+    float v = cq * __builtin_amdgcn_exp2f((zl - m) * c - shift);
     if (LOSS == LOSS_POLICY && tail == target) v -= coef;
     d[tail] = R::to(v);
   }
   if constexpr (LOSS == LOSS_DISTILL) {
-    // The kept columns again, with the teacher's part; the first entry of a column that
-    // occurs more than once writes the sum. The row's stores have reached this XCD's L2
-    // before any of these is issued (a wait for them and a barrier; a device-wide fence
-    // would write the L2 back: 1685 us against 339 us for 2048 rows of 152064).
+    // The kept columns again, with the teacher's part. The row's stores have reached this
+    // XCD's L2 before any of these is issued (a wait for them and a barrier; a device-wide
+    // fence would write the L2 back: 1685 us against 339 us for 2048 rows of 152064).
     wait_vmcnt<0>();
     __syncthreads();
-    for (int j = tid; j < p.top; j += THREADS) {
-      const int id = tid_of[j];
-      if (id < 0) continue;
-      float pj = 0.0f;
-      bool first = true;
-      for (int k = 0; k < p.top; ++k) {
-        if (tid_of[k] != id) continue;
-        if (k < j) { first = false; break; }
-        pj += tp[k];
-      }
-      if (first)
-        d[id] = R::to(cq * __builtin_amdgcn_exp2f((tz[j] - m) * c - shift) - pj * scale);
-    }
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+      if (tc[k] >= 0) d[tc[k]] = R::to(cq * __builtin_amdgcn_exp2f((tz[k] - m) * c - shift) - fix[k]);
   }
 }
 
+template <typename E, int LOSS, int THREADS, int NV>
+hipError_t launch_as(const LossParams& p, hipStream_t st) {
+  hipLaunchKernelGGL((loss_kernel<E, LOSS, THREADS, NV>), dim3(static_cast<unsigned int>(p.rows)), dim3(THREADS), 0, st, p);
+  return hipGetLastError();
+}
+
+// The smallest form that holds the row; a row past the largest is read twice.
 template <typename E, int LOSS>
 hipError_t launch(const LossParams& p, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned int>(p.rows));
-  if (p.vocab <= 16384)
-    hipLaunchKernelGGL((loss_kernel<E, LOSS, 256>), grid, dim3(256), 0, st, p);
-  else
-    hipLaunchKernelGGL((loss_kernel<E, LOSS, 1024>), grid, dim3(1024), 0, st, p);
-  return hipGetLastError();
+  const int vectors = p.vocab / Row<E>::VEC;
+  if (vectors < 1) return launch_as<E, LOSS, 256, 0>(p, st);
+  if (vectors <= 256 * 4) return launch_as<E, LOSS, 256, 4>(p, st);
+  if (vectors <= 256 * 8) return launch_as<E, LOSS, 256, 8>(p, st);
+  if (vectors <= 256 * 16) return launch_as<E, LOSS, 256, 16>(p, st);
+  if (vectors <= 512 * 16) return launch_as<E, LOSS, 512, 16>(p, st);
+  if (vectors <= 1024 * 12) return launch_as<E, LOSS, 1024, 12>(p, st);
+  if (vectors <= 1024 * 16) return launch_as<E, LOSS, 1024, 16>(p, st);
+  if (vectors <= 1024 * 19) return launch_as<E, LOSS, 1024, 19>(p, st);
+  return launch_as<E, LOSS, 1024, 0>(p, st);
 }
 
 }  // namespace
