@@ -79,6 +79,7 @@ __device__ __forceinline__ void mma(f32x16& acc, const u32x4& a, const u32x4& b)
 // 16 bytes at element alignment (one instruction at any address).
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
 // Row m of one 32 x 32 block leaves in pieces of 8 columns. A lane holds columns
 // 8 q + 4 (l / 32) .. + 3 for q = 0..3 of row l % 32. fp32: 16 bytes per q. bf16: lanes l
@@ -161,7 +162,8 @@ __device__ __forceinline__ int64_t saved_at(int64_t mb, int64_t Hp, int f8, int 
 template <int KIND, int R>
 __device__ __forceinline__ int swz_strided(int k, int c) {
   constexpr int CPR = R * (KIND == KIND_F32 ? 4 : 2) / 16;
-  if constexpr (KIND == KIND_F32) return c ^ (((k >> 2) & 1) << 3);
+  if constexpr (R == 32) return c;  // four (16-bit) or two rows to 256 bytes: apart as they are
+  else if constexpr (KIND == KIND_F32) return c ^ (((k >> 2) & 1) << 3);
   else if constexpr (CPR >= 16) return c ^ ((k & 3) << 2);
   else return c ^ (((k >> 1) & 1) << 2);
 }
@@ -194,7 +196,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
   constexpr bool DUAL = EPI == FFN_GATE;
   static_assert(IA * 64 * NW == BM * CH && IB * 64 * NW == BN * CH, "whole instructions");
   static_assert(!DUAL || (!AS && !BS && CH == 8), "gate: K-contiguous, 8 rows an instruction");
-  static_assert(KL % 2 == 0, "fragment buffers alternate in pairs");
+  static_assert(KL == 1 || KL % 2 == 0, "fragment buffers alternate in pairs");
   static_assert(KS == 1 || BM * BN * 4 <= NS * STAGE * 16, "the joined sums fit in LDS");
   __shared__ u32x4 lds[NS * STAGE];
 
@@ -431,6 +433,12 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) mma<KIND>(acc[i][j], fb[cur][j], fa[cur][i]);
     }
+    if constexpr (KL == 1) {  // one k-step a slice: the next slice's fragments move up
+#pragma unroll
+      for (int i = 0; i < FM; ++i) fa[0][i] = fa[1][i];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[0][j] = fb[1][j];
+    }
     if constexpr (NEXT) {
       constexpr int NL = IA + IB;
       constexpr int NP = NL < NMF ? NL : NMF;
@@ -602,64 +610,79 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
 }
 
 // Sum of the K splits' fp32 partial products in split order, then the store: one thread per
-// 8 columns. Bound by the reads of the partials (splits x 4 bytes per element).
+// 4 columns, up to 8 partials requested at a time. Bound by the reads of the partials
+// (splits x 4 bytes per element), or by their latency when there are few.
 __global__ __launch_bounds__(256) void ffn_join(const FfnGemm p, int64_t pieces) {
-  const int per_row = (p.N + 7) / 8;
+  const int per_row = (p.N + 3) / 4;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t row = i / per_row;      // batch * M + m
-    const int n = static_cast<int>(i - row * per_row) * 8;
-    const int batch = static_cast<int>(row / p.M);
-    const int64_t m = row - static_cast<int64_t>(batch) * p.M;
+    const int n = static_cast<int>(i - row * per_row) * 4;
+    const int batch = row >= p.M ? 1 : 0;
+    const int64_t m = row - (batch ? p.M : 0);
     const float* src = p.part + (static_cast<int64_t>(batch) * p.splits * p.M + m) * p.Np + n;
     const int64_t step = static_cast<int64_t>(p.M) * p.Np;
-    f32x4 lo{0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
-    for (int s = 0; s < p.splits; ++s) {
-      lo += *reinterpret_cast<const f32x4*>(src + s * step);
-      hi += *reinterpret_cast<const f32x4*>(src + s * step + 4);
+    f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < p.splits; s += 8) {
+      f32x4 w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = *reinterpret_cast<const f32x4*>(src + min(s + k, p.splits - 1) * step);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (s + k < p.splits) v += w[k];
     }
-    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     const int left = p.N - n;
     if (p.c_bf16) {
       unsigned short* c = static_cast<unsigned short*>(p.C[batch]) + m * p.ldc + n;
-      if (p.accumulate) {
+      unsigned short out[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < left) v[e] += from_bf16(c[e]);
+      for (int e = 0; e < 4; ++e) {
+        if (p.accumulate && e < left) v[e] += from_bf16(c[e]);
+        out[e] = to_bf16(v[e]);
       }
-      if (left >= 8) {
-        u32x4 w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = to_bf16(v[2 * e]) | (static_cast<unsigned int>(to_bf16(v[2 * e + 1])) << 16);
-        *reinterpret_cast<u32x4_a2*>(c) = w;
+      if (left >= 4) {
+        *reinterpret_cast<u32x2_a2*>(c) = u32x2{out[0] | (static_cast<unsigned int>(out[1]) << 16),
+                                                out[2] | (static_cast<unsigned int>(out[3]) << 16)};
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < left) c[e] = to_bf16(v[e]);
+        for (int e = 0; e < 4; ++e)
+          if (e < left) c[e] = out[e];
       }
     } else {
       float* c = static_cast<float*>(p.C[batch]) + m * p.ldc + n;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int e = 0; e < 4; ++e)
         if (e < left) c[e] = (p.accumulate ? c[e] : 0.0f) + v[e];
     }
   }
 }
 
-// Copy of a rows x cols matrix whose rows are not 16-byte aligned into one whose rows are
-// (ldd elements apart, zero behind cols): the product kernel's loads need whole chunks.
+// Copies of matrices whose rows are not 16-byte aligned into ones whose rows are (zero behind
+// the last column): the product kernel's loads need whole chunks. One launch for all of a
+// call's operands; a workgroup copies 256 chunks of one.
 template <typename T>
-__global__ __launch_bounds__(256) void ffn_align(const T* src, int64_t lds, T* dst, int64_t ldd, int64_t rows, int cols) {
+__global__ __launch_bounds__(256) void ffn_align(const FfnCopies c) {
   constexpr int VEC = 16 / sizeof(T);
-  const int64_t per_row = ldd / VEC;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < rows * per_row;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = i / per_row;
-    const int c = static_cast<int>(i - r * per_row) * VEC;
-    T v[VEC];
+  int o = 0;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = c + e < cols ? src[r * lds + c + e] : T(0);
-    *reinterpret_cast<u32x4*>(dst + i * VEC) = *reinterpret_cast<const u32x4*>(v);
+  for (int k = 1; k < FfnCopies::kMost; ++k)
+    if (k < c.n && c.block0[k] <= static_cast<int64_t>(blockIdx.x)) o = k;
+  const int64_t i = (blockIdx.x - c.block0[o]) * 256 + threadIdx.x;
+  const int64_t per_row = c.ldd[o] / VEC;
+  const int64_t r = i / per_row;
+  if (r >= c.rows[o]) return;
+  const int at = static_cast<int>(i - r * per_row) * VEC;
+  const T* src = static_cast<const T*>(c.src[o]) + r * c.lds[o] + at;
+  const int left = c.cols[o] - at;
+  u32x4 v;
+  if (left >= VEC) {
+    v = *reinterpret_cast<const u32x4_a2*>(src);
+  } else {
+    T e[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) e[k] = k < left ? src[k] : T(0);
+    v = __builtin_bit_cast(u32x4, e);
   }
+  reinterpret_cast<u32x4*>(c.dst[o])[i] = v;
 }
 
 // out (rows x cols, ld apart) <- 0: the weight gradients of no tokens.
@@ -684,9 +707,13 @@ hipError_t launch(const FfnGemm& p, int batches, hipStream_t st) {
 template <int KIND, bool AS, bool BS, int EPI>
 hipError_t launch_tile(int tile, const FfnGemm& p, int batches, hipStream_t st) {
   switch (tile) {
+    case FFN_TILE_32: return launch<KIND, 32, 32, 1, 1, 4, 8, 8, AS, BS, EPI>(p, batches, st);
     case FFN_TILE_64: return launch<KIND, 64, 64, 2, 2, 2, 4, 8, AS, BS, EPI>(p, batches, st);
     case FFN_TILE_64x128: return launch<KIND, 64, 128, 2, 2, 1, 3, 8, AS, BS, EPI>(p, batches, st);
     case FFN_TILE_128: return launch<KIND, 128, 128, 2, 2, 1, 4, 8, AS, BS, EPI>(p, batches, st);
+    case FFN_TILE_128x256:
+      if constexpr (KIND != KIND_F32) return launch<KIND, 128, 256, 2, 4, 1, 3, 8, AS, BS, EPI>(p, batches, st);
+      return hipErrorInvalidValue;
     case FFN_TILE_256:
       if constexpr (KIND != KIND_F32) return launch<KIND, 256, 256, 2, 4, 1, 2, 8, AS, BS, EPI>(p, batches, st);
       return hipErrorInvalidValue;
@@ -712,23 +739,23 @@ hipError_t launch_ffn(FfnStage stage, bool f32, int tile, const FfnGemm& p, int 
   hipError_t e = f32 ? launch_kind<KIND_F32>(stage, tile, p, batches, st)
                      : launch_kind<KIND_BF16>(stage, tile, p, batches, st);
   if (e != hipSuccess || p.part == nullptr) return e;
-  const int64_t pieces = static_cast<int64_t>(batches) * p.M * ((p.N + 7) / 8);
+  const int64_t pieces = static_cast<int64_t>(batches) * p.M * ((p.N + 3) / 4);
   const int64_t blocks = (pieces + 255) / 256;
   hipLaunchKernelGGL(ffn_join, dim3(static_cast<unsigned int>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, p, pieces);
   return hipGetLastError();
 }
 
-hipError_t launch_ffn_align(const void* src, int64_t ld, void* dst, int64_t ldd, int64_t rows, int cols, bool f32,
-                            hipStream_t st) {
-  const int64_t chunks = rows * ldd * (f32 ? 4 : 2) / 16;
-  const int64_t blocks = (chunks + 255) / 256;
-  const dim3 grid(static_cast<unsigned int>(blocks < 8192 ? blocks : 8192));
-  if (f32)
-    hipLaunchKernelGGL(ffn_align<float>, grid, dim3(256), 0, st, static_cast<const float*>(src), ld,
-                       static_cast<float*>(dst), ldd, rows, cols);
-  else
-    hipLaunchKernelGGL(ffn_align<unsigned short>, grid, dim3(256), 0, st, static_cast<const unsigned short*>(src), ld,
-                       static_cast<unsigned short*>(dst), ldd, rows, cols);
+hipError_t launch_ffn_align(FfnCopies& c, bool f32, hipStream_t st) {
+  if (c.n == 0) return hipSuccess;
+  int64_t blocks = 0;
+  for (int k = 0; k < c.n; ++k) {
+    c.block0[k] = blocks;
+    blocks += (c.rows[k] * c.ldd[k] * (f32 ? 4 : 2) / 16 + 255) / 256;
+  }
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned int>(blocks));
+  if (f32) hipLaunchKernelGGL(ffn_align<float>, grid, dim3(256), 0, st, c);
+  else hipLaunchKernelGGL(ffn_align<unsigned short>, grid, dim3(256), 0, st, c);
   return hipGetLastError();
 }
 

@@ -259,11 +259,13 @@ enum FfnStage : int {
   FFN_STAGE_DW = 4,     // A^T B over the tokens; both K-strided
 };
 enum FfnTile : int {
-  FFN_TILE_64 = 0,      // 64 x 64, two k-groups of 4 waves
-  FFN_TILE_64x128 = 1,  // 4 waves
-  FFN_TILE_128 = 2,     // 128 x 128, 4 waves
-  FFN_TILE_256 = 3,     // 256 x 256, 8 waves; not fp32
-  FFN_TILE_COUNT = 4
+  FFN_TILE_32 = 0,      // 32 x 32, four k-groups of one wave
+  FFN_TILE_64 = 1,      // 64 x 64, two k-groups of 4 waves
+  FFN_TILE_64x128 = 2,  // 4 waves
+  FFN_TILE_128 = 3,     // 128 x 128, 4 waves
+  FFN_TILE_128x256 = 4, // 8 waves; not fp32
+  FFN_TILE_256 = 5,     // 256 x 256, 8 waves; not fp32
+  FFN_TILE_COUNT = 6
 };
 struct FfnGemm {
   const void* A[2];       // operand, or (batched) operand of batch entry 0 / 1
@@ -287,8 +289,15 @@ struct FfnGemm {
   int32_t c_bf16, accumulate;
 };
 hipError_t launch_ffn(FfnStage stage, bool f32, int tile, const FfnGemm& p, int batches, hipStream_t st);
-hipError_t launch_ffn_align(const void* src, int64_t ld, void* dst, int64_t ldd, int64_t rows, int cols, bool f32,
-                            hipStream_t st);
+// Matrices to copy into 16-byte aligned rows.
+struct FfnCopies {
+  static constexpr int kMost = 5;
+  const void* src[kMost]; void* dst[kMost];
+  int64_t lds[kMost], ldd[kMost], rows[kMost], block0[kMost];
+  int32_t cols[kMost];
+  int32_t n;
+};
+hipError_t launch_ffn_align(FfnCopies& c, bool f32, hipStream_t st);
 hipError_t launch_ffn_zero(void* out, int64_t ld, int64_t rows, int64_t cols, bool bf16, hipStream_t st);
 
 // Losses over vocabulary logits (losses.hip): one workgroup per row.

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "internal.hpp"
 
@@ -110,27 +111,27 @@ struct Shape {
 enum Layout { BOTH_CONTIGUOUS = 0, B_STRIDED = 1, BOTH_STRIDED = 2 };
 // [fp32][layout][tile][two workgroups a CU, one]; the two large tiles always have one.
 constexpr float kSliceUs[2][3][FFN_TILE_COUNT][2] = {
-    {{{0.443f, 0.183f}, {0.694f, 0.335f}, {0.518f, 0.518f}, {1.070f, 1.070f}},
-     {{0.443f, 0.256f}, {0.681f, 0.386f}, {0.522f, 0.522f}, {1.136f, 1.136f}},
-     {{0.526f, 0.314f}, {0.679f, 0.414f}, {0.539f, 0.539f}, {1.179f, 1.179f}}},
-    {{{1.177f, 0.568f}, {2.228f, 1.105f}, {2.058f, 2.058f}, {1e9f, 1e9f}},
-     {{1.163f, 0.643f}, {2.009f, 1.117f}, {2.031f, 2.031f}, {1e9f, 1e9f}},
-     {{1.072f, 0.570f}, {2.001f, 1.047f}, {2.058f, 2.058f}, {1e9f, 1e9f}}}};
-constexpr double kFillUs = 1.5, kEpilogueUs = 8.4, kDgateEpilogueUs = 37.0;  // per round; epilogues per 256 x 256
-constexpr double kJoinUs = 2.0, kJoinBytesPerUs = 6.5e6;
+    {{{0.190f, 0.114f}, {0.406f, 0.173f}, {0.669f, 0.329f}, {0.534f, 0.534f}, {0.815f, 0.815f}, {1.375f, 1.375f}},
+     {{0.244f, 0.146f}, {0.424f, 0.213f}, {0.677f, 0.376f}, {0.537f, 0.537f}, {0.815f, 0.815f}, {1.332f, 1.332f}},
+     {{0.309f, 0.179f}, {0.494f, 0.305f}, {0.663f, 0.411f}, {0.575f, 0.575f}, {0.886f, 0.886f}, {1.526f, 1.526f}}},
+    {{{0.353f, 0.184f}, {1.106f, 0.553f}, {2.171f, 1.106f}, {2.143f, 2.143f}, {1e9f, 1e9f}, {1e9f, 1e9f}},
+     {{0.415f, 0.260f}, {1.123f, 0.628f}, {1.932f, 1.123f}, {2.031f, 2.031f}, {1e9f, 1e9f}, {1e9f, 1e9f}},
+     {{0.418f, 0.292f}, {1.017f, 0.582f}, {1.918f, 1.053f}, {2.084f, 2.084f}, {1e9f, 1e9f}, {1e9f, 1e9f}}}};
+constexpr double kFillUs = 2.2, kEpilogueUs = 4.0, kDgateEpilogueUs = 35.2;  // per round; epilogues per 256 x 256
+constexpr double kJoinUs = 2.7, kJoinBytesPerUs = 6.2e6;
 constexpr int64_t kMaxPartBytes = int64_t{1} << 28;
 constexpr int64_t kMinSplitSlices = 4;
 
 // cols: tile columns covered (twice the output's for the gate stage); dgate: its epilogue.
 Shape choose(bool f32, Layout layout, int64_t M, int64_t cols, int64_t slices, int batches, bool may_split, bool dgate,
              int cus) {
-  static const int bm[FFN_TILE_COUNT] = {64, 64, 128, 256}, bn[FFN_TILE_COUNT] = {64, 128, 128, 256};
-  static const int per_cu[FFN_TILE_COUNT] = {2, 2, 1, 1};
+  static const int bm[FFN_TILE_COUNT] = {32, 64, 64, 128, 128, 256}, bn[FFN_TILE_COUNT] = {32, 64, 128, 128, 256, 256};
+  static const int per_cu[FFN_TILE_COUNT] = {2, 2, 2, 1, 1, 1};
   static const int try_splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
   Shape best;
   double best_us = 1e300;
   for (int t = 0; t < FFN_TILE_COUNT; ++t) {
-    if (f32 && t == FFN_TILE_256) continue;
+    if (f32 && t >= FFN_TILE_128x256) continue;
     const int64_t tm = cdiv(M, bm[t]), tn = cdiv(cols, bn[t]);
     const double area = bm[t] * bn[t] / 65536.0;
     for (const int want : try_splits) {
@@ -211,10 +212,18 @@ FfnPlan plan_of(const muon_ffn* f, const muon_ffn_grads* g, int cus) {
   return p;
 }
 
-hipError_t settle(Operand& o, char* ws, bool f32, hipStream_t st) {
-  if (!o.copied) return hipSuccess;
-  o.p = ws + o.off;
-  return launch_ffn_align(o.src, o.src_ld, ws + o.off, o.ld, o.rows, static_cast<int>(o.cols), f32, st);
+hipError_t settle(std::initializer_list<Operand*> operands, char* ws, bool f32, hipStream_t st) {
+  FfnCopies c;
+  c.n = 0;
+  for (Operand* o : operands) {
+    if (!o->copied) continue;
+    o->p = ws + o->off;
+    c.src[c.n] = o->src; c.lds[c.n] = o->src_ld;
+    c.dst[c.n] = ws + o->off; c.ldd[c.n] = o->ld;
+    c.rows[c.n] = o->rows; c.cols[c.n] = static_cast<int32_t>(o->cols);
+    ++c.n;
+  }
+  return launch_ffn_align(c, f32, st);
 }
 
 FfnGemm product(const Shape& s, int64_t M, int64_t N, int64_t K, int act) {
@@ -320,7 +329,7 @@ int muon_ffn_forward(muon_ctx* ctx, const muon_ffn* f, void* y, int64_t ld_y, vo
     const hipStream_t st = static_cast<hipStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     const bool f32 = f->dtype == MUON_F32;
-    for (Operand* o : {&p.x, &p.wg, &p.wu, &p.wd}) MUON_HIP(settle(*o, ws, f32, st));
+    MUON_HIP(settle({&p.x, &p.wg, &p.wu, &p.wd}, ws, f32, st));
     const int64_t T = f->tokens, D = f->dim, F = f->hidden;
 
     FfnGemm q = product(p.gate, T, F, D, f->activation);
@@ -370,7 +379,7 @@ int muon_ffn_backward(muon_ctx* ctx, const muon_ffn* f, const muon_ffn_grads* g,
       return MUON_OK;
     }
     char* ws = static_cast<char*>(workspace);
-    for (Operand* o : {&p.x, &p.wg, &p.wu, &p.wd, &p.dy}) MUON_HIP(settle(*o, ws, f32, st));
+    MUON_HIP(settle({&p.x, &p.wg, &p.wu, &p.wd, &p.dy}, ws, f32, st));
     char *h = ws + p.off_h, *dgp = ws + p.off_dg, *dup = dgp + p.Hp * p.es, *part = ws + p.off_part;
 
     FfnGemm q = product(p.dgate, T, F, D, f->activation);
