@@ -441,6 +441,12 @@ typedef struct muon_logits {
   int32_t lse_given;       /* 0 or 1 */
 } muon_logits;
 
+/* Bytes of workspace (256-byte aligned; 0: none, null is accepted) muon_policy_loss (top 0) or
+ * muon_distill_loss (its number of kept entries) needs for these logits: rows, vocab, dtype,
+ * lse_given and whether dlogits is null count. Not zero only for fewer rows than half the
+ * GPU's CUs. */
+int muon_loss_workspace_size(muon_ctx *ctx, const muon_logits *l, int top, size_t *bytes);
+
 /* Clipped policy loss with a KL term. Row r with target t, lp = z_t - lse,
  * rho = exp(lp - old_logp), A the advantage:
  *   l = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A)
@@ -457,7 +463,8 @@ typedef struct muon_policy {
   float kl_coef;
 } muon_policy;
 
-int muon_policy_loss(muon_ctx *ctx, const muon_logits *l, const muon_policy *t, void *stream);
+int muon_policy_loss(muon_ctx *ctx, const muon_logits *l, const muon_policy *t, void *workspace,
+                     size_t workspace_bytes, void *stream);
 
 /* Distillation from a teacher's `top` kept logits per row (entry j: logit t_j at column
  * i_j), p_j = exp(t_j / temperature - L) with L = top_lse[r], the teacher's log sum exp of its
@@ -479,7 +486,8 @@ typedef struct muon_distill {
   int32_t id_dtype;        /* MUON_I32 or MUON_I64 */
 } muon_distill;
 
-int muon_distill_loss(muon_ctx *ctx, const muon_logits *l, const muon_distill *t, void *stream);
+int muon_distill_loss(muon_ctx *ctx, const muon_logits *l, const muon_distill *t, void *workspace,
+                      size_t workspace_bytes, void *stream);
 
 /* ---- Owner assignment: which rank updates which matrix ----
  * DMuon summary (gist.science), section 2.3 (compute-aware load balancing): the update

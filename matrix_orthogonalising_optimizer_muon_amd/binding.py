@@ -201,9 +201,14 @@ _lib.muon_ffn_forward.restype = ctypes.c_int
 _lib.muon_ffn_backward.argtypes = [_P, ctypes.POINTER(muon_ffn), ctypes.POINTER(muon_ffn_grads), _P,
                                    ctypes.c_size_t, _P]
 _lib.muon_ffn_backward.restype = ctypes.c_int
-_lib.muon_policy_loss.argtypes = [_P, ctypes.POINTER(muon_logits), ctypes.POINTER(muon_policy), _P]
+_lib.muon_loss_workspace_size.argtypes = [_P, ctypes.POINTER(muon_logits), ctypes.c_int,
+                                          ctypes.POINTER(ctypes.c_size_t)]
+_lib.muon_loss_workspace_size.restype = ctypes.c_int
+_lib.muon_policy_loss.argtypes = [_P, ctypes.POINTER(muon_logits), ctypes.POINTER(muon_policy), _P,
+                                  ctypes.c_size_t, _P]
 _lib.muon_policy_loss.restype = ctypes.c_int
-_lib.muon_distill_loss.argtypes = [_P, ctypes.POINTER(muon_logits), ctypes.POINTER(muon_distill), _P]
+_lib.muon_distill_loss.argtypes = [_P, ctypes.POINTER(muon_logits), ctypes.POINTER(muon_distill), _P,
+                                   ctypes.c_size_t, _P]
 _lib.muon_distill_loss.restype = ctypes.c_int
 _lib.muon_destroy.argtypes = [_P]
 _lib.muon_destroy.restype = ctypes.c_int
@@ -474,12 +479,21 @@ def muon_ffn_backward(ctx, f: muon_ffn, g: muon_ffn_grads, workspace: int | None
     return _lib.muon_ffn_backward(ctx, f, g, workspace, workspace_bytes, stream_ptr)
 
 
-def muon_policy_loss(ctx, l: muon_logits, t: muon_policy, stream_ptr: int | None) -> int:
-    return _lib.muon_policy_loss(ctx, l, t, stream_ptr)
+def muon_loss_workspace_size(ctx, l: muon_logits, top: int = 0) -> int:
+    """Workspace bytes of ``muon_policy_loss``, or of ``muon_distill_loss`` with ``top`` entries."""
+    n = ctypes.c_size_t()
+    check(_lib.muon_loss_workspace_size(ctx, l, int(top), n), "muon_loss_workspace_size")
+    return n.value
 
 
-def muon_distill_loss(ctx, l: muon_logits, t: muon_distill, stream_ptr: int | None) -> int:
-    return _lib.muon_distill_loss(ctx, l, t, stream_ptr)
+def muon_policy_loss(ctx, l: muon_logits, t: muon_policy, workspace: int | None, workspace_bytes: int,
+                     stream_ptr: int | None) -> int:
+    return _lib.muon_policy_loss(ctx, l, t, workspace, workspace_bytes, stream_ptr)
+
+
+def muon_distill_loss(ctx, l: muon_logits, t: muon_distill, workspace: int | None, workspace_bytes: int,
+                      stream_ptr: int | None) -> int:
+    return _lib.muon_distill_loss(ctx, l, t, workspace, workspace_bytes, stream_ptr)
 
 
 def shape_cost(points) -> muon_shape_cost:
@@ -521,5 +535,6 @@ def exported_symbols() -> list:
                         "muon_plan_info", "muon_debug_gemm", "muon_debug_stage", "muon_profile_read", "muon_tune_save",
                         "muon_tune_load", "muon_adamw_hparams_default", "muon_adamw_step",
                         "muon_destroy", "muon_status_str", "muon_owner_plan", "muon_ffn_workspace_size",
-                        "muon_ffn_forward", "muon_ffn_backward", "muon_policy_loss", "muon_distill_loss")
+                        "muon_ffn_forward", "muon_ffn_backward", "muon_loss_workspace_size", "muon_policy_loss",
+                        "muon_distill_loss")
             if hasattr(_lib, n)]

@@ -19,7 +19,8 @@ struct DeviceGuard {
   int prev = -1;
   bool ok = false;
   explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) == hipSuccess && hipSetDevice(dev) == hipSuccess) ok = true;
+    ok = hipGetDevice(&prev) == hipSuccess && (prev == dev || hipSetDevice(dev) == hipSuccess);
+    if (prev == dev) prev = -1;  // nothing to restore
   }
   ~DeviceGuard() {
     if (prev >= 0) (void)hipSetDevice(prev);
@@ -324,6 +325,10 @@ struct LossParams {
   const void* ids; int64_t ld_ids;
   const float* top_lse;             // null: normalised over the kept entries
   int32_t top, top_bf16, ids64;
+  // few rows: each in `splits` parts (at most 64) of `part` 16-byte vectors
+  int32_t splits, part;
+  float* stats;                     // [rows][splits] running maximum and sum
+  float* own;                       // [rows] target logit, or [rows][top] kept entries' logits
 };
 hipError_t launch_loss(int loss, bool bf16, const LossParams& p, hipStream_t st);
 

@@ -123,32 +123,109 @@ struct Shared {
   float sum[16];
 };
 
+// Few long rows: every row is split into p.splits parts of p.part vectors, one workgroup
+// each. This kernel leaves each part's running maximum and sum, and the row's own logits
+// (the target's, or the kept entries'), which a gradient in place may overwrite, in the
+// workspace; loss_kernel with SPLIT joins them and does the rest.
+template <typename E, int LOSS, int THREADS>
+__global__ __launch_bounds__(THREADS) void loss_parts(const LossParams p) {
+  using R = Row<E>;
+  __shared__ Stat lds[THREADS / 64];
+  const int tid = threadIdx.x;
+  const int64_t r = blockIdx.x / p.splits;
+  const int part = blockIdx.x - static_cast<int>(r) * p.splits;
+  const int V = p.vocab;
+  const E* z = static_cast<const E*>(p.logits) + r * p.ld;
+  if (p.weights && p.weights[r] == 0.0f) return;
+  if (LOSS == LOSS_POLICY && (p.targets[r] < 0 || p.targets[r] >= V)) return;
+  if (part == 0) {
+    float* own = p.own + r * (LOSS == LOSS_POLICY ? 1 : p.top);
+    if constexpr (LOSS == LOSS_POLICY) {
+      if (tid == 0) own[0] = R::from(z[p.targets[r]]);
+    } else {
+      for (int j = tid; j < p.top; j += THREADS) {
+        const int64_t id = p.ids64 ? static_cast<const int64_t*>(p.ids)[r * p.ld_ids + j]
+                                   : static_cast<const int32_t*>(p.ids)[r * p.ld_ids + j];
+        own[j] = id >= 0 && id < V ? R::from(z[id]) : 0.0f;
+      }
+    }
+  }
+  if (p.lse_given) return;
+  const float c = p.inv_temperature * kLog2e;
+  const int full = V / R::VEC;
+  const int first = part * p.part, last = min(full, first + p.part);
+  Stat st{-INFINITY, 0.0f};
+#pragma unroll 4
+  for (int i = first + tid; i < last; i += THREADS) {
+    float v[R::VEC];
+    R::unpack(R::load(z + static_cast<int64_t>(i) * R::VEC), v);
+    float mx = st.m;
+#pragma unroll
+    for (int e = 0; e < R::VEC; ++e) mx = fmaxf(mx, v[e]);
+    const float at = base_of(mx);
+    float s = st.s * __builtin_amdgcn_exp2f((st.m - at) * c);
+#pragma unroll
+    for (int e = 0; e < R::VEC; ++e) s += __builtin_amdgcn_exp2f((v[e] - at) * c);
+    st = {mx, s};
+  }
+  const int tail = full * R::VEC + tid;
+  if (part == p.splits - 1 && tail < V) {
+    const float v = R::from(z[tail]);
+    st = join(st, Stat{v, v == v ? 1.0f : v}, c);
+  }
+  st = join_all<THREADS>(st, c, lds);
+  if (tid == 0) {
+    p.stats[(r * p.splits + part) * 2] = st.m;
+    p.stats[(r * p.splits + part) * 2 + 1] = st.s;
+  }
+}
+
 // NV > 0: the row stays in registers between the passes, NV 16-byte vectors a thread, and is
-// read once. NV == 0: the second pass reads it again (rows too long to hold).
-template <typename E, int LOSS, int THREADS, int NV>
+// read once. NV == 0: the second pass reads it again (rows too long to hold). SPLIT: the
+// second pass of one part of a row, after loss_parts. SAFE: the row has more than
+// SAFE x THREADS vectors.
+template <typename E, int LOSS, int THREADS, int NV, int SAFE, bool SPLIT = false>
 __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
+  static_assert(!SPLIT || NV == 0, "a part is read again");
   using R = Row<E>;
   constexpr int VEC = R::VEC;
   constexpr int KT = LOSS == LOSS_DISTILL ? (kMaxTop + THREADS - 1) / THREADS : 1;  // kept entries a thread takes
   __shared__ Shared sh;
   __shared__ __attribute__((aligned(16))) int col[LOSS == LOSS_DISTILL ? kMaxTop : 4];   // the kept entries' columns, -1: absent
-  __shared__ float mass_of[LOSS == LOSS_DISTILL ? kMaxTop : 1];                          // and teacher probabilities
+  __shared__ float p_of[LOSS == LOSS_DISTILL ? kMaxTop : 1];    // their teacher probabilities p, then loss terms
+  __shared__ float lp_of[LOSS == LOSS_DISTILL ? kMaxTop : 1];   // log2 p, then the student's logit
+  __shared__ float fix_of[LOSS == LOSS_DISTILL ? kMaxTop : 1];  // the column's sum of p (-1: absent, or not the column's first)
+  __shared__ int head[LOSS == LOSS_DISTILL ? THREADS : 1];      // entries by the thread that writes their column
+  __shared__ int next_of[LOSS == LOSS_DISTILL ? kMaxTop : 1];
 
   const int tid = threadIdx.x;
-  const int64_t r = blockIdx.x;
+  const int64_t r = SPLIT ? blockIdx.x / p.splits : blockIdx.x;
+  const int part = SPLIT ? static_cast<int>(blockIdx.x - r * p.splits) : 0;
   const int V = p.vocab;
   const E* z = static_cast<const E*>(p.logits) + r * p.ld;
   E* d = p.dlogits ? static_cast<E*>(p.dlogits) + r * p.ld_d : nullptr;
   const float c = p.inv_temperature * kLog2e;
+  // the row's scalars, requested together
   const float w = p.weights ? p.weights[r] : 1.0f;
-  const int full = V / VEC;                 // whole vectors
-  const int tail = full * VEC + tid;        // the column behind them that this thread takes
+  const float up = p.grad_rows ? p.grad_rows[r] : 1.0f;
+  float adv = 0.0f, old_logp = 0.0f, ref_logp = 0.0f;
   int64_t target = 0;
-  if constexpr (LOSS == LOSS_POLICY) target = p.targets[r];
+  if constexpr (LOSS == LOSS_POLICY) {
+    target = p.targets[r];
+    adv = p.advantages[r];
+    old_logp = p.old_logp[r];
+    if (p.ref_logp) ref_logp = p.ref_logp[r];
+  }
+  const int full = V / VEC;                 // whole vectors
+  const int v0 = SPLIT ? part * p.part : 0, v1 = SPLIT ? min(full, v0 + p.part) : full;  // this workgroup's
+  const bool last_part = !SPLIT || part == p.splits - 1;
+  // the column behind the whole vectors that this thread takes
+  const int tail = last_part ? full * VEC + tid : V;
+  const bool first = tid == 0 && part == 0;  // writes the row's scalars
 
   // A row that takes no part (weight 0, or no target) is not read.
   if (w == 0.0f || target < 0 || target >= V) {
-    if (tid == 0) {
+    if (first) {
       if (p.loss) p.loss[r] = 0.0f;
       if (!p.lse_given && p.lse) p.lse[r] = 0.0f;
       if (LOSS == LOSS_POLICY && p.logp) p.logp[r] = 0.0f;
@@ -157,51 +234,110 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
       float zero[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) zero[e] = 0.0f;
-      for (int i = tid; i < full; i += THREADS) R::store(d + static_cast<int64_t>(i) * VEC, zero);
+      for (int i = v0 + tid; i < v1; i += THREADS) R::store(d + static_cast<int64_t>(i) * VEC, zero);
       if (tail < V) d[tail] = R::to(0.0f);
     }
     return;
   }
 
-  // The teacher's entries first, then the row: loads return in order, so the columns are
-  // known (and their logits requested) while the row is still on its way.
-  float tt[KT], tz[KT];
-  int tc[KT];
+  // The teacher's entries are requested before the row and decoded after it (loads return in
+  // order): their columns' logits, their normaliser and mass and the repeated columns are
+  // dealt with while the row is on its way. Ids as two words, the upper one of a 32-bit id
+  // being itself.
+  unsigned int id_lo[KT], id_hi[KT], t_word[KT];
   if constexpr (LOSS == LOSS_DISTILL) {
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
-      const int j = k * THREADS + tid;
-      tc[k] = -1;
-      tt[k] = -INFINITY;
-      tz[k] = 0.0f;
-      if (j < p.top) {
-        const int64_t id = p.ids64 ? static_cast<const int64_t*>(p.ids)[r * p.ld_ids + j]
-                                   : static_cast<const int32_t*>(p.ids)[r * p.ld_ids + j];
-        const int64_t at = r * p.ld_top + j;
-        const float t = p.top_bf16 ? Row<unsigned short>::from(static_cast<const unsigned short*>(p.top_logits)[at])
-                                   : static_cast<const float*>(p.top_logits)[at];
-        if (id >= 0 && id < V) {
-          tc[k] = static_cast<int>(id);
-          tt[k] = t;
-        }
-      }
+      const int j = min(k * THREADS + tid, p.top - 1);
+      const char* id = static_cast<const char*>(p.ids) + (r * p.ld_ids + j) * (p.ids64 ? 8 : 4);
+      id_lo[k] = *reinterpret_cast<const unsigned int*>(id);
+      id_hi[k] = *reinterpret_cast<const unsigned int*>(id + (p.ids64 ? 4 : 0));
+      const int64_t t = r * p.ld_top + j;
+      if (p.top_bf16) t_word[k] = static_cast<const unsigned short*>(p.top_logits)[t];
+      else t_word[k] = static_cast<const unsigned int*>(p.top_logits)[t];
     }
   }
+  const float zl = R::from(z[min(tail, V - 1)]);
+  float zt = 0.0f;
+  if constexpr (LOSS == LOSS_POLICY) zt = SPLIT ? p.own[r] : R::from(z[target]);
   u32x4 row[NV > 0 ? NV : 1];
   if constexpr (NV > 0) {
     // past the row's last vector a thread loads that one again and leaves it out below
-    if (d || !p.lse_given)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) row[i] = R::load(z + static_cast<int64_t>(min(i * THREADS + tid, full - 1)) * VEC);
+    for (int i = 0; i < NV; ++i) {
+      if (i < SAFE) row[i] = R::load(z + i * THREADS * VEC + tid * VEC);
+      else row[i] = R::load(z + min(i * THREADS + tid, full - 1) * VEC);
+      // in the order of their use, and the entries' decoding behind them
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
-  const float zl = tail < V ? R::from(z[tail]) : 0.0f;
-  float zt = 0.0f;
-  if constexpr (LOSS == LOSS_POLICY) {
-    zt = R::from(z[target]);
-  } else {
+  float mass = 0.0f;
+  if constexpr (LOSS == LOSS_DISTILL) {
+    head[tid] = -1;
+    float tt[KT];
+    int tc[KT];
 #pragma unroll
-    for (int k = 0; k < KT; ++k)
-      if (tc[k] >= 0) tz[k] = R::from(z[tc[k]]);
+    for (int k = 0; k < KT; ++k) {
+      const int j = k * THREADS + tid;
+      const int64_t id = p.ids64 ? static_cast<int64_t>((static_cast<uint64_t>(id_hi[k]) << 32) | id_lo[k])
+                                 : static_cast<int32_t>(id_lo[k]);
+      const bool in = j < p.top && id >= 0 && id < V;
+      tc[k] = in ? static_cast<int>(id) : -1;
+      const float t = __uint_as_float(p.top_bf16 ? t_word[k] << 16 : t_word[k]);
+      tt[k] = in ? t : -INFINITY;
+    }
+    // p_j = exp((t_j - tm) c - log2 of the normaliser)
+    float tm, tlog2;
+    if (p.top_lse) {
+      tm = 0.0f;
+      tlog2 = p.top_lse[r] * kLog2e;
+    } else {
+      Stat st{-INFINITY, 0.0f};
+#pragma unroll
+      for (int k = 0; k < KT; ++k) st = join(st, Stat{tt[k], tt[k] == -INFINITY ? 0.0f : 1.0f}, c);
+      st = join_all<THREADS>(st, c, sh.stat);
+      tm = base_of(st.m);
+      tlog2 = __builtin_amdgcn_logf(st.s);
+    }
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      const float lp = (tt[k] - tm) * c - tlog2;
+      const float pk = tt[k] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lp);
+      mass += pk;
+      const int j = k * THREADS + tid;
+      if (j < kMaxTop) {
+        col[j] = tc[k];
+        p_of[j] = pk;
+        lp_of[j] = lp;
+      }
+    }
+    mass = sum_all<THREADS>(mass, sh.sum);
+    // A column that occurs more than once: its first entry carries the sum, the others nothing.
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      const int j = k * THREADS + tid;
+      if (j >= p.top) continue;
+      float fix = 0.0f;
+      bool lead = tc[k] >= 0;
+      for (int o = 0; lead && o < p.top; o += 4) {
+        const int4 others = *reinterpret_cast<const int4*>(col + o);  // entries behind the last are -1
+        const int oc[4] = {others.x, others.y, others.z, others.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (oc[e] == tc[k]) {
+            if (o + e < j) lead = false;
+            else fix += p_of[o + e];
+          }
+      }
+      fix_of[j] = lead ? fix : -1.0f;  // sums are not negative (a NaN is kept)
+      // into the list of the thread that writes this column (in any order: the list is only
+      // walked for values of the entries' own)
+      const int v = tc[k] / VEC;
+      if (tc[k] >= 0 && v >= v0 && (last_part || v < v1)) {
+        const int owner = v >= full ? tc[k] - full * VEC : (v - v0) % THREADS;
+        next_of[j] = atomicExch(&head[owner], j);
+      }
+    }
   }
 
   // m and s: q_v = exp2((z_v - m) c) / s, log2 of the normaliser (m c + log2 s).
@@ -210,17 +346,28 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     m = 0.0f;
     log2s = p.lse[r] * kLog2e;
     inv_s = 1.0f;
+  } else if constexpr (SPLIT) {
+    // every wave joins the parts in the same order (at most 64, one a lane)
+    const int lane = tid & 63;
+    Stat st{-INFINITY, 0.0f};
+    if (lane < p.splits) st = Stat{p.stats[(r * p.splits + lane) * 2], p.stats[(r * p.splits + lane) * 2 + 1]};
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) st = join(st, Stat{__shfl_xor(st.m, o), __shfl_xor(st.s, o)}, c);
+    m = st.m;
+    log2s = __builtin_amdgcn_logf(st.s);
+    inv_s = 1.0f / st.s;
+    if (first && p.lse) p.lse[r] = m * p.inv_temperature + log2s * kLn2;
   } else {
     Stat st{-INFINITY, 0.0f};
     // one rescale of the running sum per G vectors
     constexpr int G = NV == 0 ? 1 : 16 / VEC;
-    auto take = [&](const u32x4* vec, auto n_tag, int first) {
+    auto take = [&](const u32x4* vec, auto n_tag, int at0) {
       constexpr int N = decltype(n_tag)::value;
       float v[N][VEC], mx = st.m;
 #pragma unroll
       for (int g = 0; g < N; ++g) {
         R::unpack(vec[g], v[g]);
-        const bool in = NV == 0 || (first + g) * THREADS + tid < full;
+        const bool in = NV == 0 || at0 + g < SAFE || (at0 + g) * THREADS + tid < full;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           v[g][e] = in ? v[g][e] : -INFINITY;
@@ -237,7 +384,10 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     };
     if constexpr (NV > 0) {
 #pragma unroll
-      for (int i = 0; i + G <= NV; i += G) take(row + i, std::integral_constant<int, G>{}, i);
+      for (int i = 0; i + G <= NV; i += G) {
+        take(row + i, std::integral_constant<int, G>{}, i);
+        __builtin_amdgcn_sched_barrier(0);  // a group when it has arrived, not all of them behind the last
+      }
       if constexpr (NV % G != 0) take(row + NV / G * G, std::integral_constant<int, NV % G>{}, NV / G * G);
     } else {
       for (int i = tid; i < full; i += THREADS) {
@@ -250,88 +400,68 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     m = st.m;
     log2s = __builtin_amdgcn_logf(st.s);
     inv_s = 1.0f / st.s;
-    if (tid == 0 && p.lse) p.lse[r] = m * p.inv_temperature + log2s * kLn2;
+    if (first && p.lse) p.lse[r] = m * p.inv_temperature + log2s * kLn2;
   }
 
-  const float up = p.grad_rows ? p.grad_rows[r] : 1.0f;
   const float scale = w * up * p.inv_temperature;
   float coef;  // dlogits_v = coef q_v, less the kept entries' part
-  float fix[KT];
   if constexpr (LOSS == LOSS_POLICY) {
     const float lp = ((zt - m) * c - log2s) * kLn2;
-    const float adv = p.advantages[r];
-    const float rho = __builtin_amdgcn_exp2f((lp - p.old_logp[r]) * kLog2e);
+    const float rho = __builtin_amdgcn_exp2f((lp - old_logp) * kLog2e);
     const float kept = rho * adv;
     const float cut = fminf(fmaxf(rho, 1.0f - p.clip_low), 1.0f + p.clip_high) * adv;
     float loss = kept <= cut ? -kept : -cut;
     float slope = kept <= cut ? -kept : 0.0f;
     if (kept != kept) loss = slope = kept;
     if (p.ref_logp) {
-      const float diff = p.ref_logp[r] - lp, em1 = expm1_f(diff);
+      const float diff = ref_logp - lp, em1 = expm1_f(diff);
       loss += p.kl_coef * (em1 - diff);
       slope -= p.kl_coef * em1;
     }
-    if (tid == 0) {
+    if (first) {
       if (p.loss) p.loss[r] = loss * w;
       if (p.logp) p.logp[r] = lp;
     }
     coef = -slope * scale;
   } else {
-    // Teacher: p_j = exp((t_j - tm) c - log2 of the normaliser)
-    float tm, tlog2;
-    if (p.top_lse) {
-      tm = 0.0f;
-      tlog2 = p.top_lse[r] * kLog2e;
-    } else {
-      Stat st{-INFINITY, 0.0f};
-#pragma unroll
-      for (int k = 0; k < KT; ++k) st = join(st, Stat{tt[k], tt[k] == -INFINITY ? 0.0f : 1.0f}, c);
-      st = join_all<THREADS>(st, c, sh.stat);
-      tm = base_of(st.m);
-      tlog2 = __builtin_amdgcn_logf(st.s);
-    }
-    float mass = 0.0f, loss = 0.0f, pj[KT];
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      const float lpj = (tt[k] - tm) * c - tlog2;        // log2 p_j
-      pj[k] = tt[k] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lpj);
-      mass += pj[k];
-      if (pj[k] != 0.0f) loss += pj[k] * (lpj - ((tz[k] - m) * c - log2s));
-      const int j = k * THREADS + tid;
-      if (j < kMaxTop) {
-        col[j] = tc[k];
-        mass_of[j] = pj[k];
-      }
-    }
-    mass = sum_all<THREADS>(mass, sh.sum);
-    loss = sum_all<THREADS>(loss, sh.sum);
-    if (tid == 0 && p.loss) p.loss[r] = loss * kLn2 * w;
     coef = mass * scale;
-    // A column that occurs more than once: its first entry carries the sum, the others nothing.
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      fix[k] = 0.0f;
-      const int j = k * THREADS + tid;
-      if (tc[k] < 0) continue;
-      for (int o = 0; o < p.top; o += 4) {
-        const int4 others = *reinterpret_cast<const int4*>(col + o);  // entries behind the last are -1
-        const int oc[4] = {others.x, others.y, others.z, others.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (oc[e] == tc[k]) {
-            if (o + e < j) tc[k] = -1;
-            else fix[k] += mass_of[o + e];
-          }
-        if (tc[k] < 0) break;
-      }
-      fix[k] *= scale;
+  }
+  if constexpr (LOSS == LOSS_DISTILL) {
+    // The entries' logits and loss terms: each by the thread that will write its column, so
+    // that in place no other thread can have overwritten it (SPLIT: from the workspace).
+    __syncthreads();
+    auto term = [&](int j, float zj) {
+      const float pk = p_of[j];
+      p_of[j] = pk != 0.0f ? pk * (lp_of[j] - ((zj - m) * c - log2s)) : 0.0f;
+      lp_of[j] = zj;
+    };
+    if constexpr (SPLIT) {
+      for (int j = tid; j < p.top; j += THREADS) term(j, p.own[r * p.top + j]);
+      __syncthreads();
+    } else {
+      for (int j = head[tid]; j >= 0; j = next_of[j]) term(j, R::from(z[col[j]]));
     }
   }
-  if (!d) return;
+  // The row's loss: the terms in the order of the entries.
+  auto distill_row = [&] {
+    __syncthreads();
+    if (!p.loss || part != 0) return;
+    float loss = 0.0f;
+    for (int j = tid; j < p.top; j += THREADS) loss += p_of[j];
+    loss = sum_all<THREADS>(loss, sh.sum);
+    if (tid == 0) p.loss[r] = loss * kLn2 * w;
+  };
+  if (!d) {
+    if constexpr (LOSS == LOSS_DISTILL) distill_row();
+    return;
+  }
 
-  // In place: every thread has read the row's scalars by now (and, with the row in
-  // registers, the row); with a second pass a thread reads a vector before it writes it.
-  __syncthreads();
+  // In place: every thread has received the target's logit before any writes; a vector is
+  // read, here or before, by the thread that writes it.
+  if (LOSS == LOSS_POLICY && p.dlogits == p.logits) {
+    wait_vmcnt<0>();
+    __syncthreads();
+  }
   const float cq = coef * inv_s;
   const float shift = p.lse_given ? log2s : 0.0f;
   auto give = [&](const u32x4& vec, int i) {
@@ -350,9 +480,13 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
   if constexpr (NV > 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (i * THREADS + tid < full) give(row[i], i * THREADS + tid);
+    {
+      // unpacked anew: the first pass's 8 floats a vector do not stay beside the vector
+      asm volatile("" : "+v"(row[i]));
+      if (i < SAFE || i * THREADS + tid < full) give(row[i], i * THREADS + tid);
+    }
   } else {
-    for (int i = tid; i < full; i += THREADS) give(R::load(z + static_cast<int64_t>(i) * VEC), i);
+    for (int i = v0 + tid; i < v1; i += THREADS) give(R::load(z + static_cast<int64_t>(i) * VEC), i);
   }
   if (tail < V) {
     float v = cq * __builtin_amdgcn_exp2f((zl - m) * c - shift);
@@ -360,35 +494,43 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     d[tail] = R::to(v);
   }
   if constexpr (LOSS == LOSS_DISTILL) {
-    // The kept columns again, with the teacher's part. The row's stores have reached this
-    // XCD's L2 before any of these is issued (a wait for them and a barrier; a device-wide
-    // fence would write the L2 back: 1685 us against 339 us for 2048 rows of 152064).
-    wait_vmcnt<0>();
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-      if (tc[k] >= 0) d[tc[k]] = R::to(cq * __builtin_amdgcn_exp2f((tz[k] - m) * c - shift) - fix[k]);
+    // The kept columns again, with the teacher's part, by the thread that wrote them above:
+    // its stores to one address stay in order. (Any other thread would have to wait for all
+    // of the row's stores: 2048 rows of 152064 took 299 us that way.)
+    for (int j = head[tid]; j >= 0; j = next_of[j])
+      if (!(fix_of[j] < 0.0f))
+        d[col[j]] = R::to(cq * __builtin_amdgcn_exp2f((lp_of[j] - m) * c - shift) - fix_of[j] * scale);
+    distill_row();
   }
 }
 
-template <typename E, int LOSS, int THREADS, int NV>
+template <typename E, int LOSS, int THREADS, int NV, int SAFE = 0>
 hipError_t launch_as(const LossParams& p, hipStream_t st) {
-  hipLaunchKernelGGL((loss_kernel<E, LOSS, THREADS, NV>), dim3(static_cast<unsigned int>(p.rows)), dim3(THREADS), 0, st, p);
+  hipLaunchKernelGGL((loss_kernel<E, LOSS, THREADS, NV, SAFE>), dim3(static_cast<unsigned int>(p.rows)), dim3(THREADS), 0, st, p);
   return hipGetLastError();
 }
 
 // The smallest form that holds the row; a row past the largest is read twice.
 template <typename E, int LOSS>
 hipError_t launch(const LossParams& p, hipStream_t st) {
+  if (p.splits > 1) {
+    const dim3 grid(static_cast<unsigned int>(p.rows * p.splits));
+    hipLaunchKernelGGL((loss_parts<E, LOSS, 256>), grid, dim3(256), 0, st, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((loss_kernel<E, LOSS, 256, 0, 0, true>), grid, dim3(256), 0, st, p);
+    return hipGetLastError();
+  }
   const int vectors = p.vocab / Row<E>::VEC;
-  if (vectors < 1) return launch_as<E, LOSS, 256, 0>(p, st);
+  // without a gradient and with the normaliser given no row is read
+  if (vectors < 1 || (!p.dlogits && p.lse_given)) return launch_as<E, LOSS, 256, 0>(p, st);
   if (vectors <= 256 * 4) return launch_as<E, LOSS, 256, 4>(p, st);
-  if (vectors <= 256 * 8) return launch_as<E, LOSS, 256, 8>(p, st);
-  if (vectors <= 256 * 16) return launch_as<E, LOSS, 256, 16>(p, st);
-  if (vectors <= 512 * 16) return launch_as<E, LOSS, 512, 16>(p, st);
-  if (vectors <= 1024 * 12) return launch_as<E, LOSS, 1024, 12>(p, st);
-  if (vectors <= 1024 * 16) return launch_as<E, LOSS, 1024, 16>(p, st);
-  if (vectors <= 1024 * 19) return launch_as<E, LOSS, 1024, 19>(p, st);
+  if (vectors <= 256 * 8) return launch_as<E, LOSS, 256, 8, 4>(p, st);
+  if (vectors <= 256 * 16) return launch_as<E, LOSS, 256, 16, 8>(p, st);
+  if (vectors <= 512 * 16) return launch_as<E, LOSS, 512, 16, 8>(p, st);
+  if (vectors <= 1024 * 12) return launch_as<E, LOSS, 1024, 12, 8>(p, st);
+  if (vectors <= 1024 * 16) return launch_as<E, LOSS, 1024, 16, 12>(p, st);
+  if (vectors <= 1024 * 19) return launch_as<E, LOSS, 1024, 19, 16>(p, st);
   return launch_as<E, LOSS, 1024, 0>(p, st);
 }
 

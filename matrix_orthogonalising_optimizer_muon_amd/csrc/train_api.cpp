@@ -275,6 +275,37 @@ int validate(const muon_logits* l) {
   return MUON_OK;
 }
 
+// Few long rows: one workgroup a row leaves most CUs idle, so each row is split until there
+// are about as many workgroups as CUs, with at least kMinPart vectors (16 bytes) a part. It
+// costs a launch, so it is for rows of kMinSplit columns or more: 16 rows of 152064 bf16
+// columns take 25.8 us unsplit and 9.8 us (4.1 + 5.7) split, but 77 rows of 32003 fp32 columns
+// 10.5 us unsplit and 13.8 us split.
+constexpr int kMinPart = 1024;
+constexpr int64_t kMinSplit = 98304;
+struct LossSplit {
+  int splits = 1, part = 0;
+  size_t stats = 0, bytes = 0;   // bytes of the parts' statistics; workspace in all
+};
+LossSplit split_of(const muon_logits* l, int own_per_row, int cus) {
+  LossSplit s;
+  const int64_t vectors = l->vocab * size_of(l->dtype) / 16;
+  if (l->rows == 0 || 2 * l->rows > cus || l->vocab < kMinSplit || !(l->dlogits || !l->lse_given)) return s;
+  const int64_t want = std::min<int64_t>({cus / l->rows, vectors / kMinPart, 64});
+  if (want < 2) return s;
+  s.part = static_cast<int>(cdiv(vectors, want));
+  s.splits = static_cast<int>(cdiv(vectors, s.part));
+  if (s.splits < 2) { s.splits = 1; return s; }
+  s.stats = align_up(static_cast<size_t>(l->rows) * s.splits * 8);
+  s.bytes = s.stats + align_up(static_cast<size_t>(l->rows) * own_per_row * 4);
+  return s;
+}
+void apply(const LossSplit& s, LossParams& p, void* ws) {
+  p.splits = s.splits;
+  p.part = s.part;
+  p.stats = static_cast<float*>(ws);
+  p.own = s.splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(ws) + s.stats) : nullptr;
+}
+
 LossParams params(const muon_logits* l) {
   LossParams p;
   std::memset(&p, 0, sizeof(p));
@@ -433,7 +464,19 @@ int muon_ffn_backward(muon_ctx* ctx, const muon_ffn* f, const muon_ffn_grads* g,
   }
 }
 
-int muon_policy_loss(muon_ctx* ctx, const muon_logits* l, const muon_policy* t, void* stream) {
+int muon_loss_workspace_size(muon_ctx* ctx, const muon_logits* l, int top, size_t* bytes) {
+  try {
+    if (!ctx || !l || !bytes || !dtype_ok(l->dtype) || l->rows < 0 || l->vocab < 1 || top < 0 || top > MUON_MAX_TOP)
+      return MUON_ERR_ARG;
+    *bytes = split_of(l, top > 0 ? top : 1, ctx_cus(ctx)).bytes;
+    return MUON_OK;
+  } catch (...) {
+    return MUON_ERR_HIP;
+  }
+}
+
+int muon_policy_loss(muon_ctx* ctx, const muon_logits* l, const muon_policy* t, void* workspace, size_t workspace_bytes,
+                     void* stream) {
   try {
     if (!ctx || !t) return MUON_ERR_ARG;
     const int rc = validate(l);
@@ -444,10 +487,14 @@ int muon_policy_loss(muon_ctx* ctx, const muon_logits* l, const muon_policy* t, 
     if (t->kl_coef != 0.0f && l->rows > 0 && !t->ref_logp) return MUON_ERR_ARG;
     if (l->rows > 0 && (!t->targets || !t->old_logp || !t->advantages)) return MUON_ERR_ARG;
     if (l->rows == 0) return MUON_OK;
+    const LossSplit s = split_of(l, 1, ctx_cus(ctx));
+    const int wrc = check_workspace(workspace, workspace_bytes, s.bytes);
+    if (wrc != MUON_OK) return wrc;
     if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
     DeviceGuard dg(ctx_device(ctx));
     if (!dg.ok) return MUON_ERR_HIP;
     LossParams p = params(l);
+    apply(s, p, workspace);
     p.targets = t->targets;
     p.old_logp = t->old_logp; p.advantages = t->advantages;
     p.ref_logp = t->kl_coef != 0.0f ? t->ref_logp : nullptr;
@@ -460,7 +507,8 @@ int muon_policy_loss(muon_ctx* ctx, const muon_logits* l, const muon_policy* t, 
   }
 }
 
-int muon_distill_loss(muon_ctx* ctx, const muon_logits* l, const muon_distill* t, void* stream) {
+int muon_distill_loss(muon_ctx* ctx, const muon_logits* l, const muon_distill* t, void* workspace,
+                      size_t workspace_bytes, void* stream) {
   try {
     if (!ctx || !t) return MUON_ERR_ARG;
     const int rc = validate(l);
@@ -469,10 +517,14 @@ int muon_distill_loss(muon_ctx* ctx, const muon_logits* l, const muon_distill* t
     if (!dtype_ok(t->top_dtype) || (t->id_dtype != MUON_I32 && t->id_dtype != MUON_I64)) return MUON_ERR_ARG;
     if (l->rows > 0 && (!t->top_logits || !t->top_ids)) return MUON_ERR_ARG;
     if (l->rows == 0) return MUON_OK;
+    const LossSplit s = split_of(l, t->top, ctx_cus(ctx));
+    const int wrc = check_workspace(workspace, workspace_bytes, s.bytes);
+    if (wrc != MUON_OK) return wrc;
     if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
     DeviceGuard dg(ctx_device(ctx));
     if (!dg.ok) return MUON_ERR_HIP;
     LossParams p = params(l);
+    apply(s, p, workspace);
     p.top_logits = t->top_logits; p.ld_top = t->ld_top;
     p.ids = t->top_ids; p.ld_ids = t->ld_ids;
     p.top_lse = t->top_lse;

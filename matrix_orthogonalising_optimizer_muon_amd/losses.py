@@ -72,6 +72,13 @@ def _distill(z, device, top_logits, top_ids, top_lse):
     return t, (t2, i2)
 
 
+def _call(entry, name, device, l, t, top):
+    ctx = context(device)
+    nbytes = B.muon_loss_workspace_size(ctx, l, top)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    B.check(entry(ctx, l, t, ws.data_ptr() if nbytes else None, nbytes, stream_of(device)), name)
+
+
 def policy_loss(logits, targets, old_logp, advantages, *, ref_logp=None, weights=None, clip_low: float = 0.2,
                 clip_high: float = 0.2, kl_coef: float = 0.0, temperature: float = 1.0, grad: bool = True, out=None):
     """(loss, logp, grad): the rows' weighted losses
@@ -86,7 +93,7 @@ def policy_loss(logits, targets, old_logp, advantages, *, ref_logp=None, weights
         out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     l, z, device = _rows(logits, weights, temperature, out if grad else None, loss)
     t = _policy(z, device, targets, old_logp, advantages, ref_logp, clip_low, clip_high, kl_coef, logp)
-    B.check(B.muon_policy_loss(context(device), l, t, stream_of(device)), "muon_policy_loss")
+    _call(B.muon_policy_loss, "muon_policy_loss", device, l, t, 0)
     return loss, logp, out if grad else None
 
 
@@ -102,7 +109,7 @@ def distill_loss(logits, top_logits, top_ids, *, top_lse=None, weights=None, tem
         out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     l, z, device = _rows(logits, weights, temperature, out if grad else None, loss)
     t, keep = _distill(z, device, top_logits, top_ids, top_lse)
-    B.check(B.muon_distill_loss(context(device), l, t, stream_of(device)), "muon_distill_loss")
+    _call(B.muon_distill_loss, "muon_distill_loss", device, l, t, t.top)
     return loss, out if grad else None
 
 
@@ -113,7 +120,7 @@ class _PolicyLoss(torch.autograd.Function):
         loss, logp, lse = new(), new(), new()
         l, z, device = _rows(logits, weights, temperature, None, loss, lse)
         t = _policy(z, device, targets, old_logp, advantages, ref_logp, clip_low, clip_high, kl_coef, logp)
-        B.check(B.muon_policy_loss(context(device), l, t, stream_of(device)), "muon_policy_loss")
+        _call(B.muon_policy_loss, "muon_policy_loss", device, l, t, 0)
         ctx.save_for_backward(logits, targets, old_logp, advantages, ref_logp, weights, lse)
         ctx.numbers = (clip_low, clip_high, kl_coef, temperature)
         ctx.mark_non_differentiable(logp)
@@ -128,7 +135,7 @@ class _PolicyLoss(torch.autograd.Function):
         up = grad_loss.contiguous()
         l, z, device = _rows(logits, weights, temperature, out, None, lse, True, up)
         t = _policy(z, device, targets, old_logp, advantages, ref_logp, clip_low, clip_high, kl_coef, None)
-        B.check(B.muon_policy_loss(context(device), l, t, stream_of(device)), "muon_policy_loss")
+        _call(B.muon_policy_loss, "muon_policy_loss", device, l, t, 0)
         return (out,) + (None,) * 9
 
 
@@ -146,7 +153,7 @@ class _DistillLoss(torch.autograd.Function):
         loss, lse = new(), new()
         l, z, device = _rows(logits, weights, temperature, None, loss, lse)
         t, keep = _distill(z, device, top_logits, top_ids, top_lse)
-        B.check(B.muon_distill_loss(context(device), l, t, stream_of(device)), "muon_distill_loss")
+        _call(B.muon_distill_loss, "muon_distill_loss", device, l, t, t.top)
         ctx.save_for_backward(logits, top_logits, top_ids, top_lse, weights, lse)
         ctx.temperature = temperature
         return loss
@@ -159,7 +166,7 @@ class _DistillLoss(torch.autograd.Function):
         up = grad_loss.contiguous()
         l, z, device = _rows(logits, weights, ctx.temperature, out, None, lse, True, up)
         t, keep = _distill(z, device, top_logits, top_ids, top_lse)
-        B.check(B.muon_distill_loss(context(device), l, t, stream_of(device)), "muon_distill_loss")
+        _call(B.muon_distill_loss, "muon_distill_loss", device, l, t, t.top)
         return (out,) + (None,) * 5
 
 

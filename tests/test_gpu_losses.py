@@ -252,6 +252,33 @@ def test_distill_rows_that_take_no_part(S, dtype):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,V", [(1, 152064), (2, 98304), (16, 120001), (70, 98311), (128, 99991), (1, 1000003), (77, 32003)])
+def test_few_rows_equal_many(S, n, V, dtype):
+    """The parts of few long rows against the oracle on some rows, and in place."""
+    ins = policy_inputs(n, V, dtype)
+    z, t, old, adv, ref = ins
+    w = torch.linspace(0.0, 1.5, n, device="cuda") if n > 2 else None
+    loss, logp, grad = S.policy_loss(z, t, old, adv, weights=w)
+    inplace = z.clone()
+    again = S.policy_loss(inplace, t, old, adv, weights=w, out=inplace)
+    assert all(torch.equal(a, b) for a, b in zip((loss, logp, grad), again))
+    pick = [0, n // 2, n - 1]
+    opt = lambda a: None if a is None else to_np(a[pick])  # noqa: E731
+    want = ol.policy(to_np(z[pick]), t.cpu().numpy()[pick], to_np(old[pick]), to_np(adv[pick]), None, opt(w), clip_low=0.2,
+                     clip_high=0.2, kl_coef=0.0, temperature=1.0, half_step=HALF_STEP[dtype])
+    inside(loss[pick], want["loss"], want["err_loss"], "loss")
+    inside(grad[pick], want["grad"], want["err_grad"], "grad")
+    zd, top, ids = distill_inputs(n, V, 300, dtype)
+    ids[:, 10:20] = ids[:, :10]     # repeated
+    ids[0, 30] = V - 1              # behind the last whole vector
+    loss, grad = S.distill_loss(zd, top, ids, weights=w, temperature=2.0)
+    want = ol.distill(to_np(zd[pick]), to_np(top[pick]), ids.cpu().numpy()[pick], None, opt(w), temperature=2.0,
+                      half_step=HALF_STEP[dtype])
+    inside(loss[pick], want["loss"], want["err_loss"], "loss")
+    inside(grad[pick], want["grad"], want["err_grad"], "grad")
+
+
 def test_losses_offsets_past_32_bits(S):
     """Rows a wide stride apart: element offsets past 2^32."""
     n, V, ld = 4200, 130, 1 << 20   # 8.8 GB of buffer

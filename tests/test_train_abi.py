@@ -149,7 +149,7 @@ BAD_LOGITS = [dict(logits=None), dict(rows=-1), dict(vocab=0), dict(vocab=(1 << 
 
 
 def test_policy_validation(hctx):
-    call = lambda l, t: B.muon_policy_loss(hctx, l, t, None)  # noqa: E731
+    call = lambda l, t, ws=None, n=0: B.muon_policy_loss(hctx, l, t, ws, n, None)  # noqa: E731
     assert call(logits(), policy()) == B.MUON_ERR_DEVICE
     assert call(logits(dlogits=None, ld_d=0), policy(kl_coef=0.0, ref_logp=None)) == B.MUON_ERR_DEVICE
     assert call(logits(rows=0, logits=None), policy(targets=None)) == B.MUON_OK
@@ -158,13 +158,23 @@ def test_policy_validation(hctx):
     for bad in [dict(targets=None), dict(old_logp=None), dict(advantages=None), dict(ref_logp=None), dict(clip_low=-0.1),
                 dict(clip_low=1.1), dict(clip_high=-0.1), dict(clip_high=float("nan")), dict(kl_coef=float("inf"))]:
         assert call(logits(), policy(**bad)) == B.MUON_ERR_ARG, bad
-    assert B._lib.muon_policy_loss(None, logits(), policy(), None) == B.MUON_ERR_ARG
-    assert B._lib.muon_policy_loss(hctx, None, policy(), None) == B.MUON_ERR_ARG
-    assert B._lib.muon_policy_loss(hctx, logits(), None, None) == B.MUON_ERR_ARG
+    assert B._lib.muon_policy_loss(None, logits(), policy(), None, 0, None) == B.MUON_ERR_ARG
+    assert B._lib.muon_policy_loss(hctx, None, policy(), None, 0, None) == B.MUON_ERR_ARG
+    assert B._lib.muon_policy_loss(hctx, logits(), None, None, 0, None) == B.MUON_ERR_ARG
+    few = logits(rows=3, vocab=152064, ld=152064, ld_d=152064)
+    need = B.muon_loss_workspace_size(hctx, few)
+    assert need > 0 and need % 256 == 0
+    assert call(few, policy(), FAKE, need) == B.MUON_ERR_DEVICE
+    assert call(few, policy(), FAKE, need - 1) == B.MUON_ERR_WORKSPACE
+    assert call(few, policy(), FAKE + 128, need) == B.MUON_ERR_WORKSPACE
+    assert call(few, policy()) == B.MUON_ERR_WORKSPACE
+    # many rows, short rows, or rows that are not read as a whole need none
+    for kw in [dict(rows=200), dict(vocab=4096), dict(dlogits=None, lse_given=1)]:
+        assert B.muon_loss_workspace_size(hctx, logits(**dict(dict(rows=3, vocab=152064, ld=152064, ld_d=152064), **kw))) == 0
 
 
 def test_distill_validation(hctx):
-    call = lambda l, t: B.muon_distill_loss(hctx, l, t, None)  # noqa: E731
+    call = lambda l, t, ws=None, n=0: B.muon_distill_loss(hctx, l, t, ws, n, None)  # noqa: E731
     assert call(logits(), distill()) == B.MUON_ERR_DEVICE
     assert call(logits(rows=0, logits=None), distill(top_logits=None)) == B.MUON_OK
     for bad in BAD_LOGITS:
@@ -172,7 +182,17 @@ def test_distill_validation(hctx):
     for bad in [dict(top=0), dict(top=B.MUON_MAX_TOP + 1, ld_top=2000, ld_ids=2000), dict(ld_top=3), dict(ld_ids=3),
                 dict(top_dtype=2), dict(id_dtype=1), dict(top_logits=None), dict(top_ids=None)]:
         assert call(logits(), distill(**bad)) == B.MUON_ERR_ARG, bad
-    assert B._lib.muon_distill_loss(hctx, logits(), None, None) == B.MUON_ERR_ARG
+    assert B._lib.muon_distill_loss(hctx, logits(), None, None, 0, None) == B.MUON_ERR_ARG
+    few = logits(rows=3, vocab=152064, ld=152064, ld_d=152064)
+    need = B.muon_loss_workspace_size(hctx, few, 64)
+    assert need > B.muon_loss_workspace_size(hctx, few, 4)
+    t = distill(top=64, ld_top=64, ld_ids=64)
+    assert call(few, t, FAKE, need) == B.MUON_ERR_DEVICE
+    assert call(few, t, FAKE, need - 1) == B.MUON_ERR_WORKSPACE
+    n = ctypes.c_size_t()
+    for l, top in [(None, 0), (few, -1), (few, B.MUON_MAX_TOP + 1), (logits(dtype=3), 0), (logits(vocab=0), 0)]:
+        assert B._lib.muon_loss_workspace_size(hctx, l, top, n) == B.MUON_ERR_ARG
+    assert B._lib.muon_loss_workspace_size(hctx, few, 0, None) == B.MUON_ERR_ARG
 
 
 def test_python_refusals():
