@@ -84,30 +84,58 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
   return {m, a.s * __builtin_amdgcn_exp2f((a.m - at) * c) + b.s * __builtin_amdgcn_exp2f((b.m - at) * c)};
 }
 
-// Joined over the workgroup, in a fixed order; every thread receives the result.
+// Reductions over 16 lanes by lane permutes within the vector instruction (neighbours,
+// pairs, halves of 8, halves of 16; every lane ends with the result), the rest of a wave by
+// two shuffles.
+template <int CTRL>
+__device__ __forceinline__ float permuted(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float max16(float v) {
+  v = fmaxf(v, permuted<0xB1>(v));   // lanes 1 0 3 2
+  v = fmaxf(v, permuted<0x4E>(v));   // lanes 2 3 0 1
+  v = fmaxf(v, permuted<0x141>(v));  // mirrored in 8
+  return fmaxf(v, permuted<0x140>(v));  // mirrored in 16
+}
+__device__ __forceinline__ float sum16(float v) {
+  v += permuted<0xB1>(v);
+  v += permuted<0x4E>(v);
+  v += permuted<0x141>(v);
+  return v + permuted<0x140>(v);
+}
+__device__ __forceinline__ float max64(float v) {
+  v = max16(v);
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float sum64(float v) {
+  v = sum16(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// Joined over the workgroup, in a fixed order; every thread receives the result. The maximum
+// first, then one rescale and the sum (joining pairs of statistics step by step took 1.4 us
+// of a row's 34). `lds`: at least 16 entries that this call alone uses, so that one barrier
+// is enough.
 template <int THREADS>
 __device__ __forceinline__ Stat join_all(Stat v, float c, Stat* lds) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = join(v, Stat{__shfl_xor(v.m, d), __shfl_xor(v.s, d)}, c);
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  const int lane = threadIdx.x & 63;
+  float m = max64(v.m);
+  const float s = sum64(v.s * __builtin_amdgcn_exp2f((v.m - base_of(m)) * c));
+  if (lane == 0) lds[threadIdx.x >> 6] = Stat{m, s};
   __syncthreads();
-  v = lds[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / 64; ++w) v = join(v, lds[w], c);
-  __syncthreads();
-  return v;
+  const Stat x = (lane & 15) < THREADS / 64 ? lds[lane & 15] : Stat{-INFINITY, 0.0f};
+  m = max16(x.m);
+  return {m, sum16(x.s * __builtin_amdgcn_exp2f((x.m - base_of(m)) * c))};
 }
 template <int THREADS>
 __device__ __forceinline__ float sum_all(float v, float* lds) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  const int lane = threadIdx.x & 63;
+  v = sum64(v);
+  if (lane == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
-  v = 0.0f;
-#pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) v += lds[w];
-  __syncthreads();
-  return v;
+  return sum16((lane & 15) < THREADS / 64 ? lds[lane & 15] : 0.0f);
 }
 
 // exp(d) - 1 without cancellation: the series for small d (next term d^6 / 720 below
@@ -119,8 +147,8 @@ __device__ __forceinline__ float expm1_f(float d) {
 }
 
 struct Shared {
-  Stat stat[16];
-  float sum[16];
+  Stat row[16], teacher[16];
+  float mass[16], loss[16];
 };
 
 // Few long rows: every row is split into p.splits parts of p.part vectors, one workgroup
@@ -130,7 +158,7 @@ struct Shared {
 template <typename E, int LOSS, int THREADS>
 __global__ __launch_bounds__(THREADS) void loss_parts(const LossParams p) {
   using R = Row<E>;
-  __shared__ Stat lds[THREADS / 64];
+  __shared__ Stat lds[16];
   const int tid = threadIdx.x;
   const int64_t r = blockIdx.x / p.splits;
   const int part = blockIdx.x - static_cast<int>(r) * p.splits;
@@ -295,15 +323,16 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
       Stat st{-INFINITY, 0.0f};
 #pragma unroll
       for (int k = 0; k < KT; ++k) st = join(st, Stat{tt[k], tt[k] == -INFINITY ? 0.0f : 1.0f}, c);
-      st = join_all<THREADS>(st, c, sh.stat);
+      st = join_all<THREADS>(st, c, sh.teacher);
       tm = base_of(st.m);
       tlog2 = __builtin_amdgcn_logf(st.s);
+      mass = st.s > 0.0f ? 1.0f : st.s;  // normalised among themselves; 0: no entries; NaN stays
     }
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
       const float lp = (tt[k] - tm) * c - tlog2;
       const float pk = tt[k] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lp);
-      mass += pk;
+      if (p.top_lse) mass += pk;
       const int j = k * THREADS + tid;
       if (j < kMaxTop) {
         col[j] = tc[k];
@@ -311,7 +340,8 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
         lp_of[j] = lp;
       }
     }
-    mass = sum_all<THREADS>(mass, sh.sum);
+    if (p.top_lse) mass = sum_all<THREADS>(mass, sh.mass);
+    else __syncthreads();
     // A column that occurs more than once: its first entry carries the sum, the others nothing.
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
@@ -351,9 +381,8 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     const int lane = tid & 63;
     Stat st{-INFINITY, 0.0f};
     if (lane < p.splits) st = Stat{p.stats[(r * p.splits + lane) * 2], p.stats[(r * p.splits + lane) * 2 + 1]};
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) st = join(st, Stat{__shfl_xor(st.m, o), __shfl_xor(st.s, o)}, c);
-    m = st.m;
+    m = max64(st.m);
+    st.s = sum64(st.s * __builtin_amdgcn_exp2f((st.m - base_of(m)) * c));
     log2s = __builtin_amdgcn_logf(st.s);
     inv_s = 1.0f / st.s;
     if (first && p.lse) p.lse[r] = m * p.inv_temperature + log2s * kLn2;
@@ -396,7 +425,7 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
       }
     }
     if (tail < V) st = join(st, Stat{zl, zl == zl ? 1.0f : zl}, c);
-    st = join_all<THREADS>(st, c, sh.stat);
+    st = join_all<THREADS>(st, c, sh.row);
     m = st.m;
     log2s = __builtin_amdgcn_logf(st.s);
     inv_s = 1.0f / st.s;
@@ -448,7 +477,7 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     if (!p.loss || part != 0) return;
     float loss = 0.0f;
     for (int j = tid; j < p.top; j += THREADS) loss += p_of[j];
-    loss = sum_all<THREADS>(loss, sh.sum);
+    loss = sum_all<THREADS>(loss, sh.loss);
     if (tid == 0) p.loss[r] = loss * kLn2 * w;
   };
   if (!d) {
