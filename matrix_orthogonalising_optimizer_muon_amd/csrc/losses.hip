@@ -499,11 +499,6 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     R::unpack(vec, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] = cq * __builtin_amdgcn_exp2f((v[e] - m) * c - shift);
-    if constexpr (LOSS == LOSS_POLICY) {
-      const int off = static_cast<int>(target) - i * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = off == e ? v[e] - coef : v[e];
-    }
     R::store(d + at, v);
   };
   if constexpr (NV > 0) {
@@ -519,8 +514,15 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
   }
   if (tail < V) {
     float v = cq * __builtin_amdgcn_exp2f((zl - m) * c - shift);
-    if (LOSS == LOSS_POLICY && tail == target) v -= coef;
     d[tail] = R::to(v);
+  }
+  if constexpr (LOSS == LOSS_POLICY) {
+    // The target's column again, by the thread that wrote it above: its stores to one address
+    // stay in order (a comparison per element instead took 2 of about 17 instructions).
+    const int v = static_cast<int>(target) / VEC;
+    const int owner = v >= full ? static_cast<int>(target) - full * VEC : (v - v0) % THREADS;
+    if (v >= v0 && (last_part || v < v1) && tid == owner)
+      d[target] = R::to(cq * __builtin_amdgcn_exp2f((zt - m) * c - shift) - coef);
   }
   if constexpr (LOSS == LOSS_DISTILL) {
     // The kept columns again, with the teacher's part, by the thread that wrote them above:
