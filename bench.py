@@ -57,6 +57,11 @@ def parse():
     ap.add_argument("--adamw", action="store_true",
                     help="also time the AdamW step over the 7B shape set's non-matrix parameters "
                          "(embedding, head, biases, norms; fp32 W / m / v, bf16 G)")
+    ap.add_argument("--ffn-tokens", type=int, default=0,
+                    help="also time what comes before the update for one layer of the primary workload: the "
+                         "feed-forward block's forward and backward over this many tokens, the weight "
+                         "gradients written into the layer's gate / up / down G arrays, then the Muon step "
+                         "of those three matrices (workloads with gate, up and down matrices)")
     ap.add_argument("--tune-cache", default=None,
                     help="tile-choice file: loaded before the warmup when it exists, written after "
                          "it (so that separate profiling runs use the same kernels)")
@@ -175,6 +180,51 @@ def traffic_record(workload):
     if rec.get("source_sha256") != h.hexdigest():
         return None
     return rec
+
+
+def ffn_bench(B, ctx, torch, args, w):
+    """One layer's feed-forward block before its update: forward, backward into the G arrays
+    of the layer's gate, up and down matrices (bf16), muon_step of the three; per-stage ms."""
+    from matrix_orthogonalising_optimizer_muon_amd import layers
+    from matrix_orthogonalising_optimizer_muon_amd import workloads as wl
+    spec = {m.name.split(".")[-1]: m for m in w.matrices[:7]}
+    if not {"gate", "up", "down"} <= set(spec):
+        raise SystemExit(f"--ffn-tokens: {w.name} has no gate, up and down matrices")
+    ids = [i for i, m in enumerate(w.matrices[:7]) if m.name.split(".")[-1] in ("gate", "up", "down")]
+    W = [wl.weight_torch(w, i, "cuda") for i in ids]
+    W16 = [t.to(torch.bfloat16) for t in W]
+    G = [torch.zeros_like(t) for t in W16]
+    M = [torch.zeros_like(t) for t in W16]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(11)
+    T, D = args.ffn_tokens, spec["gate"].cols
+    x, dy = (torch.randn(T, D, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    hp = B.make_hparams(lr=w.lr, momentum=w.mu, weight_decay=w.wd, mode=args.mode)
+    mats = list(zip(W, G, M))
+    nbytes = B.muon_workspace_size(ctx, mats, hp)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    stages = ("forward", "backward", "update")
+    total = dict.fromkeys(stages, 0.0)
+    for t in range(args.warmup + args.steps):
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(4)]
+        ev[0].record()
+        _, saved = layers.ffn_forward(x, *W16, save=True)
+        ev[1].record()
+        layers.ffn_backward(dy, x, *W16, saved, grads=G)
+        ev[2].record()
+        B.check(B.muon_step(ctx, mats, hp, ws.data_ptr(), nbytes), "muon_step")
+        ev[3].record()
+        torch.cuda.synchronize()
+        if t >= args.warmup:
+            for k, name in enumerate(stages):
+                total[name] += ev[k].elapsed_time(ev[k + 1])
+    ms = {k: v / args.steps for k, v in total.items()}
+    flops = 2.0 * T * sum(t.numel() for t in W)
+    out = {"tokens": T, "shape": [spec["gate"].rows, D], **{f"{k}_ms": round(v, 4) for k, v in ms.items()},
+           "forward_tflops": round(flops / ms["forward"] / 1e9, 1),
+           "backward_tflops": round(2 * flops / ms["backward"] / 1e9, 1)}
+    print(f"[bench] feed-forward block: {out}", file=sys.stderr, flush=True)
+    return out
 
 
 def adamw_bench(B, ctx, torch, args):
@@ -457,6 +507,8 @@ def main():
         out["cpu_baseline"] = cpu_baseline(w, args.cpu_budget_s)
     if args.adamw:
         out["adamw_companion"] = adamw_bench(B, ctx, torch, args)
+    if args.ffn_tokens:
+        out["feed_forward"] = ffn_bench(B, ctx, torch, args, w)
     B.muon_destroy(ctx)
     B.muon_destroy(pctx)
     print(json.dumps(out), flush=True)

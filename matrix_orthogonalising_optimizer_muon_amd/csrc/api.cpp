@@ -23,6 +23,7 @@
 #include <tuple>
 #include <vector>
 
+#include "frontend.hpp"
 #include "internal.hpp"
 
 // Stage profiler: with MUON_FLAG_PROFILE every launch is bracketed by a pair of

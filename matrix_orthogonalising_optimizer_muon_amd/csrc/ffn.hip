@@ -27,8 +27,8 @@
 #include <type_traits>
 #include <utility>
 
-#include "internal.hpp"
 #include "mfma_util.hpp"
+#include "train.hpp"
 
 namespace muon {
 namespace {

@@ -16,8 +16,8 @@
 // difference, so that rows of the type's lowest values stay exact, and q = e / s.
 #include <type_traits>
 
-#include "internal.hpp"
 #include "mfma_util.hpp"
+#include "train.hpp"
 
 namespace muon {
 namespace {

@@ -1,5 +1,6 @@
-// Device helpers shared by the MFMA kernels (gemm.hip, ffn.hip): vector types, LDS chunk
-// swizzle, counter waits and the direct global -> LDS loads of gfx950.
+// Device helpers of the training operators' kernels (ffn.hip, losses.hip): vector types, LDS
+// chunk swizzle, counter waits and the direct global -> LDS loads of gfx950. gemm.hip keeps
+// its own copies: the HBM traffic records of its profiles are tied to that file's contents.
 #pragma once
 
 #include "internal.hpp"

@@ -11,7 +11,8 @@
 #include <cstring>
 #include <initializer_list>
 
-#include "internal.hpp"
+#include "frontend.hpp"
+#include "train.hpp"
 
 namespace muon {
 namespace {
