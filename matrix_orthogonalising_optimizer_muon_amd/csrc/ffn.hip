@@ -207,25 +207,40 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
   const int kgrp = wave / NWC, wloc = wave % NWC;
 
   // Workgroups are dealt round-robin to the 8 XCDs: give each XCD a contiguous run of the
-  // logical sequence, walked in groups of 8 tile rows, so that neighbours share panels in
-  // its L2.
-  int tm, tn, z;
+  // logical sequence (split, problem, tile), tiles walked in groups of 8 tile rows, so that
+  // neighbours share panels in its L2.
+  const void* A = p.A;
+  const void* B = p.B[0];
+  void* C = p.C[0];
+  int64_t lda = p.lda, ldb = p.ldb, ldc = p.ldc, part0 = 0;
+  int M = p.M, N = p.N, tiles_m = p.tiles_m, tiles_n = p.tiles_n;
+  int tm, tn, split;
   {
     const int i = blockIdx.x, nwg = gridDim.x;
     const int xcd = i & 7, q = nwg >> 3, r = nwg & 7;
     int t = xcd * q + min(xcd, r) + (i >> 3);
-    z = t / p.tiles;
-    t -= z * p.tiles;
+    split = t / p.tiles;
+    t -= split * p.tiles;
+    if constexpr (AS && BS) {
+      int k = 0;
+      while (k + 1 < p.problems && t >= p.problem[k].tiles_m * p.problem[k].tiles_n) {
+        t -= p.problem[k].tiles_m * p.problem[k].tiles_n;
+        ++k;
+      }
+      const FfnProblem& o = p.problem[k];
+      A = o.A; B = o.B; C = o.C;
+      lda = o.lda; ldb = o.ldb; ldc = o.ldc; part0 = o.part0;
+      M = o.M; N = o.N; tiles_m = o.tiles_m; tiles_n = o.tiles_n;
+    }
     constexpr int GM = 8;
-    const int group = GM * p.tiles_n;
+    const int group = GM * tiles_n;
     const int g = t / group;
     const int first = g * GM;
-    const int gm = min(p.tiles_m - first, GM);
+    const int gm = min(tiles_m - first, GM);
     const int r2 = t - g * group;
     tm = first + r2 % gm;
     tn = r2 / gm;
   }
-  const int batch = z / p.splits, split = z - batch * p.splits;
   const int m0 = tm * BM;
   const int n0 = DUAL ? tn * (BN / 2) : tn * BN;
 
@@ -241,10 +256,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
     const int at = (wave * IA + j) * 64 + lane;
     if constexpr (AS) {
       const int k = at / (BM / VEC);
-      a_off[j] = static_cast<uint32_t>((k * p.lda + swz_strided<KIND, BM>(k, at % (BM / VEC)) * VEC) * ES);
+      a_off[j] = static_cast<uint32_t>((k * lda + swz_strided<KIND, BM>(k, at % (BM / VEC)) * VEC) * ES);
     } else {
       const int row = at / CH;
-      a_off[j] = static_cast<uint32_t>((min(row, p.M - m0 - 1) * p.lda + ((at % CH) ^ swz_bits<CH>(row)) * VEC) * ES);
+      a_off[j] = static_cast<uint32_t>((min(row, M - m0 - 1) * lda + ((at % CH) ^ swz_bits<CH>(row)) * VEC) * ES);
     }
   }
 #pragma unroll
@@ -252,16 +267,16 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
     const int at = (wave * IB + j) * 64 + lane;
     if constexpr (BS) {
       const int k = at / (BN / VEC);
-      b_off[j] = static_cast<uint32_t>((k * p.ldb + swz_strided<KIND, BN>(k, at % (BN / VEC)) * VEC) * ES);
+      b_off[j] = static_cast<uint32_t>((k * ldb + swz_strided<KIND, BN>(k, at % (BN / VEC)) * VEC) * ES);
     } else {
       const int row = at / CH;
       const int c = ((at % CH) ^ swz_bits<CH>(row)) * VEC;
       if constexpr (DUAL) {
         // rows 16 t .. 16 t + 7 of the tile come from Wg, the next 8 from Wu (same columns of g and u)
-        const int f = min((row >> 4) * 8 + (row & 7), p.N - n0 - 1);
-        b_off[j] = static_cast<uint32_t>((f * ((row & 8) ? p.ldb1 : p.ldb) + c) * ES);
+        const int f = min((row >> 4) * 8 + (row & 7), N - n0 - 1);
+        b_off[j] = static_cast<uint32_t>((f * ((row & 8) ? p.ldb1 : ldb) + c) * ES);
       } else {
-        b_off[j] = static_cast<uint32_t>((min(row, p.N - n0 - 1) * p.ldb + c) * ES);
+        b_off[j] = static_cast<uint32_t>((min(row, N - n0 - 1) * ldb + c) * ES);
       }
     }
   }
@@ -270,27 +285,27 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
   // K-strided: a pointer, and how many rows are left. Slices are loaded in order, and up to
   // NS - 1 past the last one: those land in stages that are not read, and past an operand's
   // end they read zeros.
-  const char* a_ptr = static_cast<const char*>(p.A[p.batched ? batch : 0]);
-  const char* b_ptr = static_cast<const char*>(p.B[0]);
+  const char* a_ptr = static_cast<const char*>(A);
+  const char* b_ptr = static_cast<const char*>(B);
   int a_k = 0, b_k = 0;      // K-contiguous: byte offset
   int a_rows = 0, b_rows = 0;  // K-strided: rows left
   int seg_left = 0x7FFFFFFF;   // K-strided B in two segments: slices until the second
   if constexpr (AS) {
-    a_ptr += (static_cast<int64_t>(kt0) * BK * p.lda + m0) * ES;
+    a_ptr += (static_cast<int64_t>(kt0) * BK * lda + m0) * ES;
     a_rows = p.K - kt0 * BK;
   } else {
-    a_ptr += m0 * p.lda * ES;
+    a_ptr += m0 * lda * ES;
     a_k = kt0 * BK * ES;
   }
   if constexpr (BS) {
     const bool second = p.B[1] != nullptr && kt0 >= p.slices0;
     const int s = second ? kt0 - p.slices0 : kt0;
     b_ptr = second ? static_cast<const char*>(p.B[1]) : b_ptr;
-    b_ptr += (static_cast<int64_t>(s) * BK * p.ldb + n0) * ES;
+    b_ptr += (static_cast<int64_t>(s) * BK * ldb + n0) * ES;
     b_rows = p.K - s * BK;
     if (p.B[1] != nullptr && !second) seg_left = p.slices0 - kt0;
   } else {
-    b_ptr += n0 * p.ldb * ES;
+    b_ptr += n0 * ldb * ES;
     b_k = kt0 * BK * ES;
   }
   // Buffer bounds in bytes, rounded up to whole chunks: rows are 16-byte aligned, so such a
@@ -299,26 +314,26 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
     const int b = static_cast<int>(((rows - 1) * ld + last) * ES + 15) & ~15;
     return rows > 0 ? b : 0;
   };
-  const int a_bytes = AS ? 0 : bytes_of(min(p.M - m0, BM), p.lda, p.KA);
-  const int b_bytes = BS ? 0 : bytes_of(min(p.N - n0, DUAL ? BN / 2 : BN), p.ldb, p.K);
+  const int a_bytes = AS ? 0 : bytes_of(min(M - m0, BM), lda, p.KA);
+  const int b_bytes = BS ? 0 : bytes_of(min(N - n0, DUAL ? BN / 2 : BN), ldb, p.K);
   const auto rb1 = make_rsrc(DUAL ? static_cast<const char*>(p.B[1]) + n0 * p.ldb1 * ES : b_ptr,
-                             DUAL ? bytes_of(min(p.N - n0, BN / 2), p.ldb1, p.K) : 0);
+                             DUAL ? bytes_of(min(N - n0, BN / 2), p.ldb1, p.K) : 0);
 
   auto issue = [&](int stage) {
     u32x4* sa = lds + stage * STAGE + wave * IA * 64;
     u32x4* sb = lds + stage * STAGE + BM * CH + wave * IB * 64;
     {
-      const auto r = make_rsrc(a_ptr, AS ? bytes_of(min(a_rows, BK), p.lda, p.M - m0) : a_bytes);
+      const auto r = make_rsrc(a_ptr, AS ? bytes_of(min(a_rows, BK), lda, M - m0) : a_bytes);
 #pragma unroll
       for (int j = 0; j < IA; ++j) buf_load_lds(r, sa + j * 64, a_off[j], a_k);
       if constexpr (AS) {
-        a_ptr += static_cast<int64_t>(BK * ES) * p.lda;
+        a_ptr += static_cast<int64_t>(BK * ES) * lda;
         a_rows -= BK;
       } else {
         a_k += BK * ES;
       }
     }
-    const auto r = make_rsrc(b_ptr, BS ? bytes_of(min(b_rows, BK), p.ldb, p.N - n0) : b_bytes);
+    const auto r = make_rsrc(b_ptr, BS ? bytes_of(min(b_rows, BK), ldb, N - n0) : b_bytes);
     if constexpr (DUAL) {
 #pragma unroll
       for (int j = 0; j < IB; ++j) {
@@ -330,7 +345,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
       for (int j = 0; j < IB; ++j) buf_load_lds(r, sb + j * 64, b_off[j], b_k);
     }
     if constexpr (BS) {
-      b_ptr += static_cast<int64_t>(BK * ES) * p.ldb;
+      b_ptr += static_cast<int64_t>(BK * ES) * ldb;
       b_rows -= BK;
       if (--seg_left == 0) {
         b_ptr = static_cast<const char*>(p.B[1]) + static_cast<int64_t>(n0) * ES;
@@ -520,7 +535,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
     const int m = m0 + wm0 + i * 32 + (lane & 31);
     const int64_t mb = (m0 + wm0) / 32 + i;
     if constexpr (EPI == FFN_GATE) {
-      if (mb * 32 >= p.M) return;
+      if (mb * 32 >= M) return;
       // two blocks of 16 columns each make 32 columns of h where the wave has a pair
       constexpr int PAIR = FN % 2 == 0 ? 2 : 1;
       each<FN / PAIR>([&](auto j_tag) {
@@ -534,7 +549,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             // columns behind N, and the saved rows behind M, are padding: zero
-            const bool in = f + t * 8 + half * 4 + e < p.N && m < p.M;
+            const bool in = f + t * 8 + half * 4 + e < N && m < M;
             g[e] = in ? acc[i][j + t / 2][(t & 1) * 8 + e] : 0.0f;
             u[e] = in ? acc[i][j + t / 2][(t & 1) * 8 + 4 + e] : 0.0f;
             float a, slope;
@@ -551,11 +566,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
 #pragma unroll
           for (int e = 8; e < 16; ++e) h[e] = 0.0f;
         }
-        if (m < p.M)
-          store_block<KIND>(static_cast<char*>(p.C[0]) + (static_cast<int64_t>(m) * p.ldc + f) * ES, h, 16 * PAIR, half, false);
+        if (m < M)
+          store_block<KIND>(static_cast<char*>(C) + (static_cast<int64_t>(m) * ldc + f) * ES, h, 16 * PAIR, half, false);
       });
     } else if constexpr (EPI == FFN_DGATE) {
-      if (m >= p.M) return;
+      if (m >= M) return;
       f32x4 g[FN][4], u[FN][4];
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
@@ -577,33 +592,33 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float dh = f + q * 8 + half * 4 + e < p.N ? acc[i][j][q * 4 + e] : 0.0f;
+            const float dh = f + q * 8 + half * 4 + e < N ? acc[i][j][q * 4 + e] : 0.0f;
             float a, slope;
             activation(g[j][q][e], p.act, a, slope);
             du[q * 4 + e] = dh * a;
             dg[q * 4 + e] = dh * u[j][q][e] * slope;
             h[q * 4 + e] = a * u[j][q][e];
           }
-        const int64_t at = (static_cast<int64_t>(m) * p.ldc + f) * ES;
-        store_block<KIND>(static_cast<char*>(p.C[0]) + at, dg, 32, half, false);
+        const int64_t at = (static_cast<int64_t>(m) * ldc + f) * ES;
+        store_block<KIND>(static_cast<char*>(C) + at, dg, 32, half, false);
         store_block<KIND>(static_cast<char*>(p.C[1]) + at, du, 32, half, false);
         store_block<KIND>(static_cast<char*>(p.C[2]) + (static_cast<int64_t>(m) * p.Np + f) * ES, h, 32, half, false);
       });
     } else {
-      if (m >= p.M) return;
+      if (m >= M) return;
       each<FN>([&](auto j_tag) {
         constexpr int j = decltype(j_tag)::value;
         const int n = n0 + wn0 + j * 32;
-        if (n >= p.N) return;
+        if (n >= N) return;
         float v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e];
         if (p.part != nullptr)
-          store_block<KIND_F32>(p.part + (static_cast<int64_t>(z) * p.M + m) * p.Np + n, v, p.N - n, half, false);
+          store_block<KIND_F32>(p.part + split * p.part_split + part0 + static_cast<int64_t>(m) * ((N + 7) & ~7) + n, v, N - n, half, false);
         else if (p.c_bf16)
-          store_block<KIND_BF16>(static_cast<unsigned short*>(p.C[batch]) + static_cast<int64_t>(m) * p.ldc + n, v, p.N - n, half, p.accumulate);
+          store_block<KIND_BF16>(static_cast<unsigned short*>(C) + static_cast<int64_t>(m) * ldc + n, v, N - n, half, p.accumulate);
         else
-          store_block<KIND_F32>(static_cast<float*>(p.C[batch]) + static_cast<int64_t>(m) * p.ldc + n, v, p.N - n, half, p.accumulate);
+          store_block<KIND_F32>(static_cast<float*>(C) + static_cast<int64_t>(m) * ldc + n, v, N - n, half, p.accumulate);
       });
     }
   });
@@ -613,14 +628,26 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
 // 4 columns, up to 8 partials requested at a time. Bound by the reads of the partials
 // (splits x 4 bytes per element), or by their latency when there are few.
 __global__ __launch_bounds__(256) void ffn_join(const FfnGemm p, int64_t pieces) {
-  const int per_row = (p.N + 3) / 4;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t row = i / per_row;      // batch * M + m
-    const int n = static_cast<int>(i - row * per_row) * 4;
-    const int batch = row >= p.M ? 1 : 0;
-    const int64_t m = row - (batch ? p.M : 0);
-    const float* src = p.part + (static_cast<int64_t>(batch) * p.splits * p.M + m) * p.Np + n;
-    const int64_t step = static_cast<int64_t>(p.M) * p.Np;
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < pieces; at += static_cast<int64_t>(gridDim.x) * 256) {
+    void* C = p.C[0];
+    int64_t ldc = p.ldc, part0 = 0, i = at;
+    int N = p.N;
+    if (p.problems > 0) {
+      int k = 0;
+      while (k + 1 < p.problems && i >= static_cast<int64_t>(p.problem[k].M) * ((p.problem[k].N + 3) / 4)) {
+        i -= static_cast<int64_t>(p.problem[k].M) * ((p.problem[k].N + 3) / 4);
+        ++k;
+      }
+      C = p.problem[k].C;
+      ldc = p.problem[k].ldc;
+      part0 = p.problem[k].part0;
+      N = p.problem[k].N;
+    }
+    const int per_row = (N + 3) / 4;
+    const int64_t m = i / per_row;
+    const int n = static_cast<int>(i - m * per_row) * 4;
+    const float* src = p.part + part0 + m * ((N + 7) & ~7) + n;
+    const int64_t step = p.part_split;
     f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = 0; s < p.splits; s += 8) {
       f32x4 w[8];
@@ -630,9 +657,9 @@ __global__ __launch_bounds__(256) void ffn_join(const FfnGemm p, int64_t pieces)
       for (int k = 0; k < 8; ++k)
         if (s + k < p.splits) v += w[k];
     }
-    const int left = p.N - n;
+    const int left = N - n;
     if (p.c_bf16) {
-      unsigned short* c = static_cast<unsigned short*>(p.C[batch]) + m * p.ldc + n;
+      unsigned short* c = static_cast<unsigned short*>(C) + m * ldc + n;
       unsigned short out[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -648,7 +675,7 @@ __global__ __launch_bounds__(256) void ffn_join(const FfnGemm p, int64_t pieces)
           if (e < left) c[e] = out[e];
       }
     } else {
-      float* c = static_cast<float*>(p.C[batch]) + m * p.ldc + n;
+      float* c = static_cast<float*>(C) + m * ldc + n;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (e < left) c[e] = (p.accumulate ? c[e] : 0.0f) + v[e];
@@ -696,8 +723,8 @@ __global__ __launch_bounds__(256) void ffn_zero(void* out, int64_t ld, int64_t r
 }
 
 template <int KIND, int BM, int BN, int WM, int WN, int KS, int NS, int CH, bool AS, bool BS, int EPI>
-hipError_t launch(const FfnGemm& p, int batches, hipStream_t st) {
-  const int64_t grid = static_cast<int64_t>(p.tiles) * p.splits * batches;
+hipError_t launch(const FfnGemm& p, hipStream_t st) {
+  const int64_t grid = static_cast<int64_t>(p.tiles) * p.splits;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL((ffn_gemm<KIND, BM, BN, WM, WN, KS, NS, CH, AS, BS, EPI>), dim3(static_cast<unsigned int>(grid)),
                      dim3(64 * WM * WN * KS), 0, st, p);
@@ -705,41 +732,42 @@ hipError_t launch(const FfnGemm& p, int batches, hipStream_t st) {
 }
 
 template <int KIND, bool AS, bool BS, int EPI>
-hipError_t launch_tile(int tile, const FfnGemm& p, int batches, hipStream_t st) {
+hipError_t launch_tile(int tile, const FfnGemm& p, hipStream_t st) {
   switch (tile) {
-    case FFN_TILE_32: return launch<KIND, 32, 32, 1, 1, 4, 8, 8, AS, BS, EPI>(p, batches, st);
-    case FFN_TILE_64: return launch<KIND, 64, 64, 2, 2, 2, 4, 8, AS, BS, EPI>(p, batches, st);
-    case FFN_TILE_64x128: return launch<KIND, 64, 128, 2, 2, 1, 3, 8, AS, BS, EPI>(p, batches, st);
-    case FFN_TILE_128: return launch<KIND, 128, 128, 2, 2, 1, 4, 8, AS, BS, EPI>(p, batches, st);
+    case FFN_TILE_32: return launch<KIND, 32, 32, 1, 1, 4, 8, 8, AS, BS, EPI>(p, st);
+    case FFN_TILE_64: return launch<KIND, 64, 64, 2, 2, 2, 4, 8, AS, BS, EPI>(p, st);
+    case FFN_TILE_64x128: return launch<KIND, 64, 128, 2, 2, 1, 3, 8, AS, BS, EPI>(p, st);
+    case FFN_TILE_128: return launch<KIND, 128, 128, 2, 2, 1, 4, 8, AS, BS, EPI>(p, st);
     case FFN_TILE_128x256:
-      if constexpr (KIND != KIND_F32) return launch<KIND, 128, 256, 2, 4, 1, 3, 8, AS, BS, EPI>(p, batches, st);
+      if constexpr (KIND != KIND_F32) return launch<KIND, 128, 256, 2, 4, 1, 3, 8, AS, BS, EPI>(p, st);
       return hipErrorInvalidValue;
     case FFN_TILE_256:
-      if constexpr (KIND != KIND_F32) return launch<KIND, 256, 256, 2, 4, 1, 2, 8, AS, BS, EPI>(p, batches, st);
+      if constexpr (KIND != KIND_F32) return launch<KIND, 256, 256, 2, 4, 1, 2, 8, AS, BS, EPI>(p, st);
       return hipErrorInvalidValue;
   }
   return hipErrorInvalidValue;
 }
 
 template <int KIND>
-hipError_t launch_kind(FfnStage stage, int tile, const FfnGemm& p, int batches, hipStream_t st) {
+hipError_t launch_kind(FfnStage stage, int tile, const FfnGemm& p, hipStream_t st) {
   switch (stage) {
-    case FFN_STAGE_GATE: return launch_tile<KIND, false, false, FFN_GATE>(tile, p, batches, st);
-    case FFN_STAGE_DOWN: return launch_tile<KIND, false, false, FFN_STORE>(tile, p, batches, st);
-    case FFN_STAGE_DGATE: return launch_tile<KIND, false, true, FFN_DGATE>(tile, p, batches, st);
-    case FFN_STAGE_DX: return launch_tile<KIND, false, true, FFN_STORE>(tile, p, batches, st);
-    case FFN_STAGE_DW: return launch_tile<KIND, true, true, FFN_STORE>(tile, p, batches, st);
+    case FFN_STAGE_GATE: return launch_tile<KIND, false, false, FFN_GATE>(tile, p, st);
+    case FFN_STAGE_DOWN: return launch_tile<KIND, false, false, FFN_STORE>(tile, p, st);
+    case FFN_STAGE_DGATE: return launch_tile<KIND, false, true, FFN_DGATE>(tile, p, st);
+    case FFN_STAGE_DX: return launch_tile<KIND, false, true, FFN_STORE>(tile, p, st);
+    case FFN_STAGE_DW: return launch_tile<KIND, true, true, FFN_STORE>(tile, p, st);
   }
   return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_ffn(FfnStage stage, bool f32, int tile, const FfnGemm& p, int batches, hipStream_t st) {
-  hipError_t e = f32 ? launch_kind<KIND_F32>(stage, tile, p, batches, st)
-                     : launch_kind<KIND_BF16>(stage, tile, p, batches, st);
+hipError_t launch_ffn(FfnStage stage, bool f32, int tile, const FfnGemm& p, hipStream_t st) {
+  hipError_t e = f32 ? launch_kind<KIND_F32>(stage, tile, p, st)
+                     : launch_kind<KIND_BF16>(stage, tile, p, st);
   if (e != hipSuccess || p.part == nullptr) return e;
-  const int64_t pieces = static_cast<int64_t>(batches) * p.M * ((p.N + 3) / 4);
+  int64_t pieces = p.problems > 0 ? 0 : static_cast<int64_t>(p.M) * ((p.N + 3) / 4);
+  for (int k = 0; k < p.problems; ++k) pieces += static_cast<int64_t>(p.problem[k].M) * ((p.problem[k].N + 3) / 4);
   const int64_t blocks = (pieces + 255) / 256;
   hipLaunchKernelGGL(ffn_join, dim3(static_cast<unsigned int>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, p, pieces);
   return hipGetLastError();

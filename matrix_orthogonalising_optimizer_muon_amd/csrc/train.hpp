@@ -25,8 +25,18 @@ enum FfnTile : int {
   FFN_TILE_256 = 5,     // 256 x 256, 8 waves; not fp32
   FFN_TILE_COUNT = 6
 };
+// One of up to three products that share a launch (FFN_STAGE_DW: gate, up and down).
+struct FfnProblem {
+  const void* A; const void* B; void* C;
+  int64_t lda, ldb, ldc;
+  int64_t part0;          // its partial products' offset in a split's, in elements
+  int32_t M, N;
+  int32_t tiles_m, tiles_n;
+};
 struct FfnGemm {
-  const void* A[2];       // operand, or (batched) operand of batch entry 0 / 1
+  FfnProblem problem[3];  // FFN_STAGE_DW: A, B, C, their strides, M, N and tiles come from here
+  int32_t problems;       // 0: the fields below
+  const void* A;
   const void* B[2];       // operand; B[1]: Wu (FFN_GATE), or a second K segment (K-strided B)
   int64_t lda, ldb, ldb1; // row strides in elements (ldb1: of Wu in FFN_GATE); rows 16-byte aligned
   int32_t M, N;           // output rows and columns (FFN_GATE: columns of one of g, u)
@@ -36,17 +46,17 @@ struct FfnGemm {
   int32_t slices0;        // slices of K segment 0
   int32_t slices;         // slices of all segments
   int32_t slices_per_split, splits;
-  int32_t tiles_m, tiles_n, tiles;
-  int32_t batched;        // A and C indexed by batch entry
-  void* C[3];             // FFN_STORE: outputs by batch entry; FFN_GATE: h; FFN_DGATE: dg, du, h
+  int32_t tiles_m, tiles_n, tiles;  // tiles: of all problems
+  void* C[3];             // FFN_STORE: the output; FFN_GATE: h; FFN_DGATE: dg, du, h
   int64_t ldc;            // row stride of C (FFN_DGATE: of dg and du)
-  int64_t Np;             // row stride of h, g and u; of the partial products
+  int64_t Np;             // row stride of h, g and u
   float* gu;              // saved g and u, 32 x 8 blocks (FFN_GATE: null: not saved)
-  float* part;            // fp32 partial products [batch][split][M][Np]; null: one split
+  float* part;            // fp32 partial products by split, then problem, rows of N rounded up to 8; null: one split
+  int64_t part_split;     // elements of a split's
   int32_t act;
   int32_t c_bf16, accumulate;
 };
-hipError_t launch_ffn(FfnStage stage, bool f32, int tile, const FfnGemm& p, int batches, hipStream_t st);
+hipError_t launch_ffn(FfnStage stage, bool f32, int tile, const FfnGemm& p, hipStream_t st);
 // Matrices to copy into 16-byte aligned rows.
 struct FfnCopies {
   static constexpr int kMost = 5;

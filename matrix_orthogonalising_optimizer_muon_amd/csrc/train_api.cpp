@@ -106,7 +106,10 @@ Operand operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t e
 struct Shape {
   int tile = FFN_TILE_128, splits = 1;
   int64_t slices = 0, per_split = 0;
-  int64_t tiles_m = 0, tiles_n = 0;
+};
+constexpr int kTileM[FFN_TILE_COUNT] = {32, 64, 64, 128, 128, 256}, kTileN[FFN_TILE_COUNT] = {32, 64, 128, 128, 256, 256};
+struct Extent {
+  int64_t M, cols;  // rows; columns the tiles cover (twice the output's for the gate stage)
 };
 
 enum Layout { BOTH_CONTIGUOUS = 0, B_STRIDED = 1, BOTH_STRIDED = 2 };
@@ -123,24 +126,27 @@ constexpr double kJoinUs = 2.7, kJoinBytesPerUs = 6.2e6;
 constexpr int64_t kMaxPartBytes = int64_t{1} << 28;
 constexpr int64_t kMinSplitSlices = 4;
 
-// cols: tile columns covered (twice the output's for the gate stage); dgate: its epilogue.
-Shape choose(bool f32, Layout layout, int64_t M, int64_t cols, int64_t slices, int batches, bool may_split, bool dgate,
+// The products of one launch (same K), dgate: their epilogue.
+Shape choose(bool f32, Layout layout, std::initializer_list<Extent> outputs, int64_t slices, bool may_split, bool dgate,
              int cus) {
-  static const int bm[FFN_TILE_COUNT] = {32, 64, 64, 128, 128, 256}, bn[FFN_TILE_COUNT] = {32, 64, 128, 128, 256, 256};
   static const int per_cu[FFN_TILE_COUNT] = {2, 2, 2, 1, 1, 1};
   static const int try_splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
   Shape best;
   double best_us = 1e300;
   for (int t = 0; t < FFN_TILE_COUNT; ++t) {
     if (f32 && t >= FFN_TILE_128x256) continue;
-    const int64_t tm = cdiv(M, bm[t]), tn = cdiv(cols, bn[t]);
-    const double area = bm[t] * bn[t] / 65536.0;
+    int64_t tiles = 0, elements = 0;
+    for (const Extent& o : outputs) {
+      tiles += cdiv(o.M, kTileM[t]) * cdiv(o.cols, kTileN[t]);
+      elements += o.M * round_up(o.cols, 8);
+    }
+    const double area = kTileM[t] * kTileN[t] / 65536.0;
     for (const int want : try_splits) {
       if (want > 1 && (!may_split || slices / want < kMinSplitSlices)) break;
       const int64_t per = cdiv(slices, want), splits = cdiv(slices, per);
-      const int64_t part = splits > 1 ? batches * splits * M * cols * 4 : 0;
+      const int64_t part = splits > 1 ? splits * elements * 4 : 0;
       if (part > kMaxPartBytes) break;
-      const int64_t wgs = tm * tn * batches * splits;
+      const int64_t wgs = tiles * splits;
       const int64_t slots = static_cast<int64_t>(cus) * per_cu[t];
       const double us = cdiv(wgs, slots) * (per * static_cast<double>(kSliceUs[f32][layout][t][wgs <= cus]) + kFillUs +
                                             area * (dgate ? kDgateEpilogueUs : kEpilogueUs)) +
@@ -151,8 +157,6 @@ Shape choose(bool f32, Layout layout, int64_t M, int64_t cols, int64_t slices, i
         best.splits = static_cast<int>(splits);
         best.slices = slices;
         best.per_split = per;
-        best.tiles_m = tm;
-        best.tiles_n = tn;
       }
     }
   }
@@ -164,11 +168,11 @@ struct FfnPlan {
   int64_t es = 2, bk = 64, Hp = 0;
   Operand x, wg, wu, wd, dy;
   size_t off_h = 0, off_dg = 0, off_part = 0, bytes = 0;
-  Shape gate, down, dgate, dx, dgu, dwd;
+  Shape gate, down, dgate, dx, dw;
 };
 
-size_t part_bytes(const Shape& s, int batches, int64_t M, int64_t N) {
-  return s.splits > 1 ? static_cast<size_t>(batches) * s.splits * M * round_up(N, 8) * 4 : 0;
+size_t part_bytes(const Shape& s, int64_t elements) {
+  return s.splits > 1 ? static_cast<size_t>(s.splits) * elements * 4 : 0;
 }
 
 FfnPlan plan_of(const muon_ffn* f, const muon_ffn_grads* g, int cus) {
@@ -193,20 +197,19 @@ FfnPlan plan_of(const muon_ffn* f, const muon_ffn_grads* g, int cus) {
   p.off_h = a.take(inter);
   size_t part = 0;
   if (!g) {
-    p.gate = choose(f32, BOTH_CONTIGUOUS, T, 2 * p.Hp, cdiv(D, p.bk), 1, false, false, cus);  // h's padding is written too
-    p.down = choose(f32, BOTH_CONTIGUOUS, T, D, cdiv(F, p.bk), 1, true, false, cus);
-    part = part_bytes(p.down, 1, T, D);
+    p.gate = choose(f32, BOTH_CONTIGUOUS, {{T, 2 * p.Hp}}, cdiv(D, p.bk), false, false, cus);  // h's padding is written too
+    p.down = choose(f32, BOTH_CONTIGUOUS, {{T, D}}, cdiv(F, p.bk), true, false, cus);
+    part = part_bytes(p.down, T * round_up(D, 8));
   } else {
     p.dy = operand(g->dy, g->ld_dy, T, D, p.es, a);
     p.off_dg = a.take(2 * inter);  // dg and du side by side in each row: one operand of dx
-    const int n = (g->g_gate && g->g_up) ? 2 : 1;
-    p.dgate = choose(f32, B_STRIDED, T, p.Hp, cdiv(D, p.bk), 1, false, true, cus);
-    p.dx = choose(f32, B_STRIDED, T, D, 2 * (p.Hp / p.bk), 1, true, false, cus);
-    p.dgu = choose(f32, BOTH_STRIDED, F, D, cdiv(T, p.bk), n, true, false, cus);
-    p.dwd = choose(f32, BOTH_STRIDED, D, F, cdiv(T, p.bk), 1, true, false, cus);
-    if (g->dx) part = std::max(part, part_bytes(p.dx, 1, T, D));
-    if (g->g_gate || g->g_up) part = std::max(part, part_bytes(p.dgu, n, F, D));
-    if (g->g_down) part = std::max(part, part_bytes(p.dwd, 1, D, F));
+    p.dgate = choose(f32, B_STRIDED, {{T, p.Hp}}, cdiv(D, p.bk), false, true, cus);
+    p.dx = choose(f32, B_STRIDED, {{T, D}}, 2 * (p.Hp / p.bk), true, false, cus);
+    if (g->dx) part = part_bytes(p.dx, T * round_up(D, 8));
+    // the weight gradients wanted, in one launch
+    const Extent fd{g->g_gate ? F : 0, D}, fu{g->g_up ? F : 0, D}, df{g->g_down ? D : 0, F};
+    p.dw = choose(f32, BOTH_STRIDED, {fd, fu, df}, cdiv(T, p.bk), true, false, cus);
+    part = std::max(part, part_bytes(p.dw, (fd.M + fu.M) * round_up(D, 8) + df.M * round_up(F, 8)));
   }
   p.off_part = a.take(part);
   p.bytes = a.at;
@@ -227,7 +230,7 @@ hipError_t settle(std::initializer_list<Operand*> operands, char* ws, bool f32, 
   return launch_ffn_align(c, f32, st);
 }
 
-FfnGemm product(const Shape& s, int64_t M, int64_t N, int64_t K, int act) {
+FfnGemm product(const Shape& s, int64_t M, int64_t N, int64_t cols, int64_t K, int act) {
   FfnGemm q;
   std::memset(&q, 0, sizeof(q));
   q.M = static_cast<int32_t>(M);
@@ -236,22 +239,38 @@ FfnGemm product(const Shape& s, int64_t M, int64_t N, int64_t K, int act) {
   q.slices0 = q.slices = static_cast<int32_t>(s.slices);
   q.slices_per_split = static_cast<int32_t>(s.per_split);
   q.splits = s.splits;
-  q.tiles_m = static_cast<int32_t>(s.tiles_m);
-  q.tiles_n = static_cast<int32_t>(s.tiles_n);
+  q.tiles_m = static_cast<int32_t>(cdiv(M, kTileM[s.tile]));
+  q.tiles_n = static_cast<int32_t>(cdiv(cols, kTileN[s.tile]));
   q.tiles = q.tiles_m * q.tiles_n;
   q.act = act;
   return q;
 }
 
-// A plain output: type, row stride, and where the partial products of a K split go.
-void output(FfnGemm& q, const Shape& s, char* part, bool bf16, int64_t ldc, bool accumulate) {
+// A plain output: its type, and where the partial products of a K split go.
+void output(FfnGemm& q, const Shape& s, char* part, int64_t part_split, bool bf16, bool accumulate) {
   q.c_bf16 = bf16;
-  q.ldc = ldc;
   q.accumulate = accumulate;
   if (s.splits > 1) {
     q.part = reinterpret_cast<float*>(part);
-    q.Np = round_up(q.N, 8);
+    q.part_split = part_split;
   }
+}
+
+// One more product of a launch.
+void add(FfnGemm& q, const Shape& s, const void* A, int64_t lda, const void* B, int64_t ldb, void* C, int64_t ldc,
+         int64_t M, int64_t N) {
+  FfnProblem& o = q.problem[q.problems];
+  o.A = A; o.lda = lda;
+  o.B = B; o.ldb = ldb;
+  o.C = C; o.ldc = ldc;
+  o.M = static_cast<int32_t>(M);
+  o.N = static_cast<int32_t>(N);
+  o.tiles_m = static_cast<int32_t>(cdiv(M, kTileM[s.tile]));
+  o.tiles_n = static_cast<int32_t>(cdiv(N, kTileN[s.tile]));
+  o.part0 = q.part_split;
+  q.part_split += M * round_up(N, 8);
+  q.tiles += o.tiles_m * o.tiles_n;
+  ++q.problems;
 }
 
 int check_workspace(const void* ws, size_t have, size_t need) {
@@ -364,23 +383,23 @@ int muon_ffn_forward(muon_ctx* ctx, const muon_ffn* f, void* y, int64_t ld_y, vo
     MUON_HIP(settle({&p.x, &p.wg, &p.wu, &p.wd}, ws, f32, st));
     const int64_t T = f->tokens, D = f->dim, F = f->hidden;
 
-    FfnGemm q = product(p.gate, T, F, D, f->activation);
-    q.A[0] = p.x.p; q.lda = p.x.ld;
+    FfnGemm q = product(p.gate, T, F, 2 * p.Hp, D, f->activation);
+    q.A = p.x.p; q.lda = p.x.ld;
     q.B[0] = p.wg.p; q.ldb = p.wg.ld;
     q.B[1] = p.wu.p; q.ldb1 = p.wu.ld;
     q.tail = static_cast<int32_t>(D % p.bk);
     q.C[0] = ws + p.off_h;
     q.ldc = q.Np = p.Hp;
     q.gu = static_cast<float*>(saved);
-    MUON_HIP(launch_ffn(FFN_STAGE_GATE, f32, p.gate.tile, q, 1, st));
+    MUON_HIP(launch_ffn(FFN_STAGE_GATE, f32, p.gate.tile, q, st));
 
-    q = product(p.down, T, D, F, f->activation);
-    q.A[0] = ws + p.off_h; q.lda = p.Hp;
+    q = product(p.down, T, D, D, F, f->activation);
+    q.A = ws + p.off_h; q.lda = p.Hp;
     q.B[0] = p.wd.p; q.ldb = p.wd.ld;
     q.tail = static_cast<int32_t>(F % p.bk);
-    q.C[0] = y;
-    output(q, p.down, ws + p.off_part, !f32, ld_y, false);
-    MUON_HIP(launch_ffn(FFN_STAGE_DOWN, f32, p.down.tile, q, 1, st));
+    q.C[0] = y; q.ldc = ld_y;
+    output(q, p.down, ws + p.off_part, T * round_up(D, 8), !f32, false);
+    MUON_HIP(launch_ffn(FFN_STAGE_DOWN, f32, p.down.tile, q, st));
     return MUON_OK;
   } catch (...) {
     return MUON_ERR_HIP;
@@ -414,50 +433,33 @@ int muon_ffn_backward(muon_ctx* ctx, const muon_ffn* f, const muon_ffn_grads* g,
     MUON_HIP(settle({&p.x, &p.wg, &p.wu, &p.wd, &p.dy}, ws, f32, st));
     char *h = ws + p.off_h, *dgp = ws + p.off_dg, *dup = dgp + p.Hp * p.es, *part = ws + p.off_part;
 
-    FfnGemm q = product(p.dgate, T, F, D, f->activation);
-    q.A[0] = p.dy.p; q.lda = p.dy.ld;
+    FfnGemm q = product(p.dgate, T, F, p.Hp, D, f->activation);
+    q.A = p.dy.p; q.lda = p.dy.ld;
     q.B[0] = p.wd.p; q.ldb = p.wd.ld;
     q.tail = static_cast<int32_t>(D % p.bk);
     q.C[0] = dgp; q.C[1] = dup; q.C[2] = h;
     q.ldc = 2 * p.Hp;
     q.Np = p.Hp;
     q.gu = const_cast<float*>(static_cast<const float*>(g->saved));
-    MUON_HIP(launch_ffn(FFN_STAGE_DGATE, f32, p.dgate.tile, q, 1, st));
+    MUON_HIP(launch_ffn(FFN_STAGE_DGATE, f32, p.dgate.tile, q, st));
 
     if (g->dx) {
-      q = product(p.dx, T, D, F, f->activation);
+      q = product(p.dx, T, D, D, F, f->activation);
       q.slices0 = static_cast<int32_t>(p.Hp / p.bk);
-      q.A[0] = dgp; q.lda = 2 * p.Hp; q.KA = static_cast<int32_t>(2 * p.Hp);
+      q.A = dgp; q.lda = 2 * p.Hp; q.KA = static_cast<int32_t>(2 * p.Hp);
       q.B[0] = p.wg.p; q.ldb = p.wg.ld;
       q.B[1] = p.wu.p;
-      q.C[0] = g->dx;
-      output(q, p.dx, part, !f32, g->ld_dx, false);
-      MUON_HIP(launch_ffn(FFN_STAGE_DX, f32, p.dx.tile, q, 1, st));
+      q.C[0] = g->dx; q.ldc = g->ld_dx;
+      output(q, p.dx, part, T * round_up(D, 8), !f32, false);
+      MUON_HIP(launch_ffn(FFN_STAGE_DX, f32, p.dx.tile, q, st));
     }
-    if (g->g_gate || g->g_up) {
-      // both in one launch where they share a row stride, else one after the other
-      const bool both = g->g_gate && g->g_up;
-      const bool one_launch = both && g->ld_g_gate == g->ld_g_up;
-      for (int i = 0; i < 2; ++i) {
-        void* out = i ? g->g_up : g->g_gate;
-        if (!out || (one_launch && i)) continue;
-        q = product(p.dgu, F, D, T, f->activation);
-        q.A[0] = i ? dup : dgp; q.A[1] = dup; q.lda = 2 * p.Hp;
-        q.B[0] = p.x.p; q.ldb = p.x.ld;
-        q.C[0] = out;
-        q.C[1] = one_launch ? g->g_up : nullptr;
-        q.batched = one_launch;
-        output(q, p.dgu, part, gb, i ? g->ld_g_up : g->ld_g_gate, g->accumulate);
-        MUON_HIP(launch_ffn(FFN_STAGE_DW, f32, p.dgu.tile, q, one_launch ? 2 : 1, st));
-      }
-    }
-    if (g->g_down) {
-      q = product(p.dwd, D, F, T, f->activation);
-      q.A[0] = p.dy.p; q.lda = p.dy.ld;
-      q.B[0] = h; q.ldb = p.Hp;
-      q.C[0] = g->g_down;
-      output(q, p.dwd, part, gb, g->ld_g_down, g->accumulate);
-      MUON_HIP(launch_ffn(FFN_STAGE_DW, f32, p.dwd.tile, q, 1, st));
+    if (g->g_gate || g->g_up || g->g_down) {
+      q = product(p.dw, 0, 0, 0, T, f->activation);
+      if (g->g_gate) add(q, p.dw, dgp, 2 * p.Hp, p.x.p, p.x.ld, g->g_gate, g->ld_g_gate, F, D);
+      if (g->g_up) add(q, p.dw, dup, 2 * p.Hp, p.x.p, p.x.ld, g->g_up, g->ld_g_up, F, D);
+      if (g->g_down) add(q, p.dw, p.dy.p, p.dy.ld, h, p.Hp, g->g_down, g->ld_g_down, D, F);
+      output(q, p.dw, part, q.part_split, gb, g->accumulate);
+      MUON_HIP(launch_ffn(FFN_STAGE_DW, f32, p.dw.tile, q, st));
     }
     return MUON_OK;
   } catch (...) {
