@@ -436,7 +436,7 @@ typedef struct muon_logits {
   float *lse;              /* rows: log sum exp z (0 for rows that take no part), or null */
   int64_t ld, ld_d;
   int64_t rows, vocab;
-  float temperature;       /* finite, > 0 */
+  float temperature;       /* finite, > 0, and 2 / temperature finite */
   int32_t dtype;           /* MUON_F32 or MUON_BF16 */
   int32_t lse_given;       /* 0 or 1 */
 } muon_logits;

@@ -284,7 +284,7 @@ int validate(const muon_logits* l) {
   if (!l || !dtype_ok(l->dtype)) return MUON_ERR_ARG;
   if (l->rows < 0 || l->rows > 0x7FFFFFFF || l->vocab < 1 || l->vocab > (int64_t{1} << 28)) return MUON_ERR_ARG;
   if (l->ld < l->vocab || (l->dlogits && l->ld_d < l->vocab)) return MUON_ERR_ARG;
-  if (!std::isfinite(l->temperature) || !(l->temperature > 0.0f) || !std::isfinite(1.0f / l->temperature))
+  if (!std::isfinite(l->temperature) || !(l->temperature > 0.0f) || !std::isfinite(2.0f / l->temperature))
     return MUON_ERR_ARG;
   if (l->lse_given != 0 && l->lse_given != 1) return MUON_ERR_ARG;
   const int64_t es = size_of(l->dtype);
@@ -519,6 +519,7 @@ int muon_distill_loss(muon_ctx* ctx, const muon_logits* l, const muon_distill* t
     if (t->top < 1 || t->top > MUON_MAX_TOP || t->ld_top < t->top || t->ld_ids < t->top) return MUON_ERR_ARG;
     if (!dtype_ok(t->top_dtype) || (t->id_dtype != MUON_I32 && t->id_dtype != MUON_I64)) return MUON_ERR_ARG;
     if (l->rows > 0 && (!t->top_logits || !t->top_ids)) return MUON_ERR_ARG;
+    if (!aligned(t->top_logits, size_of(t->top_dtype)) || !aligned(t->top_ids, 4)) return MUON_ERR_ARG;
     if (l->rows == 0) return MUON_OK;
     const LossSplit s = split_of(l, t->top, ctx_cus(ctx));
     const int wrc = check_workspace(workspace, workspace_bytes, s.bytes);

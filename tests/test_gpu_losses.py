@@ -304,6 +304,45 @@ def test_losses_evaluation_only_and_leading_dimensions(S):
     assert empty[0].shape == (0,) and empty[2].shape == (0, 333)
 
 
+@pytest.mark.parametrize("n", [5, 300])
+@pytest.mark.parametrize("V", [5, 3001, 152064])
+def test_policy_from_a_given_normaliser(S, n, V):
+    """The C entry with lse given: without a gradient, with one, and with one in place equal
+    each other and, like the pass that computes it, the oracle."""
+    from matrix_orthogonalising_optimizer_muon_amd import binding as B
+    from matrix_orthogonalising_optimizer_muon_amd.context import context, stream_of
+    z, t, old, adv, ref = policy_inputs(n, V, "f32")
+    t[2] = -1
+    dev, f32 = z.device, torch.float32
+    new = lambda: torch.full((n,), 7.0, device=dev)  # noqa: E731
+    loss, logp, lse = new(), new(), new()
+    def call(d, given, loss, logp, src=z):
+        l = B.muon_logits(src.data_ptr(), None if d is None else d.data_ptr(), None, None, loss.data_ptr(), lse.data_ptr(), V, V,
+                          n, V, 1.0, B.MUON_F32, given)
+        p = B.muon_policy(t.data_ptr(), old.data_ptr(), adv.data_ptr(), ref.data_ptr(), logp.data_ptr(), 0.2, 0.28, 0.1)
+        nb = B.muon_loss_workspace_size(context(dev), l)
+        ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+        assert B.muon_policy_loss(context(dev), l, p, ws.data_ptr(), nb, stream_of(dev)) == 0
+        return loss, logp
+    full = torch.full((n, V), 7.0, device=dev)
+    call(full, 0, loss, logp)
+    none = call(None, 1, new(), new())
+    given = torch.full((n, V), 7.0, device=dev)
+    some = call(given, 1, new(), new())
+    inplace = z.clone()
+    call(inplace, 1, new(), new(), inplace)
+    torch.cuda.synchronize()
+    assert torch.equal(none[0], some[0]) and torch.equal(none[1], some[1]) and torch.equal(given, inplace)
+    assert float(loss[2]) == 0.0 and bool((given[2] == 0).all())
+    # a gradient's coefficient may nearly cancel (policy and KL parts), so each side is held to the oracle
+    pick = list(range(n))[::max(1, n // 30)]
+    args = [to_np(z[pick]), t.cpu().numpy()[pick], *(to_np(a[pick]) for a in (old, adv, ref))]
+    for g, lp, kw in ((full, logp, {}), (given, none[1], dict(lse_given=True))):
+        want = ol.policy(*args, clip_low=0.2, clip_high=0.28, kl_coef=0.1, temperature=1.0, half_step=2.0 ** -24, **kw)
+        inside(g[pick], want["grad"], want["err_grad"], "grad")
+        inside(lp[pick], want["logp"], want["err_logp"], "logp")
+
+
 def test_losses_graph_and_stream(S):
     """Captured and replayed with other eager work between the replays, and on a side stream."""
     z, t, old, adv, _ = policy_inputs(40, 5003, "bf16")

@@ -144,7 +144,7 @@ def distill(**kw):
 
 BAD_LOGITS = [dict(logits=None), dict(rows=-1), dict(vocab=0), dict(vocab=(1 << 28) + 1), dict(ld=49), dict(ld_d=49),
               dict(temperature=0.0), dict(temperature=-1.0), dict(temperature=float("nan")), dict(temperature=float("inf")),
-              dict(temperature=1e-45), dict(dtype=2), dict(lse_given=2), dict(lse_given=1, lse=None), dict(logits=FAKE + 1),
+              dict(temperature=1e-45), dict(temperature=5e-39), dict(dtype=2), dict(lse_given=2), dict(lse_given=1, lse=None), dict(logits=FAKE + 1),
               dict(dlogits=FAKE + 1), dict(dlogits=FAKE, ld_d=51), dict(dtype=B.MUON_F32, logits=FAKE + 2)]
 
 
@@ -180,7 +180,8 @@ def test_distill_validation(hctx):
     for bad in BAD_LOGITS:
         assert call(logits(**bad), distill()) == B.MUON_ERR_ARG, bad
     for bad in [dict(top=0), dict(top=B.MUON_MAX_TOP + 1, ld_top=2000, ld_ids=2000), dict(ld_top=3), dict(ld_ids=3),
-                dict(top_dtype=2), dict(id_dtype=1), dict(top_logits=None), dict(top_ids=None)]:
+                dict(top_dtype=2), dict(id_dtype=1), dict(top_logits=None), dict(top_ids=None), dict(top_logits=FAKE + 2),
+                dict(top_ids=FAKE + 2)]:
         assert call(logits(), distill(**bad)) == B.MUON_ERR_ARG, bad
     assert B._lib.muon_distill_loss(hctx, logits(), None, None, 0, None) == B.MUON_ERR_ARG
     few = logits(rows=3, vocab=152064, ld=152064, ld_d=152064)
