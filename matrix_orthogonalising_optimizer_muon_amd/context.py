@@ -36,6 +36,11 @@ def stream_of(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def new_like(t: torch.Tensor) -> torch.Tensor:
+    """An uninitialised contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def dtype_code(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
@@ -63,6 +68,8 @@ def matrix(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, device:
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     rows, cols = shape
+    if t.is_contiguous():
+        return max(cols, 1)
     ld, step = t.stride()
     if rows and cols > 1 and step != 1:
         raise ValueError(f"{name} must have unit column stride, got strides {t.stride()}")

@@ -11,9 +11,15 @@
 //            dlogits_v = w u (P q_v - sum_{j: i_j = v} p_j) / tau
 //
 // One workgroup per row. The first pass keeps each thread's running maximum m and sum s of
-// exp((z - m)) over its columns (one rescale per 16-byte vector), joined in a fixed order;
-// the second writes the gradient. All of it in fp32; exp((z - m) c) is formed from the
-// difference, so that rows of the type's lowest values stay exact, and q = e / s.
+// exp(z - m) over its columns (one rescale per 16 values), joined in a fixed order; the second
+// writes the gradient. All of it in fp32; exp((z - m) c) is formed from the difference, so
+// that rows of the type's lowest values stay exact, and q = e / s.
+//
+// Bound by HBM: the logits read once, the gradient written once. 4096 x 151936 bf16, a fifth of
+// the rows without weight: 440 us, 5.1 TB/s (a copy reaches 5.1); 2048 x 152064 with 64 kept
+// entries: 273 us, 4.3 TB/s, where one row a CU at a time leaves the last of 7.2 rounds partly
+// idle. The arithmetic (two exponentials a column, about 17 instructions) takes some 18 us a row of
+// 152064 on a CU and hides behind the row's 30 us of traffic.
 #include <type_traits>
 
 #include "mfma_util.hpp"

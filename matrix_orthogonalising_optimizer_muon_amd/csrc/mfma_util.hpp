@@ -11,14 +11,12 @@ namespace {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // XOR swizzle of LDS rows of CH 16-byte chunks, so that fragment reads of 32 consecutive
-// rows spread over all banks (CH = 8: 128-byte rows; CH = 4: 64-byte
-// rows, two per 128 bytes, where rows 2t and 2t+1 share the XOR term so that 8
-// consecutive rows read at one logical chunk still cover all eight 16-byte positions of a
-// 128-byte span).
+// rows spread over all banks (CH = 8: 128-byte rows; CH = 4: 64-byte rows, two per 128 bytes,
+// where rows 2t and 2t+1 share the XOR term so that 8 consecutive rows read at one logical
+// chunk still cover all eight 16-byte positions of a 128-byte span).
 template <int CH>
 __device__ __forceinline__ int swz_bits(int row) {
   static_assert(CH == 8 || CH == 4, "chunks per row");

@@ -18,7 +18,7 @@ import math
 import torch
 
 from . import binding as B
-from .context import context, dtype_code, matrix, on_gpu, stream_of
+from .context import context, dtype_code, matrix, new_like, on_gpu, stream_of
 
 
 def _block(x, w_gate, w_up, w_down, activation):
@@ -45,7 +45,7 @@ def ffn_forward(x, w_gate, w_up, w_down, *, activation: str = "silu", save: bool
     """(y, saved): y has x's shape; ``saved`` (with ``save``) is what ``ffn_backward`` needs of
     the forward, a float32 tensor of g and u, else None."""
     f, x2, device = _block(x, w_gate, w_up, w_down, activation)
-    y = torch.empty(x.shape, dtype=x.dtype, device=device)
+    y = new_like(x)
     ctx = context(device)
     nbytes, nsaved = B.muon_ffn_workspace_size(ctx, f)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -68,14 +68,14 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, activation: str = "silu"
     if grads is None:
         if accumulate:
             raise ValueError("accumulate needs the gradient buffers (grads)")
-        grads = tuple(torch.empty(s, dtype=x.dtype, device=device) for s in shapes)
+        grads = (new_like(w_gate), new_like(w_up), new_like(w_down))
     names = ("g_gate", "g_up", "g_down")
     given = [t for t in grads if t is not None]
     g_code = dtype_code(given[0], "grads") if given else B.MUON_F32
     lds = [0 if t is None else matrix(t, n, s, given[0].dtype, device) for t, n, s in zip(grads, names, shapes)]
     if not isinstance(saved, torch.Tensor) or saved.dtype != torch.float32 or saved.device != device:
         raise TypeError("saved must be the float32 tensor ffn_forward(save=True) returned")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=device) if need_dx else None
+    dx = new_like(x) if need_dx else None
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     g = B.muon_ffn_grads(dy2.data_ptr(), saved.data_ptr(), ptr(dx), *(ptr(t) for t in grads),
                          matrix(dy2, "dy", x2.shape, x.dtype, device), f.dim, *lds, g_code, int(accumulate))
@@ -102,7 +102,7 @@ class _GatedFFN(torch.autograd.Function):
         x, w_gate, w_up, w_down, saved = ctx.saved_tensors
         need = ctx.needs_input_grad
         weights = (w_gate, w_up, w_down)
-        grads = tuple(torch.empty(w.shape, dtype=w.dtype, device=w.device) if n else None
+        grads = tuple(new_like(w) if n else None
                       for w, n in zip(weights, need[1:4]))
         # an expanded dy (of a sum) has no row stride of its own
         out = ffn_backward(dy.contiguous(), x, *weights, saved, activation=ctx.activation, grads=grads, need_dx=need[0])

@@ -16,7 +16,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .context import context, dtype_code, matrix, on_gpu, stream_of, vector
+from .context import context, dtype_code, matrix, new_like, on_gpu, stream_of, vector
 
 
 def _rows(logits, weights, temperature, out=None, loss=None, lse=None, lse_given=False, grad_rows=None):
@@ -90,7 +90,7 @@ def policy_loss(logits, targets, old_logp, advantages, *, ref_logp=None, weights
     loss = torch.empty(lead, dtype=torch.float32, device=logits.device)
     logp = torch.empty(lead, dtype=torch.float32, device=logits.device)
     if grad and out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = new_like(logits)
     l, z, device = _rows(logits, weights, temperature, out if grad else None, loss)
     t = _policy(z, device, targets, old_logp, advantages, ref_logp, clip_low, clip_high, kl_coef, logp)
     _call(B.muon_policy_loss, "muon_policy_loss", device, l, t, 0)
@@ -106,7 +106,7 @@ def distill_loss(logits, top_logits, top_ids, *, top_lse=None, weights=None, tem
     without ``grad``). Entries with an id outside the vocabulary are absent."""
     loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
     if grad and out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = new_like(logits)
     l, z, device = _rows(logits, weights, temperature, out if grad else None, loss)
     t, keep = _distill(z, device, top_logits, top_ids, top_lse)
     _call(B.muon_distill_loss, "muon_distill_loss", device, l, t, t.top)
@@ -131,7 +131,7 @@ class _PolicyLoss(torch.autograd.Function):
     def backward(ctx, grad_loss, _):
         logits, targets, old_logp, advantages, ref_logp, weights, lse = ctx.saved_tensors
         clip_low, clip_high, kl_coef, temperature = ctx.numbers
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = new_like(logits)
         up = grad_loss.contiguous()
         l, z, device = _rows(logits, weights, temperature, out, None, lse, True, up)
         t = _policy(z, device, targets, old_logp, advantages, ref_logp, clip_low, clip_high, kl_coef, None)
@@ -162,7 +162,7 @@ class _DistillLoss(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss):
         logits, top_logits, top_ids, top_lse, weights, lse = ctx.saved_tensors
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = new_like(logits)
         up = grad_loss.contiguous()
         l, z, device = _rows(logits, weights, ctx.temperature, out, None, lse, True, up)
         t, keep = _distill(z, device, top_logits, top_ids, top_lse)
