@@ -418,12 +418,13 @@ int muon_ffn_forward(muon_ctx *ctx, const muon_ffn *f, void *y, int64_t ld_y, vo
 int muon_ffn_backward(muon_ctx *ctx, const muon_ffn *f, const muon_ffn_grads *g, void *workspace,
                       size_t workspace_bytes, void *stream);
 
-/* Logits (rows x vocab, in `dtype`; vocab up to 2^28) and what every loss does with them: with
+/* Logits (rows x vocab, in `dtype`; fewer than 2^24 rows, vocab up to 2^28, row strides up to
+ * 2^36) and what every loss does with them: with
  * z = logits / temperature, loss[r] = weights[r] l_r and
  * dlogits = d(sum_r grad_rows[r] loss[r]) / dlogits, rounded once to `dtype`; computed in
  * fp32. A row of weight 0 takes no part: its logits are not read, its loss is 0 and its
  * gradient row is written as zeros. dlogits null: no gradient. dlogits may be `logits` itself
- * (same stride; the gradient replaces the logits), else must not overlap it. With lse_given
+ * (same stride; the gradient replaces the logits); any other overlap is refused. With lse_given
  * the normaliser is read from lse instead of computed (one pass less): a backward after a
  * forward that kept it. Without a gradient and with lse given only the rows' own entries are
  * read. */

@@ -280,9 +280,26 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 
 // ---- losses ----
 
+// A workgroup of 256 threads a row: 2^32 threads is past what a launch takes.
+constexpr int64_t kMaxRows = (int64_t{1} << 24) - 1;
+constexpr int64_t kMaxLogitsLd = int64_t{1} << 36;
+
+// Whether two row sets of one shape (strides in elements, at least cols) share an element:
+// apart as address ranges, or columns side by side in rows of one stride.
+bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t cols, int64_t es) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t na = static_cast<uintptr_t>(((rows - 1) * lda + cols) * es);
+  const uintptr_t nb = static_cast<uintptr_t>(((rows - 1) * ldb + cols) * es);
+  if (pa + na <= pb || pb + nb <= pa) return false;
+  if (lda != ldb) return true;
+  const uintptr_t row = static_cast<uintptr_t>(lda * es), width = static_cast<uintptr_t>(cols * es);
+  const uintptr_t shift = (pb > pa ? pb - pa : pa - pb) % row;
+  return shift < width || shift + width > row;
+}
+
 int validate(const muon_logits* l) {
   if (!l || !dtype_ok(l->dtype)) return MUON_ERR_ARG;
-  if (l->rows < 0 || l->rows > 0x7FFFFFFF || l->vocab < 1 || l->vocab > (int64_t{1} << 28)) return MUON_ERR_ARG;
+  if (l->rows < 0 || l->rows > kMaxRows || l->vocab < 1 || l->vocab > (int64_t{1} << 28)) return MUON_ERR_ARG;
   if (l->ld < l->vocab || (l->dlogits && l->ld_d < l->vocab)) return MUON_ERR_ARG;
   if (!std::isfinite(l->temperature) || !(l->temperature > 0.0f) || !std::isfinite(2.0f / l->temperature))
     return MUON_ERR_ARG;
@@ -290,8 +307,13 @@ int validate(const muon_logits* l) {
   const int64_t es = size_of(l->dtype);
   if (!aligned(l->logits, es) || !aligned(l->dlogits, es)) return MUON_ERR_ARG;
   if (l->rows > 0 && (!l->logits || (l->lse_given && !l->lse))) return MUON_ERR_ARG;
+  // row strides whose byte offsets stay within 64 bits
+  if (l->ld > kMaxLogitsLd || (l->dlogits && l->ld_d > kMaxLogitsLd)) return MUON_ERR_ARG;
   // in place only as a whole: the same rows
-  if (l->dlogits == l->logits && l->dlogits && l->ld_d != l->ld) return MUON_ERR_ARG;
+  if (l->dlogits && l->dlogits == l->logits && l->ld_d != l->ld) return MUON_ERR_ARG;
+  if (l->dlogits && l->rows > 0 && l->dlogits != l->logits &&
+      overlap(l->logits, l->ld, l->dlogits, l->ld_d, l->rows, l->vocab, es))
+    return MUON_ERR_ARG;
   return MUON_OK;
 }
 

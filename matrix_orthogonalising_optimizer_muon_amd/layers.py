@@ -8,7 +8,10 @@ the weight gradients into given buffers, such as the persistent G arrays of a
 ``MuonUpdate``. ``gated_ffn`` is the same block for torch's automatic differentiation and
 ``GatedFeedForward`` a module holding the weights as ``gate``, ``up`` and ``down``, which
 ``MuonWithAdamW`` routes to the Muon update. Work is enqueued on the current stream of the
-operands' device; workspaces come from torch's allocator for the length of the call.
+operands' device; workspaces come from torch's allocator for the length of the call. All of
+them can be captured into a graph after one eager call; a backward through ``gated_ffn`` is
+captured with ``torch.autograd.grad`` or with no eager graph of the same leaves alive, as
+torch's own functions need it.
 """
 
 from __future__ import annotations
@@ -55,13 +58,38 @@ def ffn_forward(x, w_gate, w_up, w_down, *, activation: str = "silu", save: bool
     return y, saved
 
 
+def _spans(tensors):
+    """(first byte, last byte + 1, row stride, row width) of 2-D tensors with elements."""
+    out = []
+    for t in tensors:
+        if t is not None and t.numel():
+            es, (rows, cols), p = t.element_size(), t.shape, t.data_ptr()
+            ld = t.stride(0) if rows > 1 else cols
+            out.append((p, p + ((rows - 1) * ld + cols) * es, ld * es, cols * es))
+    return out
+
+
+def _overlap(a, b):
+    if a[1] <= b[0] or b[1] <= a[0]:
+        return False
+    if a[2] != b[2]:
+        return True
+    # rows of one stride: apart when the columns lie side by side
+    shift = (b[0] - a[0]) % a[2]
+    return shift < a[3] or shift + b[3] > a[2]
+
+
 def ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, activation: str = "silu", grads=None,
                  accumulate: bool = False, need_dx: bool = True):
     """(dx, g_gate, g_up, g_down) for the gradient ``dy`` of y. ``grads``: (g_gate, g_up,
     g_down) buffers of the weights' shapes, all float32 or all bfloat16, that receive the
     weight gradients (with ``accumulate`` they are added to what is there); an entry may be
-    None when that gradient is not wanted. Without ``grads`` all three are new tensors of
-    the weights' dtype."""
+    None when that gradient is not wanted. They may not share memory with each other or with
+    an operand. Without ``grads`` all three are new tensors of the weights' dtype."""
+    return _backward(dy, x, w_gate, w_up, w_down, saved, activation, grads, accumulate, need_dx, grads is not None)
+
+
+def _backward(dy, x, w_gate, w_up, w_down, saved, activation, grads, accumulate, need_dx, check_overlap):
     f, x2, device = _block(x, w_gate, w_up, w_down, activation)
     dy2 = dy if dy.dim() == 2 else dy.reshape(-1, f.dim)
     shapes = (w_gate.shape, w_up.shape, w_down.shape)
@@ -75,13 +103,20 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, activation: str = "silu"
     lds = [0 if t is None else matrix(t, n, s, given[0].dtype, device) for t, n, s in zip(grads, names, shapes)]
     if not isinstance(saved, torch.Tensor) or saved.dtype != torch.float32 or saved.device != device:
         raise TypeError("saved must be the float32 tensor ffn_forward(save=True) returned")
+    if not saved.is_contiguous():
+        raise ValueError("saved must be contiguous")
+    ld_dy = matrix(dy2, "dy", x2.shape, x.dtype, device)
+    if check_overlap:
+        outs, ins = _spans(grads), _spans((dy2, x2, w_gate, w_up, w_down, saved.view(1, -1)))
+        if any(_overlap(o, t) for i, o in enumerate(outs) for t in ins + outs[:i]):
+            raise ValueError("the gradient buffers (grads) overlap each other or an operand")
     dx = new_like(x) if need_dx else None
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     g = B.muon_ffn_grads(dy2.data_ptr(), saved.data_ptr(), ptr(dx), *(ptr(t) for t in grads),
-                         matrix(dy2, "dy", x2.shape, x.dtype, device), f.dim, *lds, g_code, int(accumulate))
+                         ld_dy, f.dim, *lds, g_code, int(accumulate))
     ctx = context(device)
     nbytes, nsaved = B.muon_ffn_workspace_size(ctx, f, g)
-    if saved.numel() * 4 != nsaved or not saved.is_contiguous():
+    if saved.numel() * 4 != nsaved:
         raise ValueError(f"saved has {saved.numel()} elements, this block's forward wrote {nsaved // 4}")
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     B.check(B.muon_ffn_backward(ctx, f, g, ws.data_ptr(), nbytes, stream_of(device)), "muon_ffn_backward")
@@ -105,7 +140,7 @@ class _GatedFFN(torch.autograd.Function):
         grads = tuple(new_like(w) if n else None
                       for w, n in zip(weights, need[1:4]))
         # an expanded dy (of a sum) has no row stride of its own
-        out = ffn_backward(dy.contiguous(), x, *weights, saved, activation=ctx.activation, grads=grads, need_dx=need[0])
+        out = _backward(dy.contiguous(), x, *weights, saved, ctx.activation, grads, False, need[0], False)
         return (*out, None)
 
 

@@ -196,6 +196,39 @@ def test_distill_validation(hctx):
     assert B._lib.muon_loss_workspace_size(hctx, few, 0, None) == B.MUON_ERR_ARG
 
 
+def test_loss_overlaps_and_limits(hctx):
+    """A gradient that shares memory with the logits is refused unless it is the logits; columns
+    side by side in rows of one stride share none."""
+    call = lambda l: (B.muon_policy_loss(hctx, l, policy(), None, 0, None),  # noqa: E731
+                      B.muon_distill_loss(hctx, l, distill(), None, 0, None))
+    row = 50 * 2
+    for kw, ok in [(dict(dlogits=FAKE), True), (dict(dlogits=FAKE + row), False), (dict(dlogits=FAKE - row), False),
+                   (dict(dlogits=FAKE + 2), False), (dict(dlogits=FAKE + 3 * row), True), (dict(dlogits=FAKE - 3 * row), True),
+                   (dict(dlogits=FAKE + 3 * row - 2), False),
+                   (dict(ld=100, ld_d=100, dlogits=FAKE + row), True), (dict(ld=100, ld_d=100, dlogits=FAKE + row - 2), False),
+                   (dict(ld=100, ld_d=100, dlogits=FAKE + row + 2), False), (dict(ld=101, ld_d=101, dlogits=FAKE + row + 2), True),
+                   (dict(ld=100, ld_d=100, dlogits=FAKE - row), True), (dict(ld=100, ld_d=100, dlogits=FAKE + 3 * row), True),
+                   (dict(ld=100, ld_d=99, dlogits=FAKE + row), False), (dict(rows=1, dlogits=FAKE + row), True),
+                   (dict(rows=(1 << 24) - 1, dlogits=None), True), (dict(rows=1 << 24, dlogits=None), False),
+                   (dict(ld=1 << 36, dlogits=None), True), (dict(ld=(1 << 36) + 1, dlogits=None), False),
+                   (dict(ld_d=(1 << 36) + 1, rows=1), False)]:
+        assert call(logits(**kw)) == ((B.MUON_ERR_DEVICE if ok else B.MUON_ERR_ARG),) * 2, kw
+
+
+def test_gradient_buffers_that_overlap():
+    from matrix_orthogonalising_optimizer_muon_amd.layers import _overlap, _spans
+    t = torch.zeros(6, 8)
+    apart = [(t[:3], t[3:]), (t[:, :4], t[:, 4:]), (t[:, 4:], t[:, :3]), (t, torch.zeros(6, 8)), (t[:1, :4], t[:1, 4:])]
+    shared = [(t, t), (t[:4], t[3:]), (t[:, :5], t[:, 4:]), (t[:, 4:], t[:, :5]), (t[:, :4], t[1:, 3:]),
+              (t[:, 2:4], t.view(12, 4)[:, 1:3])]
+    for pairs, want in ((apart, False), (shared, True)):
+        for k, (a, b) in enumerate(pairs):
+            for p, q in ((a, b), (b, a)):
+                x, y = _spans((p, q))
+                assert _overlap(x, y) == want, (k, want)
+    assert _spans((None, t[:0], t[:, :0])) == []
+
+
 def test_python_refusals():
     """What the Python functions refuse before the library is called (CPU tensors throughout)."""
     from matrix_orthogonalising_optimizer_muon_amd import layers, losses
