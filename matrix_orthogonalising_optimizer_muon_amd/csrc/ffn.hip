@@ -55,7 +55,7 @@ __device__ __forceinline__ void activation(float g, int act, float& a, float& sl
     slope = s * (1.0f + g * (1.0f - s));
   } else {
     constexpr float c = 0.79788456080286535588f, b = 0.044715f;
-    const float g2 = g * g;
+    const float g2 = fminf(g * g, 1e30f);  // finite, so that a slope of 0 or 1 stays one; NaN comes through g
     const float v = c * (g + b * g * g2);
     const float th = 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(2.0f * kLog2e * v) + 1.0f);
     a = 0.5f * g * (1.0f + th);
@@ -734,7 +734,7 @@ __global__ __launch_bounds__(256) void ffn_zero(void* out, int64_t ld, int64_t r
 template <int KIND, int BM, int BN, int WM, int WN, int KS, int NS, int CH, bool AS, bool BS, int EPI>
 hipError_t launch(const FfnGemm& p, hipStream_t st) {
   const int64_t grid = static_cast<int64_t>(p.tiles) * p.splits;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (grid * (64 * WM * WN * KS) > 0xFFFFFFFF) return hipErrorInvalidValue;  // threads of a launch
   hipLaunchKernelGGL((ffn_gemm<KIND, BM, BN, WM, WN, KS, NS, CH, AS, BS, EPI>), dim3(static_cast<unsigned int>(grid)),
                      dim3(64 * WM * WN * KS), 0, st, p);
   return hipGetLastError();
@@ -789,7 +789,7 @@ hipError_t launch_ffn_align(FfnCopies& c, bool f32, hipStream_t st) {
     c.block0[k] = blocks;
     blocks += (c.rows[k] * c.ldd[k] * (f32 ? 4 : 2) / 16 + 255) / 256;
   }
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (blocks * 256 > 0xFFFFFFFF) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned int>(blocks));
   if (f32) hipLaunchKernelGGL(ffn_align<float>, grid, dim3(256), 0, st, c);
   else hipLaunchKernelGGL(ffn_align<unsigned short>, grid, dim3(256), 0, st, c);

@@ -155,6 +155,39 @@ def test_ffn_nan_stays_in_its_row(L):
     assert bool(torch.isnan(y[7]).all()) and bool(torch.isnan(dx[7]).all())
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_ffn_gates_whose_square_overflows(L, act):
+    """|g| = 1e25: act(g) is g or 0 and its slope 1 or 0 exactly. One hidden column of two (g u =
+    1e25 u or 0), small u and down weights, so that every value is a power-of-ten product of few factors."""
+    x = torch.tensor([[1.0, 0.0], [-1.0, 0.0]], device="cuda")
+    wg = torch.tensor([[1e25, 0.0]], device="cuda")
+    wu = torch.tensor([[2.0 ** -70, 1.0]], device="cuda")
+    wd = torch.tensor([[2.0 ** -3], [2.0 ** -4]], device="cuda")
+    dy = torch.tensor([[1.0, 2.0], [4.0, 8.0]], device="cuda")
+    y, saved = L.ffn_forward(x, wg, wu, wd, activation=act, save=True)
+    dx, g_gate, g_up, g_down = L.ffn_backward(dy, x, wg, wu, wd, saved, activation=act)
+    g = float(wg[0, 0])                       # every product below is by a power of two: exact
+    h, dh = g * 2.0 ** -70, 2.0 ** -3 + 2.0 ** -3
+    assert y.tolist() == [[h * 2.0 ** -3, h * 2.0 ** -4], [0.0, 0.0]]
+    du, dg = dh * g, dh * 2.0 ** -70
+    assert g_gate.tolist() == [[dg, 0.0]] and g_up.tolist() == [[du, 0.0]] and g_down.tolist() == [[h], [2 * h]]
+    want = dg * g + du * 2.0 ** -70           # two equal terms: exact
+    assert dx.tolist() == [[want, du], [0.0, 0.0]]
+
+
+def test_ffn_grads_that_overlap_are_refused(L):
+    x, wg, wu, wd, dy = block(40, 16, 24, "bf16")
+    y, saved = L.ffn_forward(x, wg, wu, wd, save=True)
+    both, own = torch.zeros(24, 32, device="cuda", dtype=torch.bfloat16), torch.zeros_like(wd)
+    want = L.ffn_backward(dy, x, wg, wu, wd, saved)
+    got = L.ffn_backward(dy, x, wg, wu, wd, saved, grads=(both[:, :16], both[:, 16:], own))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    for grads in [(both[:, :16], both[:, :16], own), (both[:, :16], both[:, 8:24], own), (wg, both[:, :16], own),
+                  (both[:, :16], both[:, 16:], wd), (x[:24], both[:, :16], own)]:
+        with pytest.raises(ValueError, match="overlap"):
+            L.ffn_backward(dy, x, wg, wu, wd, saved, grads=grads)
+
+
 def test_ffn_extreme_gates(L):
     """Gates far outside the curved range: act(g) is g or 0 and the slope 1 or 0, no NaN."""
     T, D, F = 20, 64, 64
