@@ -320,7 +320,7 @@ int validate(const muon_logits* l) {
 // Few long rows: one workgroup a row leaves most CUs idle, so each row is split until there
 // are about as many workgroups as CUs, with at least kMinPart vectors (16 bytes) a part. It
 // costs a launch, so it is for rows of kMinSplit columns or more: 16 rows of 152064 bf16
-// columns take 25.8 us unsplit and 9.8 us (4.1 + 5.7) split, but 77 rows of 32003 fp32 columns
+// columns take 25.8 us unsplit and 9.2 us (3.9 + 5.3) split, but 77 rows of 32003 fp32 columns
 // 10.5 us unsplit and 13.8 us split.
 constexpr int kMinPart = 1024;
 constexpr int64_t kMinSplit = 98304;
