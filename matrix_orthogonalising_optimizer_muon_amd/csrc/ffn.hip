@@ -27,6 +27,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "ffn_reads.hpp"
 #include "mfma_util.hpp"
 #include "train.hpp"
 
@@ -315,12 +316,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
     b_ptr += n0 * ldb * ES;
     b_k = kt0 * BK * ES;
   }
-  // Buffer bounds in bytes, rounded up to whole chunks: rows are 16-byte aligned, so such a
-  // chunk shares its page with a valid element.
-  auto bytes_of = [&](int rows, int64_t ld, int last) {
-    const int b = static_cast<int>(((rows - 1) * ld + last) * ES + 15) & ~15;
-    return rows > 0 ? b : 0;
-  };
+  auto bytes_of = [&](int rows, int64_t ld, int last) { return ffn_bytes(rows, ld, last, ES); };
   const int a_bytes = AS ? 0 : bytes_of(min(M - m0, BM), lda, p.KA);
   const int b_bytes = BS ? 0 : bytes_of(min(N - n0, DUAL ? BN / 2 : BN), ldb, p.K);
   const auto rb1 = make_rsrc(DUAL ? static_cast<const char*>(p.B[1]) + n0 * p.ldb1 * ES : b_ptr,
