@@ -267,7 +267,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
       a_off[j] = static_cast<uint32_t>((k * lda + swz_strided<KIND, BM>(k, at % (BM / VEC)) * VEC) * ES);
     } else {
       const int row = at / CH;
-      a_off[j] = static_cast<uint32_t>((min(row, M - m0 - 1) * lda + ((at % CH) ^ swz_bits<CH>(row)) * VEC) * ES);
+      a_off[j] = static_cast<uint32_t>((ffn_row(row, M - m0) * lda + ((at % CH) ^ swz_bits<CH>(row)) * VEC) * ES);
     }
   }
 #pragma unroll
@@ -281,10 +281,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
       const int c = ((at % CH) ^ swz_bits<CH>(row)) * VEC;
       if constexpr (DUAL) {
         // rows 16 t .. 16 t + 7 of the tile come from Wg, the next 8 from Wu (same columns of g and u)
-        const int f = min((row >> 4) * 8 + (row & 7), N - n0 - 1);
+        const int f = ffn_row((row >> 4) * 8 + (row & 7), N - n0);
         b_off[j] = static_cast<uint32_t>((f * ((row & 8) ? p.ldb1 : ldb) + c) * ES);
       } else {
-        b_off[j] = static_cast<uint32_t>((min(row, N - n0 - 1) * ldb + c) * ES);
+        b_off[j] = static_cast<uint32_t>((ffn_row(row, N - n0) * ldb + c) * ES);
       }
     }
   }
@@ -292,7 +292,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
   // Where the next slice starts. K-contiguous: a byte offset along the rows of one buffer;
   // K-strided: a pointer, and how many rows are left. Slices are loaded in order, and up to
   // NS - 1 past the last one: those land in stages that are not read, and past an operand's
-  // end they read zeros.
+  // end they read zeros through an empty bound (ffn_reads.hpp).
   const char* a_ptr = static_cast<const char*>(A);
   const char* b_ptr = static_cast<const char*>(B);
   int a_k = 0, b_k = 0;      // K-contiguous: byte offset
@@ -319,16 +319,18 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
   auto bytes_of = [&](int rows, int64_t ld, int last) { return ffn_bytes(rows, ld, last, ES); };
   const int a_bytes = AS ? 0 : bytes_of(min(M - m0, BM), lda, p.KA);
   const int b_bytes = BS ? 0 : bytes_of(min(N - n0, DUAL ? BN / 2 : BN), ldb, p.K);
-  const auto rb1 = make_rsrc(DUAL ? static_cast<const char*>(p.B[1]) + n0 * p.ldb1 * ES : b_ptr,
-                             DUAL ? bytes_of(min(N - n0, BN / 2), p.ldb1, p.K) : 0);
+  const char* b1_ptr = DUAL ? static_cast<const char*>(p.B[1]) + n0 * p.ldb1 * ES : nullptr;
+  const int b1_bytes = DUAL ? bytes_of(min(N - n0, BN / 2), p.ldb1, p.K) : 0;
+  const int a_end = ffn_end(a_bytes, p.KA, ES), b_end = ffn_end(b_bytes, p.K, ES);
 
   auto issue = [&](int stage) {
     u32x4* sa = lds + stage * STAGE + wave * IA * 64;
     u32x4* sb = lds + stage * STAGE + BM * CH + wave * IB * 64;
     {
-      const auto r = make_rsrc(a_ptr, AS ? bytes_of(min(a_rows, BK), lda, M - m0) : a_bytes);
+      const FfnWindow w = AS ? FfnWindow{bytes_of(min(a_rows, BK), lda, M - m0), 0} : ffn_window(a_k, a_end, a_bytes);
+      const auto r = make_rsrc(a_ptr, w.bytes);
 #pragma unroll
-      for (int j = 0; j < IA; ++j) buf_load_lds(r, sa + j * 64, a_off[j], a_k);
+      for (int j = 0; j < IA; ++j) buf_load_lds(r, sa + j * 64, a_off[j], w.at);
       if constexpr (AS) {
         a_ptr += static_cast<int64_t>(BK * ES) * lda;
         a_rows -= BK;
@@ -336,16 +338,19 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void ffn_gemm(const FfnGemm p) {
         a_k += BK * ES;
       }
     }
-    const auto r = make_rsrc(b_ptr, BS ? bytes_of(min(b_rows, BK), ldb, N - n0) : b_bytes);
+    const FfnWindow w = BS ? FfnWindow{bytes_of(min(b_rows, BK), ldb, N - n0), 0} : ffn_window(b_k, b_end, b_bytes);
+    const auto r = make_rsrc(b_ptr, w.bytes);
     if constexpr (DUAL) {
+      const FfnWindow w1 = ffn_window(b_k, b_end, b1_bytes);
+      const auto r1 = make_rsrc(b1_ptr, w1.bytes);
 #pragma unroll
       for (int j = 0; j < IB; ++j) {
-        if ((wave * IB + j) & 1) buf_load_lds(rb1, sb + j * 64, b_off[j], b_k);
-        else buf_load_lds(r, sb + j * 64, b_off[j], b_k);
+        if ((wave * IB + j) & 1) buf_load_lds(r1, sb + j * 64, b_off[j], w1.at);
+        else buf_load_lds(r, sb + j * 64, b_off[j], w.at);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < IB; ++j) buf_load_lds(r, sb + j * 64, b_off[j], b_k);
+      for (int j = 0; j < IB; ++j) buf_load_lds(r, sb + j * 64, b_off[j], w.at);
     }
     if constexpr (BS) {
       b_ptr += static_cast<int64_t>(BK * ES) * ldb;
