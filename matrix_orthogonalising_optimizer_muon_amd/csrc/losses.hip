@@ -92,7 +92,9 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b, float c) {
 
 // Reductions over 16 lanes by lane permutes within the vector instruction (neighbours,
 // pairs, halves of 8, halves of 16; every lane ends with the result), the rest of a wave by
-// two shuffles.
+// two shuffles. No contraction in the sums: fused with the product that made v, the first addition
+// would round each lane's own product differently from its neighbour's, and the lanes would end
+// with different last bits.
 template <int CTRL>
 __device__ __forceinline__ float permuted(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
@@ -104,6 +106,7 @@ __device__ __forceinline__ float max16(float v) {
   return fmaxf(v, permuted<0x140>(v));  // mirrored in 16
 }
 __device__ __forceinline__ float sum16(float v) {
+#pragma clang fp contract(off)
   v += permuted<0xB1>(v);
   v += permuted<0x4E>(v);
   v += permuted<0x141>(v);
@@ -115,6 +118,7 @@ __device__ __forceinline__ float max64(float v) {
   return fmaxf(v, __shfl_xor(v, 32));
 }
 __device__ __forceinline__ float sum64(float v) {
+#pragma clang fp contract(off)
   v = sum16(v);
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
