@@ -427,19 +427,26 @@ int muon_ffn_backward(muon_ctx *ctx, const muon_ffn *f, const muon_ffn_grads *g,
  * (same stride; the gradient replaces the logits); any other overlap is refused. With lse_given
  * the normaliser is read from lse instead of computed (one pass less): a backward after a
  * forward that kept it. Without a gradient and with lse given only the rows' own entries are
- * read. */
+ * read.
+ * lse_pairs: lse holds two floats a row, the largest logit m and sum exp((logits - m) /
+ * temperature). Given, they yield what computing them would, whatever the row holds. As one
+ * float, log sum exp z is rounded to 2^-24 of itself and so is every q_v relative to its
+ * size: enough for rows with |lse| up to some hundreds, wrong for rows of a mask's -1e9 or of
+ * the type's lowest value, where the log of the sum is lost. */
 typedef struct muon_logits {
   const void *logits;
   void *dlogits;
   const float *weights;    /* rows, or null: 1 */
   const float *grad_rows;  /* rows, or null: 1 */
   float *loss;             /* rows, or null */
-  float *lse;              /* rows: log sum exp z (0 for rows that take no part), or null */
+  float *lse;              /* rows: log sum exp z, or rows x 2 (lse_pairs; 0 for rows that take no
+                            * part), or null */
   int64_t ld, ld_d;
   int64_t rows, vocab;
   float temperature;       /* finite, > 0, and 2 / temperature finite */
   int32_t dtype;           /* MUON_F32 or MUON_BF16 */
   int32_t lse_given;       /* 0 or 1 */
+  int32_t lse_pairs;       /* 0 or 1 */
 } muon_logits;
 
 /* Bytes of workspace (256-byte aligned; 0: none, null is accepted) muon_policy_loss (top 0) or

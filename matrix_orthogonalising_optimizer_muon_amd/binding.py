@@ -120,7 +120,7 @@ class muon_logits(ctypes.Structure):
                 ("grad_rows", ctypes.c_void_p), ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p),
                 ("ld", ctypes.c_int64), ("ld_d", ctypes.c_int64), ("rows", ctypes.c_int64),
                 ("vocab", ctypes.c_int64), ("temperature", ctypes.c_float), ("dtype", ctypes.c_int32),
-                ("lse_given", ctypes.c_int32)]
+                ("lse_given", ctypes.c_int32), ("lse_pairs", ctypes.c_int32)]
 
 
 class muon_policy(ctypes.Structure):

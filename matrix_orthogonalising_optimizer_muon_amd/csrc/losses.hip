@@ -265,7 +265,10 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
   if (w == 0.0f || target < 0 || target >= V) {
     if (first) {
       if (p.loss) p.loss[r] = 0.0f;
-      if (!p.lse_given && p.lse) p.lse[r] = 0.0f;
+      if (!p.lse_given && p.lse) {
+        if (p.lse_pairs) p.lse[2 * r] = p.lse[2 * r + 1] = 0.0f;
+        else p.lse[r] = 0.0f;
+      }
       if (LOSS == LOSS_POLICY && p.logp) p.logp[r] = 0.0f;
     }
     if (d) {
@@ -385,22 +388,26 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     }
   }
 
-  // m and s: q_v = exp2((z_v - m) c) / s, log2 of the normaliser (m c + log2 s).
-  float m, inv_s, log2s;
-  if (p.lse_given) {
-    m = 0.0f;
-    log2s = p.lse[r] * kLog2e;
-    inv_s = 1.0f;
+  // m and s: q_v = exp2((z_v - m) c) / s, log2 s. From a kept pair they are the values the
+  // forward had, so that its backward computes what the pass over the row would have: one float
+  // for both would lose log s beside a large m (a row of -1e9 has q = 1, not 1 / V, from it).
+  float m, s, log2s;
+  if (p.lse_given && p.lse_pairs) {
+    m = p.lse[2 * r];
+    s = p.lse[2 * r + 1];
+    log2s = __builtin_amdgcn_logf(s);
+  } else if (p.lse_given) {
+    m = p.lse[r] * p.temperature;
+    s = 1.0f;
+    log2s = 0.0f;
   } else if constexpr (SPLIT) {
     // every wave joins the parts in the same order (at most 64, one a lane)
     const int lane = tid & 63;
     Stat st{-INFINITY, 0.0f};
     if (lane < p.splits) st = Stat{p.stats[(r * p.splits + lane) * 2], p.stats[(r * p.splits + lane) * 2 + 1]};
     m = max64(st.m);
-    st.s = sum64(st.s * __builtin_amdgcn_exp2f((st.m - base_of(m)) * c));
-    log2s = __builtin_amdgcn_logf(st.s);
-    inv_s = 1.0f / st.s;
-    if (first && p.lse) p.lse[r] = m * p.inv_temperature + log2s * kLn2;
+    s = sum64(st.s * __builtin_amdgcn_exp2f((st.m - base_of(m)) * c));
+    log2s = __builtin_amdgcn_logf(s);
   } else {
     Stat st{-INFINITY, 0.0f};
     // one rescale of the running sum per G vectors
@@ -442,9 +449,16 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     if (tail < V) st = join(st, Stat{zl, zl == zl ? 1.0f : zl}, c);
     st = join_all<THREADS>(st, c, sh.row);
     m = st.m;
-    log2s = __builtin_amdgcn_logf(st.s);
-    inv_s = 1.0f / st.s;
-    if (first && p.lse) p.lse[r] = m * p.inv_temperature + log2s * kLn2;
+    s = st.s;
+    log2s = __builtin_amdgcn_logf(s);
+  }
+  if (first && p.lse && !p.lse_given) {
+    if (p.lse_pairs) {
+      p.lse[2 * r] = m;
+      p.lse[2 * r + 1] = s;
+    } else {
+      p.lse[r] = m * p.inv_temperature + log2s * kLn2;
+    }
   }
 
   const float scale = w * up * p.inv_temperature;
@@ -506,14 +520,13 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     wait_vmcnt<0>();
     __syncthreads();
   }
-  const float cq = coef * inv_s;
-  const float shift = p.lse_given ? log2s : 0.0f;
+  const float cq = coef * (1.0f / s);
   auto give = [&](const u32x4& vec, int i) {
     const int64_t at = static_cast<int64_t>(i) * VEC;
     float v[VEC];
     R::unpack(vec, v);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = cq * __builtin_amdgcn_exp2f((v[e] - m) * c - shift);
+    for (int e = 0; e < VEC; ++e) v[e] = cq * __builtin_amdgcn_exp2f((v[e] - m) * c);
     R::store(d + at, v);
   };
   if constexpr (NV > 0) {
@@ -528,7 +541,7 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     for (int i = v0 + tid; i < v1; i += THREADS) give(R::load(z + static_cast<int64_t>(i) * VEC), i);
   }
   if (tail < V) {
-    float v = cq * __builtin_amdgcn_exp2f((zl - m) * c - shift);
+    float v = cq * __builtin_amdgcn_exp2f((zl - m) * c);
     d[tail] = R::to(v);
   }
   if constexpr (LOSS == LOSS_POLICY) {
@@ -537,7 +550,7 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     const int v = static_cast<int>(target) / VEC;
     const int owner = v >= full ? static_cast<int>(target) - full * VEC : (v - v0) % THREADS;
     if (v >= v0 && (last_part || v < v1) && tid == owner)
-      d[target] = R::to(cq * __builtin_amdgcn_exp2f((zt - m) * c - shift) - coef);
+      d[target] = R::to(cq * __builtin_amdgcn_exp2f((zt - m) * c) - coef);
   }
   if constexpr (LOSS == LOSS_DISTILL) {
     // The kept columns again, with the teacher's part, by the thread that wrote them above:
@@ -545,7 +558,7 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
     // of the row's stores: 2048 rows of 152064 took 299 us that way.)
     for (int j = head[tid]; j >= 0; j = next_of[j])
       if (!(fix_of[j] < 0.0f))
-        d[col[j]] = R::to(cq * __builtin_amdgcn_exp2f((lp_of[j] - m) * c - shift) - fix_of[j] * scale);
+        d[col[j]] = R::to(cq * __builtin_amdgcn_exp2f((lp_of[j] - m) * c) - fix_of[j] * scale);
     distill_row();
   }
 }

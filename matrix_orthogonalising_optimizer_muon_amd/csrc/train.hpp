@@ -76,12 +76,12 @@ struct LossParams {
   void* dlogits; int64_t ld_d;      // null: no gradient
   int64_t rows;
   int32_t vocab;
-  float inv_temperature;
+  float temperature, inv_temperature;
   const float* weights;             // null: 1
   const float* grad_rows;           // null: 1
   float* loss;                      // null: not written
   float* lse;                       // written, or read with lse_given; may be null otherwise
-  int32_t lse_given;
+  int32_t lse_given, lse_pairs;     // pairs: [rows][2], the largest logit and the sum
   // policy
   const int64_t* targets;
   const float* old_logp; const float* advantages; const float* ref_logp;

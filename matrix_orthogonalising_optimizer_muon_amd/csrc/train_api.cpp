@@ -303,7 +303,7 @@ int validate(const muon_logits* l) {
   if (l->ld < l->vocab || (l->dlogits && l->ld_d < l->vocab)) return MUON_ERR_ARG;
   if (!std::isfinite(l->temperature) || !(l->temperature > 0.0f) || !std::isfinite(2.0f / l->temperature))
     return MUON_ERR_ARG;
-  if (l->lse_given != 0 && l->lse_given != 1) return MUON_ERR_ARG;
+  if ((l->lse_given != 0 && l->lse_given != 1) || (l->lse_pairs != 0 && l->lse_pairs != 1)) return MUON_ERR_ARG;
   const int64_t es = size_of(l->dtype);
   if (!aligned(l->logits, es) || !aligned(l->dlogits, es)) return MUON_ERR_ARG;
   if (l->rows > 0 && (!l->logits || (l->lse_given && !l->lse))) return MUON_ERR_ARG;
@@ -355,9 +355,10 @@ LossParams params(const muon_logits* l) {
   p.dlogits = l->dlogits; p.ld_d = l->ld_d;
   p.rows = l->rows;
   p.vocab = static_cast<int32_t>(l->vocab);
+  p.temperature = l->temperature;
   p.inv_temperature = 1.0f / l->temperature;
   p.weights = l->weights; p.grad_rows = l->grad_rows;
-  p.loss = l->loss; p.lse = l->lse; p.lse_given = l->lse_given;
+  p.loss = l->loss; p.lse = l->lse; p.lse_given = l->lse_given; p.lse_pairs = l->lse_pairs;
   return p;
 }
 

@@ -4,8 +4,8 @@
 ``policy_loss`` and ``distill_loss`` return the rows' losses and, in the same pass over the
 logits, the gradient of their sum; with ``out`` it goes to a given tensor, which may be the
 logits themselves. ``policy_loss_rows`` and ``distill_loss_rows`` are the same losses for
-torch's automatic differentiation (the forward keeps one normaliser per row, the backward
-reads the logits once more). A row whose weight is 0 takes no part: its logits are not read,
+torch's automatic differentiation (the forward keeps each row's maximum and sum, the backward
+reads the logits once more and computes what the one call does). A row whose weight is 0 takes no part: its logits are not read,
 its loss and gradient are 0. Logits may have any leading dimensions and row stride; per-row
 operands are float32, contiguous, one value per row. Work is enqueued on the current stream
 of the logits' device.
@@ -20,7 +20,7 @@ from .context import context, dtype_code, matrix, new_like, on_gpu, stream_of, v
 
 
 def _rows(logits, weights, temperature, out=None, loss=None, lse=None, lse_given=False, grad_rows=None):
-    """(muon_logits, logits as rows x vocab, device) after the checks."""
+    """(muon_logits, logits as rows x vocab, device) after the checks. ``lse``: the rows' pairs."""
     code = dtype_code(logits, "logits")
     device = on_gpu(logits, "logits")
     if logits.dim() < 1:
@@ -39,7 +39,7 @@ def _rows(logits, weights, temperature, out=None, loss=None, lse=None, lse_given
                       None if grad_rows is None else vector(grad_rows, "grad_rows", rows, f32, device),
                       None if loss is None else loss.data_ptr(), None if lse is None else lse.data_ptr(),
                       matrix(z, "logits", z.shape, logits.dtype, device), ld_d or 0, rows, vocab, temperature, code,
-                      int(lse_given))
+                      int(lse_given), int(lse is not None))
     return l, z, device
 
 
@@ -116,8 +116,8 @@ def distill_loss(logits, top_logits, top_ids, *, top_lse=None, weights=None, tem
 class _PolicyLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, targets, old_logp, advantages, ref_logp, weights, clip_low, clip_high, kl_coef, temperature):
-        new = lambda: torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)  # noqa: E731
-        loss, logp, lse = new(), new(), new()
+        new = lambda *n: torch.empty((*logits.shape[:-1], *n), dtype=torch.float32, device=logits.device)  # noqa: E731
+        loss, logp, lse = new(), new(), new(2)
         l, z, device = _rows(logits, weights, temperature, None, loss, lse)
         t = _policy(z, device, targets, old_logp, advantages, ref_logp, clip_low, clip_high, kl_coef, logp)
         _call(B.muon_policy_loss, "muon_policy_loss", device, l, t, 0)
@@ -149,8 +149,8 @@ def policy_loss_rows(logits, targets, old_logp, advantages, *, ref_logp=None, we
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_logits, top_ids, top_lse, weights, temperature):
-        new = lambda: torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)  # noqa: E731
-        loss, lse = new(), new()
+        new = lambda *n: torch.empty((*logits.shape[:-1], *n), dtype=torch.float32, device=logits.device)  # noqa: E731
+        loss, lse = new(), new(2)
         l, z, device = _rows(logits, weights, temperature, None, loss, lse)
         t, keep = _distill(z, device, top_logits, top_ids, top_lse)
         _call(B.muon_distill_loss, "muon_distill_loss", device, l, t, t.top)

@@ -25,18 +25,21 @@ def _softmax(z):
 
 
 def _normaliser_error(z, q, m, lse, lse_given):
-    """Relative error of the normaliser, and of each q_v on top of it. The fp32 difference,
-    its product with the scale (itself rounded) and the exponential's argument each carry
-    2^-24 of |z - m|; the exponential and the sums (at most V / 256 terms in a chain, and the
-    joins) a few 2^-24 more. A given lse carries its own rounding and that of its product."""
+    """Errors of the normaliser: of lse as one float; of log q_v by what the normaliser
+    contributes; relative, of each q_v. The fp32 difference z - m, its product with the scale
+    (itself rounded) and the exponential's argument each carry 2^-24 of |z - m|; the
+    exponential and the sums (at most V / 256 terms in a chain, and the joins) a few 2^-24
+    more; neither |z| nor |lse| enters. lse_given: lse is read as one float, whose own
+    rounding, and that of its product with the temperature, counts in every difference z - lse."""
     with np.errstate(invalid="ignore"):
         far = np.where(q > 0, np.abs(z - m), 0.0)
-        big = np.where(q > 0, np.abs(z), 0.0)
+        off = np.where(q > 0, np.abs(z - lse), 0.0)
     s_err = U * (4.0 * float((q * far).sum()) + z.size / 256 + 60.0)
     lse_err = s_err + U * (4.0 * abs(lse) + 4.0 * abs(m))
     if lse_given:
-        return lse_err, lse_err + U * (4.0 * big + 4.0 * abs(lse) + 8.0)
-    return lse_err, s_err + U * (4.0 * far + 8.0)
+        one = lse_err + 3.0 * U * abs(lse)
+        return lse_err, one, one + U * (5.0 * off + 8.0)
+    return lse_err, s_err, s_err + U * (4.0 * far + 8.0)
 
 
 def policy(logits, targets, old, adv, ref=None, weights=None, grad_rows=None, *, clip_low, clip_high, kl_coef,
@@ -54,9 +57,11 @@ def policy(logits, targets, old, adv, ref=None, weights=None, grad_rows=None, *,
         z = np.asarray(logits[r], np.float64) / temperature
         m, q, logs = _softmax(z)
         lse = m + logs
-        e_lse, e_q = _normaliser_error(z, q, m, lse, lse_given)
+        e_lse, e_norm, e_q = _normaliser_error(z, q, m, lse, lse_given)
         lp = (z[t] - m) - logs   # not z_t - lse: m may be the type's lowest value
-        e_lp = e_lse + U * (6.0 * abs(z[t] - m) + 4.0 * abs(lp) + 4.0 * abs(z[t]))
+        # (z_t - m) c: five roundings of |z_t - m|; log2 s (at most |lp|) two, the difference and
+        # its product with ln 2 three of |lp|
+        e_lp = e_norm + U * (6.0 * abs(z[t] - m) + 6.0 * abs(lp))
         A, d_old = float(adv[r]), lp - float(old[r])
         rho = np.exp(d_old)
         cut = min(max(rho, 1.0 - clip_low), 1.0 + clip_high)
@@ -99,7 +104,7 @@ def distill(logits, top, ids, top_lse=None, weights=None, grad_rows=None, *, tem
         z = np.asarray(logits[r], np.float64) / temperature
         m, q, logs = _softmax(z)
         lse = m + logs
-        e_lse, e_q = _normaliser_error(z, q, m, lse, lse_given)
+        e_lse, e_norm, e_q = _normaliser_error(z, q, m, lse, lse_given)
         there = (ids[r] >= 0) & (ids[r] < V) & (top[r] > -np.inf)
         at = ids[r][there].astype(int)
         t = np.asarray(top[r], np.float64)[there] / temperature
@@ -114,7 +119,7 @@ def distill(logits, top, ids, top_lse=None, weights=None, grad_rows=None, *, tem
                         + t.size / 64 + 60.0)
             e_p = p * (e_lp + 4.0 * U)
             lq = (z[at] - m) - logs
-            e_lq = e_lse + U * (6.0 * np.abs(z[at] - m) + 6.0 * np.abs(lq) + 4.0 * np.abs(z[at]))
+            e_lq = e_norm + U * (6.0 * np.abs(z[at] - m) + 6.0 * np.abs(lq))
             terms = p * (lp - lq)
             l, mass = terms.sum(), p.sum()
             e_l = (e_p * np.abs(lp - lq) + p * (e_lp + e_lq) + 8.0 * U * p * (np.abs(lp) + np.abs(lq))).sum()

@@ -1,10 +1,17 @@
-"""What the losses' threads hold of a row: one normaliser, to the last bit."""
+"""The losses under automatic differentiation on rows whose values are far from 0: masks of the
+type's lowest value, fills of -1e9, common offsets. The backward works from what the forward
+kept of a row; its gradient is the one-pass call's."""
 
 import numpy as np
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+
+from oracle import losses as ol  # noqa: E402
+from tests.gpu_util import TORCH_DT, to_np  # noqa: E402
+
+HALF_STEP = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 
 
 @pytest.fixture(scope="module")
@@ -15,6 +22,85 @@ def S():
 
 def cuda(a, dtype=torch.float32):
     return torch.from_numpy(np.ascontiguousarray(a)).cuda().to(dtype)
+
+
+def inside(got, ref, bound, what):
+    err = np.abs(to_np(got) - ref)
+    bad = ~(err <= bound)
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:3].tolist(), to_np(got)[bad][:3], ref[bad][:3], bound[bad][:3])
+
+
+def far_rows(V, dtype):
+    """Logits whose rows differ in where their values lie, and a target in each."""
+    rng = np.random.default_rng([3, V])
+    z = torch.from_numpy((2.5 * rng.standard_normal((9, V))).astype(np.float32))
+    lowest = torch.finfo(TORCH_DT[dtype]).min
+    t = rng.integers(0, V, 9)
+    mask = torch.from_numpy(rng.random((9, V)) < 0.5)
+    mask[torch.arange(9), torch.from_numpy(t)] = False
+    z[1] = lowest                      # the mask leaves nothing
+    z[2] = -1e9
+    z[3][mask[3]] = lowest
+    z[4] += 1e4
+    z[5] -= 1e5
+    z[6][mask[6]] = float("-inf")
+    z[7] = -2e38
+    z[8][mask[8]] = -1e9
+    return z.cuda().to(TORCH_DT[dtype]), t
+
+
+SIZES = [8, 700, 40000, 152064, 262147]   # held by a thread, by a workgroup, in parts, read twice
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", [1.0, 0.7])
+@pytest.mark.parametrize("V", SIZES)
+def test_policy_rows_far_from_zero(S, V, temperature, dtype):
+    z, t = far_rows(V, dtype)
+    zz = to_np(z) / temperature
+    d = [zz[r] - zz[r].max() for r in range(len(t))]
+    lp = np.array([d[r][t[r]] - np.log(np.exp(d[r]).sum()) for r in range(len(t))])
+    rng = np.random.default_rng(5)
+    old, adv, ref = cuda(lp - 0.05), cuda(rng.standard_normal(len(t))), cuda(lp + 0.2)
+    kw = dict(clip_low=0.2, clip_high=0.28, kl_coef=0.1, temperature=temperature)
+    loss, logp, grad = S.policy_loss(z, cuda(t, torch.int64), old, adv, ref_logp=ref, **kw)
+    leaf = z.clone().requires_grad_(True)
+    loss2, logp2 = S.policy_loss_rows(leaf, cuda(t, torch.int64), old, adv, ref_logp=ref, **kw)
+    assert torch.equal(loss, loss2) and torch.equal(logp, logp2)
+    got, = torch.autograd.grad(loss2.sum(), leaf, retain_graph=True)
+    assert bool(torch.isfinite(got).all())
+    assert torch.equal(got, grad)      # upstream gradient 1: the same arithmetic on the same row
+    up = torch.linspace(-1.0, 2.0, len(t), device="cuda")
+    got, = torch.autograd.grad((loss2 * up).sum(), leaf)
+    want = ol.policy(to_np(z), t, to_np(old), to_np(adv), to_np(ref), None, to_np(up), **kw, half_step=HALF_STEP[dtype])
+    inside(got, want["grad"], want["err_grad"], "grad")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", [1.0, 0.7])
+@pytest.mark.parametrize("V", SIZES)
+def test_distill_rows_far_from_zero(S, V, temperature, dtype):
+    z, t = far_rows(V, dtype)
+    rng = np.random.default_rng([6, V])
+    K = min(V, 40)
+    ids = np.stack([rng.permutation(V)[:K] for _ in t])
+    ids[:, 0] = t
+    zz = to_np(z)
+    # the teacher keeps nothing where the student is masked with -inf (its loss would be infinite)
+    ids[np.isinf(np.take_along_axis(zz, ids, 1))] = -1
+    top, ids = cuda(2.0 * rng.standard_normal((len(t), K)) + 5.0), cuda(ids, torch.int64)
+    loss, grad = S.distill_loss(z, top, ids, temperature=temperature)
+    leaf = z.clone().requires_grad_(True)
+    loss2 = S.distill_loss_rows(leaf, top, ids, temperature=temperature)
+    assert torch.equal(loss, loss2)
+    got, = torch.autograd.grad(loss2.sum(), leaf, retain_graph=True)
+    assert bool(torch.isfinite(got).all())
+    assert torch.equal(got, grad)
+    up = torch.linspace(-1.0, 2.0, len(t), device="cuda")
+    got, = torch.autograd.grad((loss2 * up).sum(), leaf)
+    want = ol.distill(zz, to_np(top), ids.cpu().numpy(), None, None, to_np(up), temperature=temperature,
+                      half_step=HALF_STEP[dtype])
+    inside(got, want["grad"], want["err_grad"], "grad")
 
 
 @pytest.mark.parametrize("temperature", [1.0, 0.7])
