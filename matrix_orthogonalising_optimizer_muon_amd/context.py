@@ -41,6 +41,14 @@ def new_like(t: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
+def written(*tensors) -> None:
+    """Tells torch's automatic differentiation that a call has written given tensors (through
+    their addresses, which it does not see): a node that saved one refuses its backward."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def dtype_code(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")

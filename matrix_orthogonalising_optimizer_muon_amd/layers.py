@@ -21,7 +21,7 @@ import math
 import torch
 
 from . import binding as B
-from .context import context, dtype_code, matrix, new_like, on_gpu, stream_of
+from .context import context, dtype_code, matrix, new_like, on_gpu, stream_of, written
 
 
 def _block(x, w_gate, w_up, w_down, activation):
@@ -89,7 +89,7 @@ def ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, activation: str = "silu"
     return _backward(dy, x, w_gate, w_up, w_down, saved, activation, grads, accumulate, need_dx, grads is not None)
 
 
-def _backward(dy, x, w_gate, w_up, w_down, saved, activation, grads, accumulate, need_dx, check_overlap):
+def _backward(dy, x, w_gate, w_up, w_down, saved, activation, grads, accumulate, need_dx, given_buffers):
     f, x2, device = _block(x, w_gate, w_up, w_down, activation)
     dy2 = dy if dy.dim() == 2 else dy.reshape(-1, f.dim)
     shapes = (w_gate.shape, w_up.shape, w_down.shape)
@@ -106,7 +106,7 @@ def _backward(dy, x, w_gate, w_up, w_down, saved, activation, grads, accumulate,
     if not saved.is_contiguous():
         raise ValueError("saved must be contiguous")
     ld_dy = matrix(dy2, "dy", x2.shape, x.dtype, device)
-    if check_overlap:
+    if given_buffers:
         outs, ins = _spans(grads), _spans((dy2, x2, w_gate, w_up, w_down, saved.view(1, -1)))
         if any(_overlap(o, t) for i, o in enumerate(outs) for t in ins + outs[:i]):
             raise ValueError("the gradient buffers (grads) overlap each other or an operand")
@@ -120,6 +120,8 @@ def _backward(dy, x, w_gate, w_up, w_down, saved, activation, grads, accumulate,
         raise ValueError(f"saved has {saved.numel()} elements, this block's forward wrote {nsaved // 4}")
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     B.check(B.muon_ffn_backward(ctx, f, g, ws.data_ptr(), nbytes, stream_of(device)), "muon_ffn_backward")
+    if given_buffers:
+        written(*grads)
     return (dx, *grads)
 
 

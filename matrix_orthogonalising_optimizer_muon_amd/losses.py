@@ -16,7 +16,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .context import context, dtype_code, matrix, new_like, on_gpu, stream_of, vector
+from .context import context, dtype_code, matrix, new_like, on_gpu, stream_of, vector, written
 
 
 def _rows(logits, weights, temperature, out=None, loss=None, lse=None, lse_given=False, grad_rows=None):
@@ -89,11 +89,13 @@ def policy_loss(logits, targets, old_logp, advantages, *, ref_logp=None, weights
     lead = logits.shape[:-1]
     loss = torch.empty(lead, dtype=torch.float32, device=logits.device)
     logp = torch.empty(lead, dtype=torch.float32, device=logits.device)
+    given = out if grad else None
     if grad and out is None:
         out = new_like(logits)
     l, z, device = _rows(logits, weights, temperature, out if grad else None, loss)
     t = _policy(z, device, targets, old_logp, advantages, ref_logp, clip_low, clip_high, kl_coef, logp)
     _call(B.muon_policy_loss, "muon_policy_loss", device, l, t, 0)
+    written(given)
     return loss, logp, out if grad else None
 
 
@@ -105,11 +107,13 @@ def distill_loss(logits, top_logits, top_ids, *, top_lse=None, weights=None, tem
     the student's probabilities; and the gradient of the losses' sum by the logits (None
     without ``grad``). Entries with an id outside the vocabulary are absent."""
     loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
+    given = out if grad else None
     if grad and out is None:
         out = new_like(logits)
     l, z, device = _rows(logits, weights, temperature, out if grad else None, loss)
     t, keep = _distill(z, device, top_logits, top_ids, top_lse)
     _call(B.muon_distill_loss, "muon_distill_loss", device, l, t, t.top)
+    written(given)
     return loss, out if grad else None
 
 
