@@ -185,10 +185,14 @@ FfnPlan plan_of(const muon_ffn* f, const muon_ffn_grads* g, int cus) {
   if (T == 0) return p;  // nothing is launched on tiles
   Arena a;
   const size_t inter = static_cast<size_t>(T * p.Hp * p.es);
-  p.x = operand(f->x, f->ld_x, T, D, p.es, a);
+  // a backward reads x for the gradients of gate and up alone, and gate and up for dx alone
+  const bool need_x = !g || g->g_gate || g->g_up, need_gate_up = !g || g->dx;
+  if (need_x) p.x = operand(f->x, f->ld_x, T, D, p.es, a);
   p.wd = operand(f->w_down, f->ld_down, D, F, p.es, a);
-  p.wg = operand(f->w_gate, f->ld_gate, F, D, p.es, a);
-  p.wu = operand(f->w_up, f->ld_up, F, D, p.es, a);
+  if (need_gate_up) {
+    p.wg = operand(f->w_gate, f->ld_gate, F, D, p.es, a);
+    p.wu = operand(f->w_up, f->ld_up, F, D, p.es, a);
+  }
   if (g && g->dx && p.wg.ld != p.wu.ld) {
     // dx reads them as the two K segments of one operand: one row stride
     if (!p.wg.copied) p.wg = operand(f->w_gate, f->ld_gate, F, D, p.es, a, true);
