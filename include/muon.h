@@ -365,7 +365,9 @@ int muon_adamw_step(muon_ctx *ctx, const muon_adamw_tensor *tensors, int count,
  *     are first copied into the workspace (the feed-forward block) or read as they are
  *     (the losses);
  *   - the calls only read the context: several threads may make them on one context;
- *   - results do not change from run to run (no atomics; fixed summation orders).
+ *   - results do not change from run to run: every sum has a fixed order. (The distillation
+ *     loss links its kept entries into lists with atomics in LDS; their order, which may
+ *     change, touches no value: each entry is dealt with by itself.)
  * These operators are not on the pages the update is built from; the formulas are given. */
 #define MUON_ACT_SILU 0       /* act(g) = g / (1 + exp(-g)) */
 #define MUON_ACT_GELU_TANH 1  /* act(g) = g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */

@@ -121,3 +121,16 @@ def test_equal_logits_have_equal_gradients(S, half, temperature):
     a, b = grad[:, :half].clone(), grad[:, half:].clone()
     a[at, t], b[at, t] = 0.0, 0.0
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("V", [1500, 152064])
+def test_distill_same_result_every_time(S, V):
+    """1024 kept entries, several to a thread and many of them repeated, in lists of changing order."""
+    rng = np.random.default_rng(8)
+    n, K = 40, 1024
+    z = cuda((2.5 * rng.standard_normal((n, V))).astype(np.float32))
+    top, ids = cuda(2.0 * rng.standard_normal((n, K))), cuda(rng.integers(0, V // 3, (n, K)), torch.int64)
+    first = S.distill_loss(z, top, ids, temperature=2.0)
+    for _ in range(8):
+        again = S.distill_loss(z, top, ids, temperature=2.0)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
