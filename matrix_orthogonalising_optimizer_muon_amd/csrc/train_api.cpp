@@ -301,13 +301,19 @@ bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t row
   return shift < width || shift + width > row;
 }
 
-int validate(const muon_logits* l) {
+// What the workspace's size depends on.
+int validate_sizes(const muon_logits* l) {
   if (!l || !dtype_ok(l->dtype)) return MUON_ERR_ARG;
   if (l->rows < 0 || l->rows > kMaxRows || l->vocab < 1 || l->vocab > (int64_t{1} << 28)) return MUON_ERR_ARG;
+  if ((l->lse_given != 0 && l->lse_given != 1) || (l->lse_pairs != 0 && l->lse_pairs != 1)) return MUON_ERR_ARG;
+  return MUON_OK;
+}
+
+int validate(const muon_logits* l) {
+  if (validate_sizes(l) != MUON_OK) return MUON_ERR_ARG;
   if (l->ld < l->vocab || (l->dlogits && l->ld_d < l->vocab)) return MUON_ERR_ARG;
   if (!std::isfinite(l->temperature) || !(l->temperature > 0.0f) || !std::isfinite(2.0f / l->temperature))
     return MUON_ERR_ARG;
-  if ((l->lse_given != 0 && l->lse_given != 1) || (l->lse_pairs != 0 && l->lse_pairs != 1)) return MUON_ERR_ARG;
   const int64_t es = size_of(l->dtype);
   if (!aligned(l->logits, es) || !aligned(l->dlogits, es)) return MUON_ERR_ARG;
   if (l->rows > 0 && (!l->logits || (l->lse_given && !l->lse))) return MUON_ERR_ARG;
@@ -496,8 +502,7 @@ int muon_ffn_backward(muon_ctx* ctx, const muon_ffn* f, const muon_ffn_grads* g,
 
 int muon_loss_workspace_size(muon_ctx* ctx, const muon_logits* l, int top, size_t* bytes) {
   try {
-    if (!ctx || !l || !bytes || !dtype_ok(l->dtype) || l->rows < 0 || l->vocab < 1 || top < 0 || top > MUON_MAX_TOP)
-      return MUON_ERR_ARG;
+    if (!ctx || !bytes || validate_sizes(l) != MUON_OK || top < 0 || top > MUON_MAX_TOP) return MUON_ERR_ARG;
     *bytes = split_of(l, top > 0 ? top : 1, ctx_cus(ctx)).bytes;
     return MUON_OK;
   } catch (...) {

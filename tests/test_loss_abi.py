@@ -33,3 +33,15 @@ def test_pairs_in_place_of_one_normaliser(hctx):
     for kw, want in [(dict(lse_pairs=1), ok), (dict(lse_pairs=1, lse_given=1), ok), (dict(lse_pairs=1, lse=None), ok),
                      (dict(lse_pairs=1, lse_given=1, lse=None), bad), (dict(lse_pairs=2), bad), (dict(lse_pairs=-1), bad)]:
         assert both(hctx, logits(**kw)) == want, kw
+
+
+def test_workspace_size_of_sizes_that_the_losses_refuse(hctx):
+    """The size query has the losses' own limits: past them it would compute with what overflows."""
+    import ctypes
+    n = ctypes.c_size_t()
+    size = lambda **kw: B._lib.muon_loss_workspace_size(hctx, logits(**kw), 0, n)  # noqa: E731
+    assert size(rows=(1 << 24) - 1) == B.MUON_OK and size(vocab=1 << 28) == B.MUON_OK and size(rows=0) == B.MUON_OK
+    for bad in [dict(rows=1 << 24), dict(rows=1 << 62), dict(vocab=(1 << 28) + 1), dict(vocab=1 << 62), dict(lse_given=2)]:
+        assert size(**bad) == B.MUON_ERR_ARG, bad
+    # it depends on the sizes alone: pointers and strides may still be missing
+    assert size(logits=None, dlogits=None, ld=0, ld_d=0, lse=None) == B.MUON_OK
