@@ -466,7 +466,8 @@ __global__ __launch_bounds__(THREADS) void loss_kernel(const LossParams p) {
   if constexpr (LOSS == LOSS_POLICY) {
     const float lp = ((zt - m) * c - log2s) * kLn2;
     const float rho = __builtin_amdgcn_exp2f((lp - old_logp) * kLog2e);
-    const float kept = rho * adv;
+    // 0 where the advantage is, also where rho has left fp32; a NaN stays
+    const float kept = adv == 0.0f && rho == rho ? 0.0f : rho * adv;
     const float cut = fminf(fmaxf(rho, 1.0f - p.clip_low), 1.0f + p.clip_high) * adv;
     float loss = kept <= cut ? -kept : -cut;
     float slope = kept <= cut ? -kept : 0.0f;

@@ -134,3 +134,23 @@ def test_distill_same_result_every_time(S, V):
     for _ in range(8):
         again = S.distill_loss(z, top, ids, temperature=2.0)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [50, 152064])
+def test_policy_without_advantage_far_from_the_old_policy(S, V, dtype):
+    """rho beyond fp32 (an old log-probability of -200) times an advantage of 0 is 0, and the KL term
+    stays; a NaN ratio stays NaN."""
+    rng = np.random.default_rng([9, V])
+    z = cuda(2.5 * rng.standard_normal((5, V)), TORCH_DT[dtype])
+    t = rng.integers(0, V, 5)
+    zz = to_np(z)
+    lp = np.array([zz[r, t[r]] - zz[r].max() - np.log(np.exp(zz[r] - zz[r].max()).sum()) for r in range(5)])
+    old, adv, ref = cuda([-200.0, -500.0, lp[2] - 0.05, -200.0, float("nan")]), cuda([0.0, 0.0, 0.0, 0.7, 0.0]), cuda(lp + 0.2)
+    kw = dict(clip_low=0.2, clip_high=0.28, kl_coef=0.1, temperature=1.0)
+    loss, logp, grad = S.policy_loss(z, cuda(t, torch.int64), old, adv, ref_logp=ref, **kw)
+    want = ol.policy(zz[:4], t[:4], to_np(old)[:4], to_np(adv)[:4], to_np(ref)[:4], **kw, half_step=HALF_STEP[dtype])
+    inside(loss[:4], want["loss"], want["err_loss"], "loss")
+    inside(logp[:4], want["logp"], want["err_logp"], "logp")
+    inside(grad[:4], want["grad"], want["err_grad"], "grad")
+    assert bool(torch.isnan(loss[4])) and bool(torch.isnan(grad[4]).all())
