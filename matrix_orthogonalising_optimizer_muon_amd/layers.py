@@ -127,8 +127,10 @@ def _backward(dy, x, w_gate, w_up, w_down, saved, activation, grads, accumulate,
 
 class _GatedFFN(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, w_down, activation):
-        y, saved = ffn_forward(x, w_gate, w_up, w_down, activation=activation, save=any(ctx.needs_input_grad))
+    def forward(ctx, x, w_gate, w_up, w_down, activation, grad_mode):
+        # needs_input_grad names what requires a gradient also where no backward can come
+        save = grad_mode and any(ctx.needs_input_grad)
+        y, saved = ffn_forward(x, w_gate, w_up, w_down, activation=activation, save=save)
         ctx.save_for_backward(x, w_gate, w_up, w_down, saved)
         ctx.activation = activation
         return y
@@ -143,12 +145,12 @@ class _GatedFFN(torch.autograd.Function):
                       for w, n in zip(weights, need[1:4]))
         # an expanded dy (of a sum) has no row stride of its own
         out = _backward(dy.contiguous(), x, *weights, saved, ctx.activation, grads, False, need[0], False)
-        return (*out, None)
+        return (*out, None, None)
 
 
 def gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu"):
     """y of the block, differentiable in x and the three weights."""
-    return _GatedFFN.apply(x, w_gate, w_up, w_down, activation)
+    return _GatedFFN.apply(x, w_gate, w_up, w_down, activation, torch.is_grad_enabled())
 
 
 class GatedFeedForward(torch.nn.Module):
