@@ -17,6 +17,11 @@
 //   dx      A = [dg du],   B = [Wg; Wu]      B K-strided, two segments of K
 //   dW      A = [dg du] or dy, B = x or h    both K-strided
 //
+// In bf16, h, dg and du are rounded once, as operands of the next product on the bf16 matrix
+// instructions (in fp32 that product would run at a tenth of the rate); g, u and all sums stay in fp32.
+// Results are off by 2.3e-3 to 2.4e-3 relative to 64 bits that way, 1.6e-3 to 1.7e-3 with fp32
+// intermediates and the one rounding of the result.
+//
 // Operands travel global -> LDS by the direct loads (16 bytes per lane) through a ring of
 // NS stages. A K-contiguous operand lies in LDS as rows of CH chunks and its fragments are
 // 16-byte reads; a K-strided one as BK rows of m (or n), and its 16-bit fragments come
@@ -181,9 +186,10 @@ __device__ __forceinline__ void each(F&& f) {
 
 // The product kernel. Bound by the matrix cores (at the card's power limit) for many tokens,
 // by the weights' HBM traffic for few, by the fill of the ring and the epilogue where K is
-// short. 7B block, 4096 tokens, 256 x 256 tiles: gate 974 us (1142 TFLOP/s), down 443 us (1256),
-// dgate 685 us (812; 1.1 GB of g, u, dg, du, h are not overlapped), dx 908 us (1225), the weight
-// gradients 1470 us (1135). One token, 32 x 32 tiles: 5.2 TB/s. 256 x 256 carries the most products per
+// short. 7B block, 4096 tokens, 256 x 256 tiles, medians of traces on two machines: gate that saves
+// g and u 1035-1131 us (984-1075 TFLOP/s), down 489-502 us (1108-1137), dgate 703-730 us (762-791; 1.1 GB
+// of g, u, dg, du, h are not overlapped), dx 921-926 us (1201-1208), the weight gradients 1535-1545 us
+// (1080-1087). One token, 32 x 32 tiles: 5.2 TB/s. 256 x 256 carries the most products per
 // byte of LDS and L2 traffic; the small tiles exist to keep more CUs at work on small outputs,
 // their k-groups to use a CU's four SIMDs on one tile.
 // KIND: element type of x, weights and outputs. BM x BN output tile, WM x WN waves per

@@ -16,8 +16,8 @@
 // that rows of the type's lowest values stay exact, and q = e / s.
 //
 // Bound by HBM: the logits read once, the gradient written once. 4096 x 151936 bf16, a fifth of
-// the rows without weight: 440 us, 5.1 TB/s (a copy reaches 5.1); 2048 x 152064 with 64 kept
-// entries: 273 us, 4.3 TB/s, where one row a CU at a time leaves the last of 7.2 rounds partly
+// the rows without weight: 437-445 us, 5.1 TB/s (a copy reaches 5.1); 2048 x 152064 with 64 kept
+// entries: 271-278 us, 4.3 TB/s, where one row a CU at a time leaves the last of 7.2 rounds partly
 // idle. The arithmetic (two exponentials a column, about 17 instructions) takes some 18 us a row of
 // 152064 on a CU and hides behind the row's 30 us of traffic.
 #include <type_traits>
@@ -570,7 +570,9 @@ hipError_t launch_as(const LossParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The smallest form that holds the row; a row past the largest is read twice.
+// The smallest form that holds the row; a row past the largest is read twice. 19 vectors a thread are
+// not the registers' limit (100 to 106 of 128; 24 would fit without spills): longer forms have not
+// been measured.
 template <typename E, int LOSS>
 hipError_t launch(const LossParams& p, hipStream_t st) {
   if (p.splits > 1) {

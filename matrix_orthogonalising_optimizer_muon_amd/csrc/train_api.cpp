@@ -331,7 +331,11 @@ int validate(const muon_logits* l) {
 // are about as many workgroups as CUs, with at least kMinPart vectors (16 bytes) a part. It
 // costs a launch, so it is for rows of kMinSplit columns or more: 16 rows of 152064 bf16
 // columns take 25.8 us unsplit and 9.2 us (3.9 + 5.3) split, but 77 rows of 32003 fp32 columns
-// 10.5 us unsplit and 13.8 us split.
+// 10.5 us unsplit and 13.8 us split. On the two sides of the border (98303 columns unsplit, 98304
+// split; us, bf16 then fp32): 1 row 12.8 / 6.8, 14.6 / 6.4; 16 rows 14.6 / 7.4, 15.5 / 8.2; 64 rows
+// 15.8 / 11.8, 21.2 / 17.5; 128 rows 16.7 / 20.1, 26.8 / 30.4. So the border is too high for few rows and
+// the rule too wide above about 100 rows, where a row has only two parts; no border between
+// 32003 and 98304 has been measured.
 constexpr int kMinPart = 1024;
 constexpr int64_t kMinSplit = 98304;
 struct LossSplit {
