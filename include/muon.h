@@ -434,7 +434,8 @@ int muon_ffn_backward(muon_ctx *ctx, const muon_ffn *f, const muon_ffn_grads *g,
  * temperature). Given, they yield what computing them would, whatever the row holds. As one
  * float, log sum exp z is rounded to 2^-24 of itself and so is every q_v relative to its
  * size: enough for rows with |lse| up to some hundreds, wrong for rows of a mask's -1e9 or of
- * the type's lowest value, where the log of the sum is lost. */
+ * the type's lowest value, where the log of the sum is lost. (Given as one float,
+ * lse temperature has to be finite too.) */
 typedef struct muon_logits {
   const void *logits;
   void *dlogits;
