@@ -500,6 +500,132 @@ typedef struct muon_distill {
 int muon_distill_loss(muon_ctx *ctx, const muon_logits *l, const muon_distill *t, void *workspace,
                       size_t workspace_bytes, void *stream);
 
+/* ---- What else a layer's training pass runs: linear attention with a decay for each head, tokens
+ * sorted by expert and back, dropout ----
+ * Conventions as for the other training operators (calls only read the context, results do
+ * not change from run to run, no device memory is allocated). Strides are in elements, any
+ * element alignment is read and written as it is.
+ *
+ * Linear attention with a decay for each head. For batch entry b and head h with g = log_decay[h],
+ * tokens t in order and S a dim x dim_v state (fp32) that starts as state[b][h] (null: zeros):
+ *   S <- e^g S + k_t^T v_t,   o_t = scale q_t S
+ * A log_decay of -inf forgets everything (0^0 is 1); above 0 the state grows.
+ * q: batch x tokens x heads x dim; k: batch x tokens x kv_heads x dim; v: batch x tokens x kv_heads x
+ * dim_v; each with unit stride along its last axis and any batch, token and head strides >= 0 up to
+ * 2^36. heads is a multiple of kv_heads; head h reads k, v head h / (heads / kv_heads).
+ * lengths (batch, or null): entry b has the first lengths[b] tokens (clamped to [0, tokens]); the others
+ * are not read, their o and gradients are zeros, the state passes them by.
+ * Computed in chunks of 64 tokens (an infinity or NaN in a token may reach the tokens of its chunk
+ * before it). MUON_BF16: products on the bf16 matrix instructions with fp32 sums; scores and the copy of
+ * the state that q is multiplied with are rounded to bf16 as their operands. States that leave a
+ * call are fp32 sums of unrounded terms. MUON_F32: fp32 throughout.
+ * batch up to 2^20, heads to 2^16, batch x heads to 2^20, tokens to 2^24, dim and dim_v in [1, 256]. */
+#define MUON_MIX_MAX_DIM 256
+typedef struct muon_mix {
+  const void *q, *k, *v;
+  const float *log_decay;   /* heads */
+  const float *state;       /* batch x heads x dim x dim_v, contiguous, or null */
+  const int32_t *lengths;   /* batch, or null */
+  int64_t q_strides[3], k_strides[3], v_strides[3];  /* batch, token, head */
+  int64_t batch, tokens;
+  int32_t heads, kv_heads, dim, dim_v;
+  float scale;              /* finite */
+  int32_t dtype;            /* MUON_F32 or MUON_BF16: q, k, v, o and their gradients */
+} muon_mix;
+
+/* Operands of the backward: d_o, shaped as o, with its strides; d_final (batch x heads x dim x dim_v,
+ * contiguous; null: zeros), the gradient of the last state. dq, dk, dv: contiguous, of the shapes of
+ * q, k, v; d_state: of state's. Each may be null (not wanted). */
+typedef struct muon_mix_grads {
+  const void *d_o;
+  int64_t do_strides[3];
+  const float *d_final;
+  void *dq, *dk, *dv;
+  float *d_state;
+} muon_mix_grads;
+
+/* Bytes of workspace (256-byte aligned; 0: none, null is accepted) of muon_mix_forward (g null) or
+ * muon_mix_backward: sizes, dtype and which of g's outputs are null count. */
+int muon_mix_workspace_size(muon_ctx *ctx, const muon_mix *m, const muon_mix_grads *g, size_t *bytes);
+
+/* o (contiguous batch x tokens x heads x dim_v) and, with final_state not null, the states after the last
+ * token (batch x heads x dim x dim_v, contiguous). Outputs must not overlap inputs or each other. */
+int muon_mix_forward(muon_ctx *ctx, const muon_mix *m, void *o, float *final_state, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* The gradients named by g, log_decay being a constant. k's and v's are summed over the heads that share
+ * one (fp32, in head order). Outputs must not overlap inputs or each other. */
+int muon_mix_backward(muon_ctx *ctx, const muon_mix *m, const muon_mix_grads *g, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* One token (m->tokens == 1, lengths null, state not null; token strides are not read): o (contiguous
+ * batch x heads x dim_v) and the new states, which may replace `state` (same address) and must not
+ * overlap it otherwise. No workspace. fp32 throughout, o rounded once. */
+int muon_mix_step(muon_ctx *ctx, const muon_mix *m, void *o, float *new_state, void *stream);
+
+/* Tokens sorted by expert. Choice f = t top + j is token t's j-th expert, ids[f]; one outside [0, experts)
+ * is dropped. Sorted by expert, and among one expert's by f:
+ *   order[p] = f of row p; -1 for the places behind the last row
+ *   slots[f] = p; -1 for a dropped choice
+ *   offsets[e] = first row of expert e; offsets[experts] = number of rows
+ * tokens < 2^24, top in [1, MUON_MAX_CHOICES], tokens x top up to 2^25, experts in [1, MUON_MAX_EXPERTS]. The arrays must not
+ * overlap. */
+#define MUON_MAX_EXPERTS 1024
+#define MUON_MAX_CHOICES 64
+typedef struct muon_experts {
+  const void *ids;    /* tokens x top, contiguous */
+  int32_t *order;     /* tokens x top */
+  int32_t *slots;     /* tokens x top */
+  int32_t *offsets;   /* experts + 1 */
+  int64_t tokens;
+  int32_t top, experts;
+  int32_t id_dtype;   /* MUON_I32 or MUON_I64 */
+  int32_t reserved;   /* 0 */
+} muon_experts;
+/* Bytes of workspace (256-byte aligned; 0: none): tokens, top and experts count. */
+int muon_expert_plan_workspace_size(muon_ctx *ctx, const muon_experts *e, size_t *bytes);
+int muon_expert_plan(muon_ctx *ctx, const muon_experts *e, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Rows by a plan that muon_expert_plan wrote (ids and order are not read and may be null; slots outside the rows
+ * count as dropped). Token arrays: tokens x dim; sorted arrays: tokens x top rows of dim, row strides at least dim.
+ * dim in [1, 2^20], row strides up to 2^35. Outputs must not overlap inputs or each other.
+ *   dispatch:         sorted[slots[f]] = token[t]; rows behind the last one become zeros
+ *   combine:          token[t] = sum_j weights[f] sorted[slots[f]] (weights null: 1), in fp32 in the order
+ *                     of j, rounded once; with weights null also dispatch's gradient
+ *   combine_backward: d_sorted[slots[f]] = weights[f] d_token[t], zeros behind the last row (null: not wanted);
+ *                     d_weights[f] = d_token[t] . sorted[slots[f]] in fp32, 0 for a dropped choice (null: not
+ *                     wanted; sorted may then be null) */
+int muon_expert_dispatch(muon_ctx *ctx, const muon_experts *e, const void *token, int64_t ld_token, void *sorted,
+                         int64_t ld_sorted, int64_t dim, int dtype, void *stream);
+int muon_expert_combine(muon_ctx *ctx, const muon_experts *e, const void *sorted, int64_t ld_sorted,
+                        const float *weights, void *token, int64_t ld_token, int64_t dim, int dtype, void *stream);
+int muon_expert_combine_backward(muon_ctx *ctx, const muon_experts *e, const void *d_token, int64_t ld_token,
+                                 const void *sorted, int64_t ld_sorted, const float *weights, void *d_sorted,
+                                 int64_t ld_d_sorted, float *d_weights, int64_t dim, int dtype, void *stream);
+
+/* out = residual + keep x 65536 / (65536 - c), c = p 65536 rounded to the nearest whole number (half up): element
+ * i = row cols + col is kept where its 16-bit number is at least c; without residual (null) plus nothing.
+ * The numbers: Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC
+ * 2011) with counter (i / 8, offset) and key seed, each low word first; number i % 8 is the low (even) or
+ * high (odd) half of word (i % 8) / 2. So the mask hangs on seed, offset and i alone, and the gradient by
+ * x is the same call on the gradient of out, without residual. A dropped element's x is not used (a NaN
+ * there is dropped too). Computed in fp32, rounded once.
+ * counter (device memory, two uint64, 8-byte aligned; null: seed and offset as given): seed and offset, read when
+ * the call runs, so that a captured graph's replays can differ.
+ * rows in [0, 2^31), cols in [1, 2^36], rows x cols up to 2^36, row strides in [cols, 2^36], rows x stride up to 2^60. out may be x or residual
+ * (same stride) and must not overlap them otherwise. */
+typedef struct muon_drop {
+  const void *x, *residual;
+  void *out;
+  const uint64_t *counter;
+  int64_t ld_x, ld_residual, ld_out;
+  int64_t rows, cols;
+  uint64_t seed, offset;
+  float p;            /* in [0, 1] */
+  int32_t dtype;      /* MUON_F32 or MUON_BF16 */
+} muon_drop;
+int muon_dropout(muon_ctx *ctx, const muon_drop *d, void *stream);
+
 /* ---- Owner assignment: which rank updates which matrix ----
  * DMuon summary (gist.science), section 2.3 (compute-aware load balancing): the update
  * cost varies strongly with the matrix shape, so each matrix is given one owner rank to

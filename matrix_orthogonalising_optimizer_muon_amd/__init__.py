@@ -1,14 +1,15 @@
 """MI355X-native per-matrix Muon update (HIP kernels for gfx950 behind a C-ABI library).
 
 ``binding`` (loaded on first use) marshals arguments into ``libmuon_amd.so``; every step
-of the update runs in the library's HIP kernels. ``layers`` and ``losses`` are the operators a
-training step runs before the update (gated feed-forward block, vocabulary losses).
+of the update runs in the library's HIP kernels. The operators a training step runs before
+the update: ``layers`` (gated feed-forward block), ``mixers`` (linear attention with decay),
+``experts`` (tokens sorted by expert and back), ``dropout`` and ``losses`` (vocabulary losses).
 ``workloads`` holds the seeded synthetic inputs.
 """
 
 import importlib
 
-__all__ = ["binding", "layers", "losses", "workloads"]
+__all__ = ["binding", "dropout", "experts", "layers", "losses", "mixers", "workloads"]
 
 
 def __getattr__(name):

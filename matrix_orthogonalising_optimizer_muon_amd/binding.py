@@ -135,6 +135,37 @@ class muon_distill(ctypes.Structure):
                 ("top_dtype", ctypes.c_int32), ("id_dtype", ctypes.c_int32)]
 
 
+MUON_MIX_MAX_DIM = 256
+MUON_MAX_EXPERTS = 1024
+MUON_MAX_CHOICES = 64
+
+
+class muon_mix(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("log_decay", ctypes.c_void_p),
+                ("state", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("q_strides", ctypes.c_int64 * 3),
+                ("k_strides", ctypes.c_int64 * 3), ("v_strides", ctypes.c_int64 * 3), ("batch", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("dim_v", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class muon_mix_grads(ctypes.Structure):
+    _fields_ = [("d_o", ctypes.c_void_p), ("do_strides", ctypes.c_int64 * 3), ("d_final", ctypes.c_void_p),
+                ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), ("d_state", ctypes.c_void_p)]
+
+
+class muon_experts(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("order", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("top", ctypes.c_int32),
+                ("experts", ctypes.c_int32), ("id_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class muon_drop(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("counter", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("ld_residual", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("p", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
 MUON_MAX_COST_POINTS = 16
 MUON_MAX_PLAN_RANKS = 4096
 MUON_PLAN_GREEDY = 1
@@ -210,6 +241,30 @@ _lib.muon_policy_loss.restype = ctypes.c_int
 _lib.muon_distill_loss.argtypes = [_P, ctypes.POINTER(muon_logits), ctypes.POINTER(muon_distill), _P,
                                    ctypes.c_size_t, _P]
 _lib.muon_distill_loss.restype = ctypes.c_int
+_lib.muon_mix_workspace_size.argtypes = [_P, ctypes.POINTER(muon_mix), ctypes.POINTER(muon_mix_grads),
+                                         ctypes.POINTER(ctypes.c_size_t)]
+_lib.muon_mix_workspace_size.restype = ctypes.c_int
+_lib.muon_mix_forward.argtypes = [_P, ctypes.POINTER(muon_mix), _P, _P, _P, ctypes.c_size_t, _P]
+_lib.muon_mix_forward.restype = ctypes.c_int
+_lib.muon_mix_backward.argtypes = [_P, ctypes.POINTER(muon_mix), ctypes.POINTER(muon_mix_grads), _P, ctypes.c_size_t, _P]
+_lib.muon_mix_backward.restype = ctypes.c_int
+_lib.muon_mix_step.argtypes = [_P, ctypes.POINTER(muon_mix), _P, _P, _P]
+_lib.muon_mix_step.restype = ctypes.c_int
+_lib.muon_expert_plan_workspace_size.argtypes = [_P, ctypes.POINTER(muon_experts), ctypes.POINTER(ctypes.c_size_t)]
+_lib.muon_expert_plan_workspace_size.restype = ctypes.c_int
+_lib.muon_expert_plan.argtypes = [_P, ctypes.POINTER(muon_experts), _P, ctypes.c_size_t, _P]
+_lib.muon_expert_plan.restype = ctypes.c_int
+_lib.muon_expert_dispatch.argtypes = [_P, ctypes.POINTER(muon_experts), _P, ctypes.c_int64, _P, ctypes.c_int64,
+                                      ctypes.c_int64, ctypes.c_int, _P]
+_lib.muon_expert_dispatch.restype = ctypes.c_int
+_lib.muon_expert_combine.argtypes = [_P, ctypes.POINTER(muon_experts), _P, ctypes.c_int64, _P, _P, ctypes.c_int64,
+                                     ctypes.c_int64, ctypes.c_int, _P]
+_lib.muon_expert_combine.restype = ctypes.c_int
+_lib.muon_expert_combine_backward.argtypes = [_P, ctypes.POINTER(muon_experts), _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
+                                              _P, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int, _P]
+_lib.muon_expert_combine_backward.restype = ctypes.c_int
+_lib.muon_dropout.argtypes = [_P, ctypes.POINTER(muon_drop), _P]
+_lib.muon_dropout.restype = ctypes.c_int
 _lib.muon_destroy.argtypes = [_P]
 _lib.muon_destroy.restype = ctypes.c_int
 _lib.muon_status_str.argtypes = [ctypes.c_int]
@@ -496,6 +551,58 @@ def muon_distill_loss(ctx, l: muon_logits, t: muon_distill, workspace: int | Non
     return _lib.muon_distill_loss(ctx, l, t, workspace, workspace_bytes, stream_ptr)
 
 
+def muon_mix_workspace_size(ctx, m: muon_mix, g: muon_mix_grads | None = None) -> int:
+    """Workspace bytes of ``muon_mix_forward``, or of ``muon_mix_backward`` when ``g`` is given."""
+    n = ctypes.c_size_t()
+    check(_lib.muon_mix_workspace_size(ctx, m, g, n), "muon_mix_workspace_size")
+    return n.value
+
+
+def muon_mix_forward(ctx, m: muon_mix, o: int, final_state: int | None, workspace: int | None, workspace_bytes: int,
+                     stream_ptr: int | None) -> int:
+    return _lib.muon_mix_forward(ctx, m, o, final_state, workspace, workspace_bytes, stream_ptr)
+
+
+def muon_mix_backward(ctx, m: muon_mix, g: muon_mix_grads, workspace: int | None, workspace_bytes: int,
+                      stream_ptr: int | None) -> int:
+    return _lib.muon_mix_backward(ctx, m, g, workspace, workspace_bytes, stream_ptr)
+
+
+def muon_mix_step(ctx, m: muon_mix, o: int, new_state: int, stream_ptr: int | None) -> int:
+    return _lib.muon_mix_step(ctx, m, o, new_state, stream_ptr)
+
+
+def muon_expert_plan_workspace_size(ctx, e: muon_experts) -> int:
+    n = ctypes.c_size_t()
+    check(_lib.muon_expert_plan_workspace_size(ctx, e, n), "muon_expert_plan_workspace_size")
+    return n.value
+
+
+def muon_expert_plan(ctx, e: muon_experts, workspace: int | None, workspace_bytes: int, stream_ptr: int | None) -> int:
+    return _lib.muon_expert_plan(ctx, e, workspace, workspace_bytes, stream_ptr)
+
+
+def muon_expert_dispatch(ctx, e: muon_experts, token: int, ld_token: int, sorted_: int, ld_sorted: int, dim: int,
+                         dtype: int, stream_ptr: int | None) -> int:
+    return _lib.muon_expert_dispatch(ctx, e, token, ld_token, sorted_, ld_sorted, dim, dtype, stream_ptr)
+
+
+def muon_expert_combine(ctx, e: muon_experts, sorted_: int, ld_sorted: int, weights: int | None, token: int, ld_token: int,
+                        dim: int, dtype: int, stream_ptr: int | None) -> int:
+    return _lib.muon_expert_combine(ctx, e, sorted_, ld_sorted, weights, token, ld_token, dim, dtype, stream_ptr)
+
+
+def muon_expert_combine_backward(ctx, e: muon_experts, d_token: int, ld_token: int, sorted_: int | None, ld_sorted: int,
+                                 weights: int | None, d_sorted: int | None, ld_d_sorted: int, d_weights: int | None,
+                                 dim: int, dtype: int, stream_ptr: int | None) -> int:
+    return _lib.muon_expert_combine_backward(ctx, e, d_token, ld_token, sorted_, ld_sorted, weights, d_sorted, ld_d_sorted,
+                                             d_weights, dim, dtype, stream_ptr)
+
+
+def muon_dropout(ctx, d: muon_drop, stream_ptr: int | None) -> int:
+    return _lib.muon_dropout(ctx, d, stream_ptr)
+
+
 def shape_cost(points) -> muon_shape_cost:
     """A ``muon_shape_cost`` from [(batch, ms), ...] measured points."""
     c = muon_shape_cost()
@@ -536,5 +643,7 @@ def exported_symbols() -> list:
                         "muon_tune_load", "muon_adamw_hparams_default", "muon_adamw_step",
                         "muon_destroy", "muon_status_str", "muon_owner_plan", "muon_ffn_workspace_size",
                         "muon_ffn_forward", "muon_ffn_backward", "muon_loss_workspace_size", "muon_policy_loss",
-                        "muon_distill_loss")
+                        "muon_distill_loss", "muon_mix_workspace_size", "muon_mix_forward", "muon_mix_backward",
+                        "muon_mix_step", "muon_expert_plan_workspace_size", "muon_expert_plan", "muon_expert_dispatch",
+                        "muon_expert_combine", "muon_expert_combine_backward", "muon_dropout")
             if hasattr(_lib, n)]

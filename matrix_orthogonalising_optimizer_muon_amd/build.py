@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build", "muon_amd")
 LIB = os.path.join(PKG, "libmuon_amd.so")
 SOURCES = ["api.cpp", "gemm.hip", "elementwise.hip", "small.hip", "adamw.hip", "planner.cpp",
-           "train_api.cpp", "ffn.hip", "losses.hip"]
+           "train_api.cpp", "ffn.hip", "losses.hip", "layer_api.cpp", "mixer.hip", "experts.hip", "dropout.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -67,7 +67,7 @@ def build(verbose: bool = False) -> str:
 # the regular build are reused when they are newer than their sources.
 SAN_OBJ = os.path.join(ROOT, "_build", "asan")
 SAN_LIB = os.path.join(SAN_OBJ, "libmuon_amd_asan.so")
-SAN_SOURCES = ["api.cpp", "planner.cpp", "train_api.cpp"]
+SAN_SOURCES = ["api.cpp", "planner.cpp", "train_api.cpp", "layer_api.cpp"]
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=all"]
 

@@ -1,0 +1,321 @@
+"""Linear attention with decay (muon_mix_*) against the float64 oracle, element by element, within
+the errors the oracle derives, and over all elements of random inputs within one half step."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+from oracle import mixer as om  # noqa: E402
+from tests.gpu_util import TORCH_DT, rel, to_np  # noqa: E402
+
+HALF_STEP = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def X():
+    from matrix_orthogonalising_optimizer_muon_amd import mixers
+    return mixers
+
+
+def inside(got, ref, bound, what):
+    got = to_np(got)
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:3].tolist(), got[bad][:3], ref[bad][:3], bound[bad][:3])
+
+
+def decays(H):
+    """From a half-life of a fraction of a token to some thousands."""
+    return torch.from_numpy(-np.geomspace(1.5, 2e-4, H).astype(np.float32)).cuda()
+
+
+def inputs(B, T, H, kv, D, E, dtype, seed=0, state=False):
+    rng = np.random.default_rng([seed, B, T, H, D, E])
+    new = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).cuda()  # noqa: E731
+    q, k, v, do = (new(B, T, h, d).to(TORCH_DT[dtype]) for h, d in ((H, D), (kv, D), (kv, E), (H, E)))
+    s, df = (new(B, H, D, E) * 3.0, new(B, H, D, E)) if state else (None, None)
+    return q, k, v, do, decays(H), s, df
+
+
+def np_of(*ts):
+    return [None if t is None else to_np(t) for t in ts]
+
+
+def check(X, ins, dtype, scale=None, lengths=None, norm=True):
+    """Forward and backward; returns what they gave."""
+    q, k, v, do, g, s, df = ins
+    f = 1.0 / np.sqrt(q.shape[3]) if scale is None else scale
+    f32 = float(np.float32(f))
+    h = HALF_STEP[dtype]
+    lens = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    kw = dict(scale=scale, state=s, lengths=lens)
+    o, last = X.linear_attention_forward(q, k, v, g, **kw, final=True)
+    grads = X.linear_attention_backward(do, q, k, v, g, **kw, d_final=df, need_dstate=True)
+    if lengths is not None:     # the oracle reads nothing behind a sequence
+        q, k, v, do = (t.clone() for t in (q, k, v, do))
+        for b, n in enumerate(lengths):
+            for t in (q, k, v, do):
+                t[b, max(n, 0):] = 0
+    a = np_of(q, k, v, g)
+    ns, ndo, ndf = np_of(s, do, df)
+    want = om.forward(*a, f32, ns, lengths)
+    limit = om.bounds(*a, f32, h, ns, lengths)
+    for x, r, b, name in zip((o, last), want, limit, ("o", "states")):
+        inside(x, r, b, name)
+    gwant = om.backward(ndo, *a, f32, ns, lengths, ndf)
+    glimit = om.bounds(*a, f32, h, ns, lengths, ndo, ndf)
+    for x, r, b, name in zip(grads, gwant, glimit, ("dq", "dk", "dv", "dstate")):
+        inside(x, r, b, name)
+    if norm:
+        # independent roundings of random values, each about 0.42 of a half step (uniform over the step, averaged over a
+        # binade): the result's and a score's or the state's copy: 0.42 sqrt(2) = 0.6
+        for x, r, name in zip((o, *grads[:3]), (want[0], *gwant[:3]), ("o", "dq", "dk", "dv")):
+            if dtype == "bf16" and r.size >= 4096:
+                assert rel(to_np(x), r) <= h, name
+    return o, last, grads
+
+
+SIZES = [(1, 1, 1, 1, 1, 1), (2, 1, 2, 1, 16, 8), (1, 63, 2, 2, 64, 64), (2, 64, 1, 1, 32, 32), (1, 65, 3, 1, 40, 72),
+         (2, 130, 2, 2, 128, 128), (1, 200, 4, 2, 17, 33), (1, 129, 1, 1, 256, 256), (1, 77, 2, 2, 255, 1),
+         (1, 77, 2, 1, 1, 255), (1, 100, 2, 2, 128, 64), (1, 100, 2, 2, 64, 128), (1, 90, 1, 1, 200, 100)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", SIZES)
+def test_parity(X, size, dtype):
+    check(X, inputs(*size, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [(1, 1, 2, 1, 48, 32), (2, 100, 2, 2, 64, 64), (1, 300, 3, 1, 128, 128), (1, 70, 1, 1, 130, 256)])
+def test_states_in_and_out(X, size, dtype):
+    check(X, inputs(*size, dtype, state=True), dtype, scale=-0.3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [(1, 1537, 2, 1, 64, 64), (2, 2048, 1, 1, 128, 128), (1, 1100, 1, 1, 256, 40)])
+def test_segments(X, size, dtype):
+    """Few heads and a long axis: the walk is split over workgroups and joined."""
+    check(X, inputs(*size, dtype, state=True), dtype)
+    check(X, inputs(*size, dtype, seed=1), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [100, 1200])
+def test_padded_batch(X, T, dtype):
+    """Lengths from 0 (and below) to past the end; NaN and infinities behind a sequence are not read."""
+    lengths = [T, 0, 1, 63, 64, 65, T - 1, -5, T + 9]
+    q, k, v, do, g, s, df = inputs(len(lengths), T, 2, 1, 40, 48, dtype, state=True)
+    for b, n in enumerate(lengths):
+        for t, x in zip((q, k, v, do), (float("nan"), float("inf"), float("nan"), float("-inf"))):
+            t[b, max(n, 0):] = x
+    o, last, grads = check(X, (q, k, v, do, g, s, df), dtype, lengths=lengths)
+    for b, n in enumerate(lengths):
+        for t in (o, *grads[:3]):
+            assert bool((t[b, max(n, 0):] == 0).all())
+    assert torch.equal(last[1], s[1]) and torch.equal(grads[3][1], df[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strides(X, dtype):
+    """Heads-first arrays, a joint projection, rows off every alignment, broadcast heads: read in place."""
+    B, T, H, D = 2, 150, 3, 33
+    q, k, v, do, g, _, _ = ins = inputs(B, T, H, H, D, D, dtype)
+    base = check(X, ins, dtype)
+    first = lambda t: t.transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731
+    wide = torch.full((B, T, H, 3 * D + 5), float("nan"), dtype=q.dtype, device="cuda")
+    joint = [wide[..., 1 + i * D:1 + (i + 1) * D] for i in range(3)]
+    for t, x in zip(joint, (q, k, v)):
+        t.copy_(x)
+    late = torch.full((B * T * H * D + 1,), float("nan"), dtype=q.dtype, device="cuda")[1:].view(B, T, H, D)
+    late.copy_(do)
+    for a in ((first(q), first(k), first(v), first(do)), (*joint, late)):
+        o, last = X.linear_attention_forward(*a[:3], g, final=True)
+        grads = X.linear_attention_backward(a[3], *a[:3], g)
+        assert torch.equal(o, base[0]) and torch.equal(last, base[1])
+        assert all(torch.equal(x, y) for x, y in zip(grads[:3], base[2][:3]))
+    # one head of k and v for all, as a broadcast view and as a shared head
+    k1, v1 = k[:, :, :1], v[:, :, :1]
+    o = X.linear_attention_forward(q, k1, v1, g)[0]
+    assert torch.equal(o, X.linear_attention_forward(q, k1.expand(-1, -1, H, -1), v1.expand(-1, -1, H, -1), g)[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [(1, 1, 1, 1, 1), (3, 4, 2, 64, 64), (2, 6, 2, 40, 72), (1, 2, 1, 256, 255), (5, 3, 3, 17, 6),
+                                  (64, 4, 4, 128, 128)])
+def test_step(X, size, dtype):
+    B, H, kv, D, E = size
+    q, k, v, _, g, s, _ = inputs(B, 1, H, kv, D, E, dtype, state=True)
+    q, k, v = q[:, 0], k[:, 0], v[:, 0]
+    f = float(np.float32(1.0 / np.sqrt(D)))
+    o, S = om.step(*np_of(q, k, v, g), f, to_np(s))
+    top, size_s = om.step(*(np.abs(x) for x in np_of(q, k, v)), to_np(g), f, np.abs(to_np(s)))
+    c = om.sums32(1, D)
+    other = torch.full_like(s, float("nan"))
+    got, new = X.linear_attention_step(q, k, v, g, s, out_state=other)
+    assert new is other
+    inside(got, o, c * top + 1.01 * HALF_STEP[dtype] * np.abs(o), "o")
+    inside(new, S, c * size_s, "states")
+    before = s._version
+    again, same = X.linear_attention_step(q, k, v, g, s)
+    assert same is s and s._version > before and torch.equal(s, other) and torch.equal(again, got)
+
+
+def test_steps_follow_a_prompt(X):
+    """A prompt's states carried on token by token give what the whole sequence gives."""
+    q, k, v, _, g, _, _ = inputs(2, 140, 4, 2, 64, 64, "f32")
+    o, last = X.linear_attention_forward(q, k, v, g, final=True)
+    _, s = X.linear_attention_forward(q[:, :130], k[:, :130], v[:, :130], g, final=True)
+    a = np_of(q, k, v, g)
+    limit = om.bounds(*a, float(np.float32(0.125)), 2.0 ** -24)
+    want = om.forward(*a, 0.125)
+    for t in range(130, 140):
+        x, s = X.linear_attention_step(q[:, t], k[:, t], v[:, t], g, s)
+        inside(x, want[0][:, t], 2 * limit[0][:, t], t)
+    inside(s, want[1], 2 * limit[1], "states")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decay_of_nothing_and_of_all(X, dtype):
+    """log_decay 0 keeps everything, -inf and very negative ones only the token itself."""
+    q, k, v, do, _, s, df = inputs(1, 150, 3, 3, 32, 32, dtype, state=True)
+    for T in (1, 150):
+        g = torch.tensor([0.0, -float("inf"), -200.0], device="cuda")
+        o, last, grads = check(X, (q[:, :T], k[:, :T], v[:, :T], do[:, :T], g, s, df), dtype)
+        assert bool(torch.isfinite(o.float()).all())
+
+
+def test_no_tokens(X):
+    q, k, v, do, g, s, df = inputs(2, 0, 2, 1, 24, 16, "bf16", state=True)
+    o, last = X.linear_attention_forward(q, k, v, g, state=s, final=True)
+    assert o.shape == (2, 0, 2, 16) and torch.equal(last, s)
+    assert bool((X.linear_attention_forward(q, k, v, g, final=True)[1] == 0).all())
+    dq, dk, dv, ds = X.linear_attention_backward(do, q, k, v, g, state=s, d_final=df, need_dstate=True)
+    assert dq.shape == q.shape and dk.shape == k.shape and dv.shape == v.shape and torch.equal(ds, df)
+    e = torch.empty(0, 5, 2, 24, dtype=torch.bfloat16, device="cuda")
+    assert X.linear_attention_forward(e, e[:, :, :1], e[:, :, :1], g, final=True)[1].shape == (0, 2, 24, 24)
+
+
+def test_wanted_gradients_alone(X):
+    """Each subset of the gradients is what all of them are."""
+    q, k, v, do, g, s, df = inputs(1, 700, 2, 1, 64, 40, "bf16", state=True)
+    full = X.linear_attention_backward(do, q, k, v, g, state=s, d_final=df, need_dstate=True)
+    for need in ((True, False, False), (False, True, False), (False, False, True), (True, False, True), (False, False, False)):
+        for ds in (False, True):
+            got = X.linear_attention_backward(do, q, k, v, g, state=s, d_final=df, need=need, need_dstate=ds)
+            for x, y, n in zip(got, full, (*need, ds)):
+                assert (x is None) == (not n)
+                assert not n or torch.equal(x, y)
+
+
+def test_same_from_run_to_run(X):
+    ins = inputs(2, 1500, 2, 1, 128, 128, "bf16", state=True)
+    q, k, v, do, g, s, df = ins
+    call = lambda: (*X.linear_attention_forward(q, k, v, g, state=s, final=True),  # noqa: E731
+                    *X.linear_attention_backward(do, q, k, v, g, state=s, d_final=df, need_dstate=True))
+    first = call()
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(first, call()))
+
+
+def test_automatic_differentiation(X):
+    q, k, v, do, g, s, df = inputs(2, 90, 4, 2, 32, 48, "f32", state=True)
+    leaves = [t.clone().requires_grad_(True) for t in (q, k, v, s)]
+    o, last = X.linear_attention(*leaves[:3], g, state=leaves[3], final=True)
+    got = torch.autograd.grad((o * do).sum() + (last * df).sum(), leaves)
+    want = X.linear_attention_backward(do, q, k, v, g, state=s, d_final=df, need_dstate=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # the states alone, the output alone, a sum's expanded gradient, k not wanted
+    last = X.linear_attention(*leaves[:3], g, state=leaves[3], final=True)[1]
+    got = torch.autograd.grad((last * df).sum(), leaves)
+    want = X.linear_attention_backward(torch.zeros_like(do), q, k, v, g, state=s, d_final=df, need_dstate=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    o = X.linear_attention(leaves[0], k, leaves[2], g)
+    got = torch.autograd.grad(o.sum(), (leaves[0], leaves[2]))
+    want = X.linear_attention_backward(torch.ones_like(do), q, k, v, g)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[2])
+    with pytest.raises(ValueError, match="constant"):
+        X.linear_attention(q, k, v, g.clone().requires_grad_(True))
+    # a saved operand written to in between
+    o = X.linear_attention(leaves[0] * 1.0, (kk := leaves[1] * 1.0), leaves[2], g)
+    with torch.no_grad():
+        kk.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.sum().backward()
+
+
+def test_differences(X):
+    """The gradient against differences of the forward itself, fp32."""
+    q, k, v, do, g, s, df = inputs(1, 70, 2, 1, 8, 8, "f32", state=True)
+    rng = np.random.default_rng(5)
+    value = lambda a: float((to_np(X.linear_attention_forward(*a[:3], g, state=a[3])[0]) * to_np(do)).sum())  # noqa: E731
+    grads = X.linear_attention_backward(do, q, k, v, g, state=s, need_dstate=True)
+    for i in range(4):
+        ops = [q, k, v, s]
+        move = torch.from_numpy(rng.standard_normal(ops[i].shape).astype(np.float32)).cuda()
+        up, down = list(ops), list(ops)
+        up[i], down[i] = ops[i] + move, ops[i] - move
+        # the output is linear in each operand alone: the difference is exact but for the roundings of o, at most
+        # sums32 of its absolute terms (here below 2^-15 of their sum) a side, and of the operands moved
+        size = sum(float((np.abs(to_np(do)) * om.forward(*(np.abs(to_np(x)) for x in a[:3]), to_np(g), 1 / np.sqrt(8),
+                                                         np.abs(to_np(a[3])))[0]).sum()) for a in (up, down))
+        slope = float((to_np(grads[i]) * to_np(move)).sum())
+        assert abs((value(up) - value(down)) / 2 - slope) <= 2 * om.sums32(70, 8, 2) * size, i
+
+
+def test_far_offsets(X):
+    """Tokens more than 2^31 elements apart, on another than the default stream."""
+    if torch.cuda.mem_get_info()[0] < (24 << 30):
+        pytest.skip("needs 24 GB")
+    T, D = 70, 64
+    far = torch.empty((T - 1) * (1 << 26) + D, dtype=torch.bfloat16, device="cuda")
+    view = far.as_strided((1, T, 1, D), (0, 1 << 26, 0, 1))
+    q, k, v, do, g, _, _ = inputs(1, T, 1, 1, D, D, "bf16")
+    view.copy_(k)
+    want = X.linear_attention_forward(q, k, v, g)[0], *X.linear_attention_backward(do, q, k, v, g)[:3]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = X.linear_attention_forward(q, view, v, g)[0], *X.linear_attention_backward(do, q, view, v, g)[:3]
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_refusals(X):
+    q, k, v, do, g, s, df = inputs(2, 10, 4, 2, 16, 24, "bf16", state=True)
+    fwd, bwd, step = X.linear_attention_forward, X.linear_attention_backward, X.linear_attention_step
+    for bad in [dict(k=k[:, :9]), dict(v=v[:, :, :1]), dict(k=k[..., :8]), dict(g=g[:3]), dict(k=k.expand(2, 10, 2, 16).repeat(1, 1, 2, 1)[:, :, :3]),
+                dict(q=q[0]), dict(q=torch.zeros(2, 10, 4, 257, device="cuda", dtype=torch.bfloat16)), dict(q=q.cpu())]:
+        a = dict(q=q, k=k, v=v, g=g) | bad
+        with pytest.raises((ValueError, TypeError)):
+            fwd(a["q"], a["k"], a["v"], a["g"])
+    for bad in [dict(q=q.half()), dict(k=k.float()), dict(g=g.double()), dict(g=None), dict(q=None)]:
+        a = dict(q=q, k=k, v=v, g=g) | bad
+        with pytest.raises((TypeError, AttributeError)):
+            fwd(a["q"], a["k"], a["v"], a["g"])
+    with pytest.raises(ValueError, match="unit stride"):
+        fwd(q.transpose(2, 3).contiguous().transpose(2, 3), k, v, g)
+    for st in (s[:1], s.transpose(2, 3), s.transpose(0, 1).contiguous().transpose(0, 1)):
+        with pytest.raises(ValueError):
+            fwd(q, k, v, g, state=st)
+    with pytest.raises(TypeError):
+        fwd(q, k, v, g, state=s.bfloat16())
+    with pytest.raises(TypeError):
+        fwd(q, k, v, g, lengths=torch.tensor([1, 2], device="cuda"))
+    with pytest.raises(ValueError):
+        fwd(q, k, v, g, lengths=torch.ones(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(Exception, match="MUON_ERR_ARG|muon_mix_forward"):
+        fwd(q, k, v, g, scale=float("nan"))
+    with pytest.raises(ValueError):
+        bwd(do[:, :, :2], q, k, v, g)
+    with pytest.raises(ValueError):
+        bwd(do, q, k, v, g, d_final=df[..., :8])
+    with pytest.raises(ValueError):
+        step(q, k, v, g, s)
+    with pytest.raises(ValueError):
+        step(q[:, 0], k[:, 0], v[:, 0], g, None)
+    with pytest.raises(Exception, match="muon_mix_step"):
+        both = torch.zeros(2 * s.numel() - 16, device="cuda")
+        step(q[:, 0], k[:, 0], v[:, 0], g, both[:s.numel()].view(s.shape), out_state=both[-s.numel():].view(s.shape))
