@@ -35,8 +35,10 @@ __device__ __forceinline__ unsigned short to_bf16(float f) {
 __device__ __forceinline__ float from_bf16(unsigned short h) {
   return __uint_as_float(static_cast<unsigned int>(h) << 16);
 }
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ unsigned int pack(float lo, float hi) {
-  return to_bf16(lo) | (static_cast<unsigned int>(to_bf16(hi)) << 16);
+  return __builtin_bit_cast(unsigned int, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
 template <bool F32>
@@ -71,8 +73,8 @@ __device__ __forceinline__ u32x2 read_transposed(const __attribute__((address_sp
 
 // The fragment of tile t's columns (as rows) over tokens, from an array of tokens (rows of
 // PITCH bytes). Tokens in the order the scores' results have: 16-bit step s: 32 s + 16 (e / 4) +
-// 4 (l / 16) + e % 4 for e = 0..7; fp32: 16 s + 4 (l / 16) + e.
-template <bool F32, int PITCH>
+// 4 (l / 16) + e % 4 for e = 0..7; fp32: 16 s + 4 (l / 16) + e. BY_TILE: the fours of columns lie by tile.
+template <bool F32, int PITCH, bool BY_TILE>
 __device__ __forceinline__ u32x4 columns(const char* lds, int t, int s, int lane) {
   const int g = lane >> 4, i = lane & 15;
   u32x4 f;
@@ -84,7 +86,8 @@ __device__ __forceinline__ u32x4 columns(const char* lds, int t, int s, int lane
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // 16 lanes read four rows of four pieces; lane i receives column i of the 16
-      const char* p = lds + (32 * s + 16 * h + 4 * g + (i >> 2)) * PITCH + col_of<F32>(t, 4 * (i & 3)) * 2;
+      const int c = BY_TILE ? 16 * t + 4 * (i & 3) : col_of<F32>(t, 4 * (i & 3));
+      const char* p = lds + (32 * s + 16 * h + 4 * g + (i >> 2)) * PITCH + c * 2;
       const u32x2 r = read_transposed((const __attribute__((address_space(3))) unsigned short*)p);
       f[2 * h] = r[0];
       f[2 * h + 1] = r[1];
@@ -93,14 +96,17 @@ __device__ __forceinline__ u32x4 columns(const char* lds, int t, int s, int lane
   return f;
 }
 
-// 16 bytes of a row from column c on, zeros behind its `dim` columns.
+// 16 bytes of a row from column c on.
+template <bool F32>
+__device__ __forceinline__ u32x4 load_whole(const char* row, int c) {
+  if constexpr (F32) return *reinterpret_cast<const u32x4_a4*>(row + c * 4);
+  else return *reinterpret_cast<const u32x4_a2*>(row + c * 2);
+}
+// The same with zeros behind its `dim` columns.
 template <bool F32>
 __device__ __forceinline__ u32x4 load_row(const char* row, int c, int dim) {
-  constexpr int ES = Type<F32>::ES, VEC = Type<F32>::VEC;
-  if (c + VEC <= dim) {
-    if constexpr (F32) return *reinterpret_cast<const u32x4_a4*>(row + c * ES);
-    else return *reinterpret_cast<const u32x4_a2*>(row + c * ES);
-  }
+  constexpr int VEC = Type<F32>::VEC;
+  if (c + VEC <= dim) return load_whole<F32>(row, c);
   u32x4 v{0, 0, 0, 0};
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
@@ -112,20 +118,33 @@ __device__ __forceinline__ u32x4 load_row(const char* row, int c, int dim) {
   return v;
 }
 
+// Waits for this workgroup's LDS traffic and its waves. The two kinds of waves below meet here from
+// loops of their own, with the same number of turns.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+}
+
+// Four waves keep the state (each dim / 4 of its rows, or half of rows and columns), with OUT four
+// more make the outputs (16 of a chunk's tokens each): a SIMD then has one of either, whose matrix
+// instructions, conversions and LDS reads fill each other's gaps. BUFS copies of a chunk's operands
+// in LDS: with two the next chunk's are written while this one's are read.
 template <bool F32, int DP, int NV, bool OUT>
-__global__ __launch_bounds__(256) void mix_walk(const MixParams p) {
+__global__ __launch_bounds__(OUT ? 512 : 256, OUT ? 2 : 2) void mix_walk(const MixParams p) {
   constexpr int ES = Type<F32>::ES, VEC = Type<F32>::VEC, KF = Type<F32>::KF;
-  constexpr int PB = DP * ES + 16, PC = NV * ES + 16;          // rows of LDS in bytes
+  constexpr int THREADS = OUT ? 512 : 256;
+  constexpr int PB = DP * ES + 16, PC = NV * ES + (F32 ? 16 : 32);   // rows of LDS in bytes
   constexpr int WD = DP == 64 ? 2 : 4, WE = 4 / WD;            // waves over the state's rows and columns
   constexpr int MT = DP / WD / 16, NT = NV / WE / 16;          // its 16 x 16 tiles a wave
   constexpr int JS = C / KF;                                   // fragments over a chunk's tokens
   constexpr int DS = DP / KF;                                  // fragments over dim
-  constexpr int LB = C * DP / VEC / 256, LC = C * NV / VEC / 256;  // 16-byte loads a thread and chunk
+  constexpr int LB = (C * DP / VEC + THREADS - 1) / THREADS, LC = (C * NV / VEC + THREADS - 1) / THREADS;  // loads a thread and chunk
   constexpr int TILES = NV / 16;
-  static_assert(MT * WD * 16 == DP && NT * WE * 16 == NV && LB >= 1 && LC >= 1, "whole tiles");
-  __shared__ __attribute__((aligned(16))) char lds_b[C * PB];
-  __shared__ __attribute__((aligned(16))) char lds_c[C * PC];
-  __shared__ __attribute__((aligned(16))) char lds_z[OUT ? NV * PB : 16];   // the state, rounded, dim_v x dim
+  constexpr int SET = C * PB + C * PC + (OUT ? NV * PB : 0);
+  constexpr int BUFS = 2 * SET <= (OUT ? 160 : 80) * 1024 ? 2 : 1;
+  static_assert(MT * WD * 16 == DP && NT * WE * 16 == NV, "whole tiles");
+  __shared__ __attribute__((aligned(16))) char lds[BUFS * SET];
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -137,7 +156,7 @@ __global__ __launch_bounds__(256) void mix_walk(const MixParams p) {
     const int i = blockIdx.x, n = gridDim.x, xcd = i & 7, q = n >> 3, r = n & 7;
     at = xcd * q + min(xcd, r) + (i >> 3);
   }
-  int which = at % p.per;
+  const int which = at % p.per;
   at /= p.per;
   const int seg = at % p.walked;
   const int bh = at / p.walked;
@@ -146,7 +165,7 @@ __global__ __launch_bounds__(256) void mix_walk(const MixParams p) {
   while (ri + 1 < p.roles && which >= p.role[ri + 1].first) ++ri;
   const MixRole& o = p.role[ri];
   const int e0 = (which - o.first) * NV;
-  const int dim = o.dim, cols = min(o.dim_v - e0, NV);
+  const int dim = o.dim, dim_v = o.dim_v, cols = min(dim_v - e0, NV);
   const bool rev = o.reversed;
   const int off = rev ? 0 : 1;
 
@@ -156,121 +175,100 @@ __global__ __launch_bounds__(256) void mix_walk(const MixParams p) {
   g2 = g2 < -1e30f ? -1e30f : g2;                               // a decay to 0: 0^0 stays 1
   const int begin = seg * p.segment, end = min(begin + p.segment, p.tokens);
   const int live = min(end, n);                                 // places begin .. live - 1 hold tokens
-
+  auto token = [&](int r) -> int64_t { return rev ? n - 1 - r : r; };
   auto base = [&](const MixArray& x) {
     return static_cast<const char*>(x.p) + (batch * x.sb + (head / x.group) * x.sh) * ES;
   };
-  // the address of the row at place r of the walk
-  const char* rows_a = OUT ? base(o.a) : nullptr;
+
+  // ---- b and c of a chunk: on their way in registers, then in LDS ----
   const char* rows_b = base(o.b);
   const char* rows_c = base(o.c) + e0 * ES;
-  const int64_t sa = o.a.st * ES, sb = o.b.st * ES, sc = o.c.st * ES;
-  auto token = [&](int r) -> int64_t { return rev ? n - 1 - r : r; };
-
-  // ---- the state: rows d = dbase + col_of(mt, .), columns e = col_of(we NT + nt, .) ----
-  const int wd = wave % WD, we = wave / WD;
-  const int dbase = wd * (DP / WD);
-  f32x4 z[MT][NT];
-  bool have = false;
-  {
-    const float* src = o.z_in;
-    if (src && (p.z_in_per_segment || seg == 0)) {
-      have = true;
-      src += (static_cast<int64_t>(bh) * (p.z_in_per_segment ? p.segments : 1) + (p.z_in_per_segment ? seg : 0)) * o.dim * o.dim_v;
+  const int64_t sb = o.b.st * ES, sc = o.c.st * ES;
+  u32x4 nb[LB], nc[LC];
+  auto request = [&](int r0) {
+    const bool inside = r0 + C <= live;
+    if (inside && dim == DP) {
+#pragma unroll
+      for (int j = 0; j < LB; ++j) {
+        const int x = j * THREADS + tid, row = x / (DP / VEC), c = x % (DP / VEC) * VEC;
+        if (C * DP / VEC % THREADS == 0 || row < C) nb[j] = load_whole<F32>(rows_b + token(r0 + row) * sb, c);
+      }
     } else {
-      src = nullptr;
+#pragma unroll
+      for (int j = 0; j < LB; ++j) {
+        const int x = j * THREADS + tid, row = x / (DP / VEC), c = x % (DP / VEC) * VEC;
+        nb[j] = u32x4{0, 0, 0, 0};
+        if (row < C && r0 + row < live && c < dim) nb[j] = load_row<F32>(rows_b + token(r0 + row) * sb, c, dim);
+      }
+    }
+    if (inside && cols == NV) {
+#pragma unroll
+      for (int j = 0; j < LC; ++j) {
+        const int x = j * THREADS + tid, row = x / (NV / VEC), c = x % (NV / VEC) * VEC;
+        if (C * NV / VEC % THREADS == 0 || row < C) nc[j] = load_whole<F32>(rows_c + token(r0 + row) * sc, c);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < LC; ++j) {
+        const int x = j * THREADS + tid, row = x / (NV / VEC), c = x % (NV / VEC) * VEC;
+        nc[j] = u32x4{0, 0, 0, 0};
+        if (row < C && r0 + row < live && c < cols) nc[j] = load_row<F32>(rows_c + token(r0 + row) * sc, c, cols);
+      }
+    }
+  };
+  auto keep = [&](char* set) {
+#pragma unroll
+    for (int j = 0; j < LB; ++j) {
+      const int x = j * THREADS + tid;
+      if (C * DP / VEC % THREADS == 0 || x < C * DP / VEC)
+        *reinterpret_cast<u32x4*>(set + x / (DP / VEC) * PB + x % (DP / VEC) * 16) = nb[j];
     }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int e = col_of<F32>(we * NT + nt, l16);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int d = dbase + col_of<F32>(mt, 4 * g + r);
-          z[mt][nt][r] = src && d < dim && e < cols ? src[d * o.z_row + (e0 + e) * o.z_col] : 0.0f;
+    for (int j = 0; j < LC; ++j) {
+      const int x = j * THREADS + tid, ch = x % (NV / VEC);
+      char* row = set + C * PB + x / (NV / VEC) * PC;
+      if (C * NV / VEC % THREADS == 0 || x < C * NV / VEC) {
+        if constexpr (F32) {
+          *reinterpret_cast<u32x4*>(row + ch * 16) = nc[j];
+        } else {
+          // columns by tile: of 32, the fours of the even tile first (its transpose reads then take 32 bytes a row)
+          *reinterpret_cast<u32x2*>(row + (ch >> 2) * 64 + (ch & 3) * 8) = u32x2{nc[j][0], nc[j][1]};
+          *reinterpret_cast<u32x2*>(row + (ch >> 2) * 64 + (ch & 3) * 8 + 32) = u32x2{nc[j][2], nc[j][3]};
         }
       }
-  }
-
-  // ---- per-lane constants ----
-  const int i_tok = 16 * wave + l16;                            // this lane's token of a chunk (columns of the products)
-  float within[4][4];                                           // e^{g (i - s)} of the scores' tiles, 0 above the diagonal
-  float reach = 0.0f;
-  if constexpr (OUT) {
-#pragma unroll
-    for (int jt = 0; jt < 4; ++jt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int d = i_tok - (16 * jt + 4 * g + r);
-        within[jt][r] = d >= 0 ? __builtin_amdgcn_exp2f(g2 * d) * o.p_scale : 0.0f;
-      }
-    reach = __builtin_amdgcn_exp2f(g2 * (i_tok + off)) * o.o_scale;
-  }
-  // the weights of a chunk's tokens in the state, in the order of `columns`
-  float weight[JS][VEC];
-  auto weigh = [&](int rows) {
-#pragma unroll
-    for (int s = 0; s < JS; ++s)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int j = F32 ? 16 * s + 4 * g + e : 32 * s + 16 * (e >> 2) + 4 * g + (e & 3);
-        weight[s][e] = __builtin_amdgcn_exp2f(g2 * max(rows - off - j, 0)) * o.u_scale;
-      }
-  };
-  weigh(C);
-  float over = __builtin_amdgcn_exp2f(g2 * C);
-
-  // ---- the next chunk's operands, on their way in registers ----
-  u32x4 nb[LB], nc[LC], na[OUT ? DS : 1];
-  auto request = [&](int r0) {
-#pragma unroll
-    for (int j = 0; j < LB; ++j) {
-      const int x = j * 256 + tid, row = x / (DP / VEC), c = x % (DP / VEC) * VEC;
-      nb[j] = u32x4{0, 0, 0, 0};
-      if (r0 + row < live && c < dim) nb[j] = load_row<F32>(rows_b + token(r0 + row) * sb, c, dim);
-    }
-#pragma unroll
-    for (int j = 0; j < LC; ++j) {
-      const int x = j * 256 + tid, row = x / (NV / VEC), c = x % (NV / VEC) * VEC;
-      nc[j] = u32x4{0, 0, 0, 0};
-      if (r0 + row < live && c < cols) nc[j] = load_row<F32>(rows_c + token(r0 + row) * sc, c, cols);
-    }
-    if constexpr (OUT) {
-#pragma unroll
-      for (int s = 0; s < DS; ++s) {
-        const int c = KF * s + VEC * g;
-        na[s] = u32x4{0, 0, 0, 0};
-        if (r0 + i_tok < live && c < dim) na[s] = load_row<F32>(rows_a + token(r0 + i_tok) * sa, c, dim);
-      }
     }
   };
 
-  const int64_t o_row = static_cast<int64_t>(p.heads) * o.dim_v;   // elements from token to token of the output
-  const int64_t o_at = (static_cast<int64_t>(batch) * p.tokens * p.heads + head) * o.dim_v + e0;
+  const bool carried = o.z_in && (p.z_in_per_segment || seg == 0);
   if (begin < live) request(begin);
-  for (int r0 = begin; r0 < live; r0 += C) {
-    const int rows = min(live - r0, C);
-    __syncthreads();   // the last chunk's reads of LDS are done
+
+  if (!OUT || wave >= 4) {
+    // ---- the state: rows d = dbase + col_of(mt, .), columns e = col_of(we NT + nt, .) ----
+    const int own = wave & 3, wd = own % WD, we = own / WD;
+    const int dbase = wd * (DP / WD);
+    f32x4 z[MT][NT];
+    {
+      const float* src = nullptr;
+      if (carried) src = o.z_in + (p.z_in_per_segment ? static_cast<int64_t>(bh) * p.segments + seg : bh) * dim * dim_v;
 #pragma unroll
-    for (int j = 0; j < LB; ++j) {
-      const int x = j * 256 + tid;
-      *reinterpret_cast<u32x4*>(lds_b + x / (DP / VEC) * PB + x % (DP / VEC) * 16) = nb[j];
-    }
-#pragma unroll
-    for (int j = 0; j < LC; ++j) {
-      const int x = j * 256 + tid;
-      *reinterpret_cast<u32x4*>(lds_c + x / (NV / VEC) * PC + x % (NV / VEC) * 16) = nc[j];
-    }
-    u32x4 a[OUT ? DS : 1];
-    if constexpr (OUT) {
-#pragma unroll
-      for (int s = 0; s < DS; ++s) a[s] = na[s];
-      if (have) {
-        // 16-bit: the state is rounded to bf16 as the operand of q Z, like the scores as that of the product with v
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          char* row = lds_z + col_of<F32>(we * NT + nt, l16) * PB + dbase * ES;
+          const int e = col_of<F32>(we * NT + nt, l16);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int d = dbase + col_of<F32>(mt, 4 * g + r);
+            z[mt][nt][r] = src && d < dim && e < cols ? src[d * o.z_row + (e0 + e) * o.z_col] : 0.0f;
+          }
+        }
+    }
+    // its copy for the outputs, dim_v (by tile) x dim. 16-bit: rounded to bf16, as the operand of q Z, like the
+    // scores as that of the product with v
+    auto show = [&](char* set) {
+      if constexpr (OUT) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          char* row = set + C * (PB + PC) + (16 * (we * NT + nt) + l16) * PB + dbase * ES;
           if constexpr (F32) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -284,96 +282,198 @@ __global__ __launch_bounds__(256) void mix_walk(const MixParams p) {
           }
         }
       }
-    }
-    if (r0 + C < live) request(r0 + C);
-    __syncthreads();
-
-    if (rows < C) {
-      weigh(rows);
-      over = __builtin_amdgcn_exp2f(g2 * rows);
-    }
-    // scores of this wave's 16 tokens, transposed: rows s (a chunk's tokens up to its own), columns its tokens
-    u32x4 score[OUT ? JS : 1];
-    if constexpr (OUT) {
-      f32x4 sc4[4];
+    };
+    // the weights of a chunk's tokens, in the order of `columns`
+    float weight[JS][VEC];
+    auto weigh = [&](int rows) {
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        sc4[jt] = f32x4{0, 0, 0, 0};
-        if (jt <= wave) {
+      for (int s = 0; s < JS; ++s)
 #pragma unroll
-          for (int s = 0; s < DS; ++s) {
-            const u32x4 k = *reinterpret_cast<const u32x4*>(lds_b + (16 * jt + l16) * PB + (KF * s + VEC * g) * ES);
-            mma<F32>(sc4[jt], k, a[s]);
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            sc4[jt][r] = 16 * jt + 4 * g + r <= i_tok ? sc4[jt][r] * within[jt][r] : 0.0f;
+        for (int e = 0; e < VEC; ++e) {
+          const int j = F32 ? 16 * s + 4 * g + e : 32 * s + 16 * (e >> 2) + 4 * g + (e & 3);
+          weight[s][e] = __builtin_amdgcn_exp2f(g2 * max(rows - off - j, 0)) * o.u_scale;
         }
-      }
-#pragma unroll
-      for (int s = 0; s < JS; ++s) {
-        if constexpr (F32) score[s] = __builtin_bit_cast(u32x4, sc4[s]);
-        else
-          score[s] = u32x4{pack(sc4[2 * s][0], sc4[2 * s][1]), pack(sc4[2 * s][2], sc4[2 * s][3]),
-                           pack(sc4[2 * s + 1][0], sc4[2 * s + 1][1]), pack(sc4[2 * s + 1][2], sc4[2 * s + 1][3])};
-      }
+    };
+    weigh(C);
+    float over = __builtin_amdgcn_exp2f(g2 * C);
+
+    if (begin < live) {
+      keep(lds);
+      show(lds);
     }
-    // weighted b of this wave's rows of the state. 16-bit: as three parts whose sum has the
-    // product's 24 bits, so that the state is the sum of unrounded terms
-    constexpr int PARTS = F32 ? 1 : 3;
-    u32x4 kf[PARTS][MT][JS];
+    int buf = 0;
+    for (int r0 = begin; r0 < live; r0 += C) {
+      const char* set = lds + buf * SET;
+      meet();
+      const bool more = r0 + C < live;
+      if (more) request(r0 + C);
+      const int rows = min(live - r0, C);
+      if (rows < C) {
+        weigh(rows);
+        over = __builtin_amdgcn_exp2f(g2 * rows);
+      }
+      // weighted b of this wave's rows. 16-bit: as three parts whose sum has the product's 24
+      // bits, so that the state is the sum of unrounded terms
+      constexpr int PARTS = F32 ? 1 : 3;
+      u32x4 kf[PARTS][MT][JS];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int s = 0; s < JS; ++s) {
-        const u32x4 f = columns<F32, PB>(lds_b + dbase * ES, mt, s, lane);
-        if constexpr (F32) {
+        for (int s = 0; s < JS; ++s) {
+          const u32x4 f = columns<F32, PB, false>(set + dbase * ES, mt, s, lane);
+          if constexpr (F32) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) kf[0][mt][s][e] = __float_as_uint(__uint_as_float(f[e]) * weight[s][e]);
-        } else {
+            for (int e = 0; e < 4; ++e) kf[0][mt][s][e] = __float_as_uint(__uint_as_float(f[e]) * weight[s][e]);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float lo = __uint_as_float(f[e] << 16) * weight[s][2 * e];
-            float hi = __uint_as_float(f[e] & 0xFFFF0000u) * weight[s][2 * e + 1];
+            for (int e = 0; e < 4; ++e) {
+              float lo = __uint_as_float(f[e] << 16) * weight[s][2 * e];
+              float hi = __uint_as_float(f[e] & 0xFFFF0000u) * weight[s][2 * e + 1];
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q) {
-              const unsigned int w = pack(lo, hi);
-              kf[q][mt][s][e] = w;
-              lo -= __uint_as_float(w << 16);
-              hi -= __uint_as_float(w & 0xFFFF0000u);
+              for (int q = 0; q < PARTS; ++q) {
+                const unsigned int w = pack(lo, hi);
+                kf[q][mt][s][e] = w;
+                lo -= __uint_as_float(w << 16);
+                hi -= __uint_as_float(w & 0xFFFF0000u);
+              }
             }
           }
         }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        u32x4 v[JS];
+#pragma unroll
+        for (int s = 0; s < JS; ++s) v[s] = columns<F32, PC, true>(set + C * PB, we * NT + nt, s, lane);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          z[mt][nt] *= over;
+#pragma unroll
+          for (int s = 0; s < JS; ++s)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) mma<F32>(z[mt][nt], kf[q][mt][s], v[s]);
+        }
       }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) z[mt][nt] *= over;
+      if (more) {
+        if constexpr (BUFS == 1) meet();
+        buf = BUFS == 2 ? buf ^ 1 : 0;
+        keep(lds + buf * SET);
+        show(lds + buf * SET);
+      }
+    }
 
-    const int64_t o_tok = OUT ? o_at + token(r0 + i_tok) * o_row : 0;
-    f32x4 acc[2];
+    if (o.z_out && (p.z_out_per_segment || seg == (n > 0 ? (n - 1) / p.segment : 0))) {
+      float* dst = o.z_out + (p.z_out_per_segment ? static_cast<int64_t>(bh) * p.segments + seg : bh) * dim * dim_v;
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      u32x4 v[JS];
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int s = 0; s < JS; ++s) v[s] = columns<F32, PC>(lds_c, t, s, lane);
-      if constexpr (OUT) {
+        for (int nt = 0; nt < NT; ++nt) {
+          const int e = col_of<F32>(we * NT + nt, l16);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int d = dbase + col_of<F32>(mt, 4 * g + r);
+            if (d < dim && e < cols) dst[static_cast<int64_t>(d) * dim_v + e0 + e] = z[mt][nt][r];
+          }
+        }
+    }
+  }
+
+  if (OUT && wave < 4) {
+    // ---- the outputs of tokens 16 wave .. + 15 of each chunk; a lane's token is a column of the products ----
+    const int i_tok = 16 * wave + l16;
+    const char* rows_a = base(o.a);
+    const int64_t sa = o.a.st * ES;
+    u32x4 na[DS];
+    auto request_a = [&](int r0) {
+      const char* row = rows_a + token(r0 + i_tok) * sa;
+      if (r0 + C <= live && dim == DP) {
+#pragma unroll
+        for (int s = 0; s < DS; ++s) na[s] = load_whole<F32>(row, KF * s + VEC * g);
+      } else {
+#pragma unroll
+        for (int s = 0; s < DS; ++s) {
+          const int c = KF * s + VEC * g;
+          na[s] = u32x4{0, 0, 0, 0};
+          if (r0 + i_tok < live && c < dim) na[s] = load_row<F32>(row, c, dim);
+        }
+      }
+    };
+    float within[4][4];                                         // e^{g (i - s)} of the scores' tiles
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        within[jt][r] = __builtin_amdgcn_exp2f(g2 * max(i_tok - (16 * jt + 4 * g + r), 0)) * o.p_scale;
+    const float reach = __builtin_amdgcn_exp2f(g2 * (i_tok + off)) * o.o_scale;
+    const int64_t o_row = static_cast<int64_t>(p.heads) * dim_v;   // elements from token to token of the output
+    const int64_t o_at = (static_cast<int64_t>(batch) * p.tokens * p.heads + head) * dim_v + e0;
+
+    if (begin < live) {
+      request_a(begin);
+      keep(lds);
+    }
+    int buf = 0;
+    for (int r0 = begin; r0 < live; r0 += C) {
+      const char* set = lds + buf * SET;
+      meet();
+      const bool more = r0 + C < live;
+      u32x4 a[DS];
+#pragma unroll
+      for (int s = 0; s < DS; ++s) a[s] = na[s];
+      if (more) {
+        request(r0 + C);
+        request_a(r0 + C);
+      }
+      // scores, transposed: rows s (the chunk's tokens up to its own), columns this wave's tokens
+      u32x4 score[JS];
+      {
+        f32x4 sc4[4];
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) {
+          sc4[jt] = f32x4{0, 0, 0, 0};
+          if (jt <= wave) {
+#pragma unroll
+            for (int s = 0; s < DS; ++s) {
+              const u32x4 k = *reinterpret_cast<const u32x4*>(set + (16 * jt + l16) * PB + (KF * s + VEC * g) * ES);
+              mma<F32>(sc4[jt], k, a[s]);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sc4[jt][r] *= within[jt][r];
+            if (jt == wave) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) sc4[jt][r] = 4 * g + r <= l16 ? sc4[jt][r] : 0.0f;
+            }
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < JS; ++s) {
+          if constexpr (F32) score[s] = __builtin_bit_cast(u32x4, sc4[s]);
+          else
+            score[s] = u32x4{pack(sc4[2 * s][0], sc4[2 * s][1]), pack(sc4[2 * s][2], sc4[2 * s][3]),
+                             pack(sc4[2 * s + 1][0], sc4[2 * s + 1][1]), pack(sc4[2 * s + 1][2], sc4[2 * s + 1][3])};
+        }
+      }
+      const bool have = carried || r0 > begin;
+      const bool mine = o.out && r0 + i_tok < live;
+      const int64_t o_tok = o_at + token(r0 + i_tok) * o_row;
+      f32x4 acc[2];
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
         f32x4 x{0, 0, 0, 0};
         if (have) {
 #pragma unroll
           for (int s = 0; s < DS; ++s) {
-            const u32x4 k = *reinterpret_cast<const u32x4*>(lds_z + col_of<F32>(t, l16) * PB + (KF * s + VEC * g) * ES);
+            const u32x4 k = *reinterpret_cast<const u32x4*>(set + C * (PB + PC) + (16 * t + l16) * PB + (KF * s + VEC * g) * ES);
             mma<F32>(x, k, a[s]);
           }
           x *= reach;
         }
 #pragma unroll
         for (int s = 0; s < JS; ++s)
-          if (KF * s <= 16 * wave) mma<F32>(x, v[s], score[s]);
+          if (KF * s <= 16 * wave) mma<F32>(x, columns<F32, PC, true>(set + C * PB, t, s, lane), score[s]);
         acc[t & 1] = x;
         // lane: token i_tok, columns of the tile (pair) 16 g .. or 32 .. + 8 g ..
-        if (o.out && r0 + i_tok < live) {
-          if constexpr (F32) {
+        if constexpr (F32) {
+          if (mine) {
             float* out = static_cast<float*>(o.out) + o_tok + 16 * t + 4 * g;
             const int left = cols - (16 * t + 4 * g);
             if (left >= 4) *reinterpret_cast<u32x4_a4*>(out) = __builtin_bit_cast(u32x4, x);
@@ -381,68 +481,37 @@ __global__ __launch_bounds__(256) void mix_walk(const MixParams p) {
 #pragma unroll
               for (int r = 0; r < 4; ++r)
                 if (r < left) out[r] = x[r];
-          } else if (t & 1) {
-            const int c = 32 * (t >> 1) + 8 * g, left = cols - c;
-            if (o.out_f32) {
-              float* out = static_cast<float*>(o.out) + o_tok + c;
+          }
+        } else if (t & 1) {
+          const int c = 32 * (t >> 1) + 8 * g, left = cols - c;
+          if (mine && o.out_f32) {
+            float* out = static_cast<float*>(o.out) + o_tok + c;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (left >= 4 * h + 4) *reinterpret_cast<u32x4_a4*>(out + 4 * h) = __builtin_bit_cast(u32x4, acc[h]);
-                else
-#pragma unroll
-                  for (int r = 0; r < 4; ++r)
-                    if (4 * h + r < left) out[4 * h + r] = acc[h][r];
-              }
-            } else {
-              unsigned short* out = static_cast<unsigned short*>(o.out) + o_tok + c;
-              const u32x4 w{pack(acc[0][0], acc[0][1]), pack(acc[0][2], acc[0][3]), pack(acc[1][0], acc[1][1]),
-                            pack(acc[1][2], acc[1][3])};
-              if (left >= 8) *reinterpret_cast<u32x4_a2*>(out) = w;
+            for (int h = 0; h < 2; ++h) {
+              if (left >= 4 * h + 4) *reinterpret_cast<u32x4_a4*>(out + 4 * h) = __builtin_bit_cast(u32x4, acc[h]);
               else
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                  if (r < left) out[r] = static_cast<unsigned short>(w[r / 2] >> (16 * (r & 1)));
+                for (int r = 0; r < 4; ++r)
+                  if (4 * h + r < left) out[4 * h + r] = acc[h][r];
             }
+          } else if (mine) {
+            unsigned short* out = static_cast<unsigned short*>(o.out) + o_tok + c;
+            const u32x4 w{pack(acc[0][0], acc[0][1]), pack(acc[0][2], acc[0][3]), pack(acc[1][0], acc[1][1]),
+                          pack(acc[1][2], acc[1][3])};
+            if (left >= 8) *reinterpret_cast<u32x4_a2*>(out) = w;
+            else
+#pragma unroll
+              for (int r = 0; r < 8; ++r)
+                if (r < left) out[r] = static_cast<unsigned short>(w[r / 2] >> (16 * (r & 1)));
           }
         }
       }
-      if (t / NT == we) {
-        const int nt_dyn = t % NT;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (nt != nt_dyn) continue;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int s = 0; s < JS; ++s) {
-              mma<F32>(z[mt][nt], kf[0][mt][s], v[s]);
-              if constexpr (!F32) {
-                mma<F32>(z[mt][nt], kf[1][mt][s], v[s]);
-                mma<F32>(z[mt][nt], kf[2][mt][s], v[s]);
-              }
-            }
-        }
+      if (more) {
+        if constexpr (BUFS == 1) meet();
+        buf = BUFS == 2 ? buf ^ 1 : 0;
+        keep(lds + buf * SET);
       }
     }
-    have = true;
-  }
-
-  if (o.z_out && (p.z_out_per_segment || seg == (n > 0 ? (n - 1) / p.segment : 0))) {
-    float* dst = o.z_out + (static_cast<int64_t>(bh) * (p.z_out_per_segment ? p.segments : 1) + (p.z_out_per_segment ? seg : 0)) *
-                               o.dim * o.dim_v;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int e = col_of<F32>(we * NT + nt, l16);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int d = dbase + col_of<F32>(mt, 4 * g + r);
-          if (d < dim && e < cols) dst[static_cast<int64_t>(d) * o.dim_v + e0 + e] = z[mt][nt][r];
-        }
-      }
-  }
-  if constexpr (OUT) {
     // rows behind the last token: zeros
     const int first = max(live, begin);
     const int64_t count = o.out ? static_cast<int64_t>(end - first) * cols : 0;
@@ -561,7 +630,7 @@ __global__ __launch_bounds__(256) void mix_step(const MixStep p) {
 template <bool F32, int DP, int NV>
 hipError_t walk(bool out, const MixParams& p, int64_t groups, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(groups));
-  if (out) mix_walk<F32, DP, NV, true><<<grid, 256, 0, st>>>(p);
+  if (out) mix_walk<F32, DP, NV, true><<<grid, 512, 0, st>>>(p);
   else mix_walk<F32, DP, NV, false><<<grid, 256, 0, st>>>(p);
   return hipGetLastError();
 }
