@@ -91,7 +91,7 @@ MixPlan plan_of(const muon_mix* m, const muon_mix_grads* g, int cus) {
     return static_cast<int>((g->dq ? cdiv(m->dim, nv) : 0) + (g->dk ? cdiv(m->dim, nv) : 0) +
                             (g->dv || g->d_state ? cdiv(m->dim_v, nv) : 0));
   };
-  int nv = p.tile.dim == 128 ? 128 : 64;
+  int nv = p.tile.dim == 128 && m->dtype == MUON_BF16 ? 128 : 64;
   if (wide <= 64) nv = std::min(nv, 64);
   if (wide <= 32) nv = 32;
   p.tile.dim_v = nv;
@@ -120,6 +120,14 @@ MixPlan plan_of(const muon_mix* m, const muon_mix_grads* g, int cus) {
 }
 
 MixArray array(const void* p, const int64_t (&s)[3], int group) { return {p, s[0], s[1], s[2], group}; }
+
+// Whether the direct loads can take an array: rows of whole 16-byte pieces at 16-byte addresses that do not
+// overlap, a chunk of them within 2^29 bytes.
+bool direct(const MixArray& a, int dim, int64_t es) {
+  const int64_t tok = a.st * es;
+  return aligned(a.p, 16) && a.sb * es % 16 == 0 && tok % 16 == 0 && a.sh * es % 16 == 0 && dim * es % 16 == 0 &&
+         tok >= dim * es && tok * kMixChunk <= (int64_t{1} << 29);
+}
 
 MixParams params(const muon_mix* m, const MixPlan& pl) {
   MixParams p;
@@ -245,6 +253,9 @@ int muon_mix_forward(muon_ctx* ctx, const muon_mix* m, void* o, float* final_sta
     const MixArray q = array(m->q, m->q_strides, 1), k = array(m->k, m->k_strides, group), v = array(m->v, m->v_strides, group);
     float* z = static_cast<float*>(workspace);
     MixParams p = params(m, pl);
+    p.exact = final_state != nullptr;
+    const int64_t es = size_of(m->dtype);
+    p.direct = direct(q, m->dim, es) && direct(k, m->dim, es) && direct(v, m->dim_v, es);
     if (pl.segments > 1) {
       MixParams s = p;
       add(s, pl, q, k, v, nullptr, m->dim, m->dim_v).z_out = z;
@@ -295,6 +306,9 @@ int muon_mix_backward(muon_ctx* ctx, const muon_mix* m, const muon_mix_grads* g,
     float *z = reinterpret_cast<float*>(ws), *zr = reinterpret_cast<float*>(ws + pl.off_rev);
     const bool back = g->dk || g->dv || g->d_state;
     MixParams p = params(m, pl);
+    p.exact = g->d_state != nullptr;
+    const int64_t es = size_of(m->dtype);
+    p.direct = direct(q, m->dim, es) && direct(k, m->dim, es) && direct(v, m->dim_v, es) && direct(d_o, m->dim_v, es);
     if (pl.segments > 1) {
       MixParams s = p;
       MixScan c;

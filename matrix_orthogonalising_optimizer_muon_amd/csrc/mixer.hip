@@ -25,6 +25,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int C = kMixChunk;
@@ -60,40 +61,79 @@ __device__ __forceinline__ void mma(f32x4& acc, const u32x4& a, const u32x4& b) 
   }
 }
 
-// Which column row m of 16-row tile `t` stands for. 16-bit: tiles go in pairs that interleave
-// by fours, so that a lane's results of both are eight neighbours (16 bytes).
-template <bool F32>
-__device__ __forceinline__ int col_of(int t, int m) {
-  return F32 ? 16 * t + m : 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3);
+// LDS arrays are rows of CHUNKS 16-byte pieces, a power of two, with the pieces of row r in the order
+// given by XOR with mixed(r), so that the reads below find different banks: 16-byte reads
+// of 8 neighbouring rows at one piece; 16-bit transpose reads of 32 bytes of 8 neighbouring
+// rows; 4-byte reads of 64 bytes of the rows r, r + 4, r + 8, r + 12. (Padded rows would do, but the
+// direct loads write whole kilobytes.)
+template <bool F32, int CHUNKS>
+__device__ __forceinline__ int mixed(int r) {
+  if constexpr (F32) return CHUNKS >= 16 ? r & 15 : ((r >> 2) & 1) << 2;
+  constexpr int SHIFT = CHUNKS >= 16 ? 0 : CHUNKS == 8 ? 1 : 2;   // rows in 256 bytes
+  constexpr int PAIRS = CHUNKS >= 16 ? 7 : CHUNKS / 2 - 1;
+  return (((r >> SHIFT) & PAIRS) << 1) | ((r >> 3) & 1);
+}
+template <bool F32, int CHUNKS>
+__device__ __forceinline__ int piece(int r, int c) {             // its byte offset
+  return (r * CHUNKS + (c ^ mixed<F32, CHUNKS>(r))) * 16;
 }
 
-__device__ __forceinline__ u32x2 read_transposed(const __attribute__((address_space(3))) unsigned short* __restrict__ p) {
+// LDS accesses go through restrict pointers: without any alias information the compiler waits
+// for every direct load in flight before each of them. What has to be waited for is waited for by hand.
+typedef __attribute__((address_space(3))) char lds_char;
+__device__ __forceinline__ u32x2 read_transposed(const lds_char* __restrict__ p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
 }
+__device__ __forceinline__ u32x4 read16(const lds_char* __restrict__ p) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(p);
+}
+__device__ __forceinline__ unsigned int read4(const lds_char* __restrict__ p) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) unsigned int*>(p);
+}
+__device__ __forceinline__ void write16(lds_char* __restrict__ p, u32x4 v) {
+  *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(p) = v;
+}
+__device__ __forceinline__ void write8(lds_char* __restrict__ p, u32x2 v) {
+  *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(p) = v;
+}
 
-// The fragment of tile t's columns (as rows) over tokens, from an array of tokens (rows of
-// PITCH bytes). Tokens in the order the scores' results have: 16-bit step s: 32 s + 16 (e / 4) +
-// 4 (l / 16) + e % 4 for e = 0..7; fp32: 16 s + 4 (l / 16) + e. BY_TILE: the fours of columns lie by tile.
-template <bool F32, int PITCH, bool BY_TILE>
-__device__ __forceinline__ u32x4 columns(const char* lds, int t, int s, int lane) {
+// Where a lane reads: its part of an address is computed once, and a tile's or step's is an XOR with a
+// constant (pieces of a row) and an instruction's offset (rows by sixteens). `at` is an array's offset in LDS plus the lane's part.
+//
+// The fragment of columns 16 t .. + 15 (as rows) over tokens, from an array of tokens. Tokens in
+// the order the scores' results have: 16-bit step s: 32 s + 16 (e / 4) + 4 (l / 16) + e % 4 for
+// e = 0..7; fp32: 16 s + 4 (l / 16) + e.
+template <bool F32, int CHUNKS>
+__device__ __forceinline__ int columns_lane(int lane) {
   const int g = lane >> 4, i = lane & 15;
+  if constexpr (F32) return piece<true, CHUNKS>(4 * g, i >> 2) + (i & 3) * 4;
+  // 16 lanes read four rows of four 8-byte pieces; lane i receives column i of the 16
+  return piece<false, CHUNKS>(4 * g + (i >> 2), (i & 3) >> 1) + (i & 1) * 8;
+}
+template <bool F32, int CHUNKS>
+__device__ __forceinline__ u32x4 columns(const lds_char* lds, int at, int t, int s) {
   u32x4 f;
   if constexpr (F32) {
-    const char* p = lds + (16 * s + 4 * g) * PITCH + col_of<F32>(t, i) * 4;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) f[r] = *reinterpret_cast<const unsigned int*>(p + r * PITCH);
+    for (int r = 0; r < 4; ++r) f[r] = read4(lds + (at ^ (t << 6 | (CHUNKS >= 16 ? r << 4 : 0))) + (16 * s + r) * CHUNKS * 16);
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      // 16 lanes read four rows of four pieces; lane i receives column i of the 16
-      const int c = BY_TILE ? 16 * t + 4 * (i & 3) : col_of<F32>(t, 4 * (i & 3));
-      const char* p = lds + (32 * s + 16 * h + 4 * g + (i >> 2)) * PITCH + c * 2;
-      const u32x2 r = read_transposed((const __attribute__((address_space(3))) unsigned short*)p);
+      const u32x2 r = read_transposed(lds + (at ^ t << 5) + (32 * s + 16 * h) * CHUNKS * 16);
       f[2 * h] = r[0];
       f[2 * h + 1] = r[1];
     }
   }
   return f;
+}
+// The fragment of rows 16 t .. + 15 at inner step s.
+template <bool F32, int CHUNKS>
+__device__ __forceinline__ int rows_lane(int lane) {
+  return piece<F32, CHUNKS>(lane & 15, lane >> 4);
+}
+template <int CHUNKS>
+__device__ __forceinline__ u32x4 rows(const lds_char* lds, int at, int t, int s) {
+  return read16(lds + (at ^ s << 6) + 16 * t * CHUNKS * 16);
 }
 
 // 16 bytes of a row from column c on.
@@ -118,6 +158,37 @@ __device__ __forceinline__ u32x4 load_row(const char* row, int c, int dim) {
   return v;
 }
 
+// N fragments from LDS in groups of G: a group is read while the one before is used. The compiler
+// alone waits for each read before the product it is for, and asks for the next one after that.
+template <int N, int G, typename Read, typename Use>
+__device__ __forceinline__ void stream(Read&& read, Use&& use) {
+  static_assert(N % G == 0, "whole groups");
+  u32x4 f[2][G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) f[0][i] = read(i);
+#pragma unroll
+  for (int k = 0; k < N / G; ++k) {
+    if (k + 1 < N / G) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) f[(k + 1) & 1][i] = read((k + 1) * G + i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    use(k * G, f[k & 1]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// acc[t] += of the fragments f of (tile, inner step) i0 .. i0 + G - 1, tile by tile of INNER steps; inner steps
+// outermost, so that neighbours in time are of different tiles.
+template <bool F32, int INNER, int T, int G, int K>
+__device__ __forceinline__ void products(f32x4 (&acc)[T], int i0, const u32x4 (&f)[G], const u32x4 (&b)[K]) {
+#pragma unroll
+  for (int s = 0; s < INNER; ++s)
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if ((i0 + i) % INNER == s) mma<F32>(acc[(i0 + i) / INNER], f[i], b[s]);
+}
+
 // Waits for this workgroup's LDS traffic and its waves. The two kinds of waves below meet here from
 // loops of their own, with the same number of turns.
 __device__ __forceinline__ void meet() {
@@ -126,25 +197,42 @@ __device__ __forceinline__ void meet() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
 }
 
+// How a chunk's operands and the state's copy share a workgroup's LDS.
+template <bool F32, int DP, int NV, bool OUT, bool DIRECT>
+struct Layout {
+  static constexpr int ES = F32 ? 4 : 2;
+  static constexpr int B = C * DP * ES, CB = C * NV * ES, Z = OUT ? NV * DP * ES : 0;
+  static constexpr int MOST = 160 * 1024;
+  // copies of the operands: the next chunk's arrive (direct loads: the next two) while one is read
+  static constexpr int STAGES = DIRECT && OUT && 3 * (B + CB) + 2 * Z <= MOST ? 3 : 2 * (B + CB) + 2 * Z <= MOST ? 2 : 1;
+  static constexpr int COPIES = STAGES > 1 ? 2 : 1;              // of the state's copy
+  static constexpr int BYTES = STAGES * (B + CB) + COPIES * Z;
+};
+
 // Four waves keep the state (each dim / 4 of its rows, or half of rows and columns), with OUT four
 // more make the outputs (16 of a chunk's tokens each): a SIMD then has one of either, whose matrix
-// instructions, conversions and LDS reads fill each other's gaps. BUFS copies of a chunk's operands
-// in LDS: with two the next chunk's are written while this one's are read.
-template <bool F32, int DP, int NV, bool OUT>
-__global__ __launch_bounds__(OUT ? 512 : 256, OUT ? 2 : 2) void mix_walk(const MixParams p) {
+// instructions, conversions and LDS reads fill each other's gaps. They meet once a chunk.
+// DIRECT: operands whose rows are 16-byte aligned and not more than 2^31 bytes apart in a chunk go global -> LDS
+// by the direct loads, issued by the state's waves up to two chunks ahead, zeros past the last row and
+// column by the buffer's bounds; else all waves bring the next chunk's through registers.
+// EXACT: the state is a result, so its terms are not rounded to the operands' type.
+template <bool F32, int DP, int NV, bool OUT, bool DIRECT, bool EXACT>
+__global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix_walk(const MixParams p) {
   constexpr int ES = Type<F32>::ES, VEC = Type<F32>::VEC, KF = Type<F32>::KF;
   constexpr int THREADS = OUT ? 512 : 256;
-  constexpr int PB = DP * ES + 16, PC = NV * ES + (F32 ? 16 : 32);   // rows of LDS in bytes
+  using L = Layout<F32, DP, NV, OUT, DIRECT>;
+  constexpr int CHB = DP / VEC, CHC = NV / VEC;                // 16-byte pieces of a row of b (and of the state's copy), of c
   constexpr int WD = DP == 64 ? 2 : 4, WE = 4 / WD;            // waves over the state's rows and columns
   constexpr int MT = DP / WD / 16, NT = NV / WE / 16;          // its 16 x 16 tiles a wave
   constexpr int JS = C / KF;                                   // fragments over a chunk's tokens
   constexpr int DS = DP / KF;                                  // fragments over dim
-  constexpr int LB = (C * DP / VEC + THREADS - 1) / THREADS, LC = (C * NV / VEC + THREADS - 1) / THREADS;  // loads a thread and chunk
   constexpr int TILES = NV / 16;
-  constexpr int SET = C * PB + C * PC + (OUT ? NV * PB : 0);
-  constexpr int BUFS = 2 * SET <= (OUT ? 160 : 80) * 1024 ? 2 : 1;
   static_assert(MT * WD * 16 == DP && NT * WE * 16 == NV, "whole tiles");
-  __shared__ __attribute__((aligned(16))) char lds[BUFS * SET];
+  static_assert(!DIRECT || L::STAGES > 1, "direct loads need a second stage");
+  __shared__ __attribute__((aligned(1024))) char lds_all[L::BYTES];
+  lds_char* const lds = (lds_char*)lds_all;
+  auto stage_of = [&](int i) { return i * (L::B + L::CB); };                       // offsets
+  auto copy_of = [&](int i) { return L::STAGES * (L::B + L::CB) + i * L::Z; };
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -179,73 +267,101 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT ? 2 : 2) void mix_walk(const M
   auto base = [&](const MixArray& x) {
     return static_cast<const char*>(x.p) + (batch * x.sb + (head / x.group) * x.sh) * ES;
   };
-
-  // ---- b and c of a chunk: on their way in registers, then in LDS ----
   const char* rows_b = base(o.b);
   const char* rows_c = base(o.c) + e0 * ES;
   const int64_t sb = o.b.st * ES, sc = o.c.st * ES;
+
+  // A chunk's rows of an array as a buffer: its first token in memory, and the bytes to the end of its last row.
+  struct Window {
+    const char* p;
+    int bytes, down;   // reversed: row i of the chunk lies at (rows - 1 - i) strides
+  };
+  auto window = [&](const char* rows, int64_t stride, int width, int r0) -> Window {
+    const int count = min(live - r0, C);
+    if (count <= 0) return {rows, 0, 0};
+    const int64_t first = rev ? n - r0 - count : r0;
+    return {rows + first * stride, static_cast<int>((count - 1) * stride) + width * ES, rev ? static_cast<int>((count - C) * stride) : 0};
+  };
+  constexpr uint32_t OUTSIDE = 0x80000000u;
+
+  // ---- b and c of a chunk through registers ----
+  constexpr int LB = DIRECT ? 1 : (C * CHB + THREADS - 1) / THREADS, LC = DIRECT ? 1 : (C * CHC + THREADS - 1) / THREADS;
   u32x4 nb[LB], nc[LC];
   auto request = [&](int r0) {
-    const bool inside = r0 + C <= live;
-    if (inside && dim == DP) {
+    if constexpr (!DIRECT) {
 #pragma unroll
       for (int j = 0; j < LB; ++j) {
-        const int x = j * THREADS + tid, row = x / (DP / VEC), c = x % (DP / VEC) * VEC;
-        if (C * DP / VEC % THREADS == 0 || row < C) nb[j] = load_whole<F32>(rows_b + token(r0 + row) * sb, c);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < LB; ++j) {
-        const int x = j * THREADS + tid, row = x / (DP / VEC), c = x % (DP / VEC) * VEC;
+        const int x = j * THREADS + tid, row = x / CHB, c = x % CHB * VEC;
         nb[j] = u32x4{0, 0, 0, 0};
         if (row < C && r0 + row < live && c < dim) nb[j] = load_row<F32>(rows_b + token(r0 + row) * sb, c, dim);
       }
-    }
-    if (inside && cols == NV) {
 #pragma unroll
       for (int j = 0; j < LC; ++j) {
-        const int x = j * THREADS + tid, row = x / (NV / VEC), c = x % (NV / VEC) * VEC;
-        if (C * NV / VEC % THREADS == 0 || row < C) nc[j] = load_whole<F32>(rows_c + token(r0 + row) * sc, c);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < LC; ++j) {
-        const int x = j * THREADS + tid, row = x / (NV / VEC), c = x % (NV / VEC) * VEC;
+        const int x = j * THREADS + tid, row = x / CHC, c = x % CHC * VEC;
         nc[j] = u32x4{0, 0, 0, 0};
         if (row < C && r0 + row < live && c < cols) nc[j] = load_row<F32>(rows_c + token(r0 + row) * sc, c, cols);
       }
     }
   };
-  auto keep = [&](char* set) {
+  auto keep = [&](int set) {
+    if constexpr (!DIRECT) {
 #pragma unroll
-    for (int j = 0; j < LB; ++j) {
-      const int x = j * THREADS + tid;
-      if (C * DP / VEC % THREADS == 0 || x < C * DP / VEC)
-        *reinterpret_cast<u32x4*>(set + x / (DP / VEC) * PB + x % (DP / VEC) * 16) = nb[j];
-    }
+      for (int j = 0; j < LB; ++j) {
+        const int x = j * THREADS + tid;
+        if (C * CHB % THREADS == 0 || x < C * CHB) write16(lds + set + piece<F32, CHB>(x / CHB, x % CHB), nb[j]);
+      }
 #pragma unroll
-    for (int j = 0; j < LC; ++j) {
-      const int x = j * THREADS + tid, ch = x % (NV / VEC);
-      char* row = set + C * PB + x / (NV / VEC) * PC;
-      if (C * NV / VEC % THREADS == 0 || x < C * NV / VEC) {
-        if constexpr (F32) {
-          *reinterpret_cast<u32x4*>(row + ch * 16) = nc[j];
-        } else {
-          // columns by tile: of 32, the fours of the even tile first (its transpose reads then take 32 bytes a row)
-          *reinterpret_cast<u32x2*>(row + (ch >> 2) * 64 + (ch & 3) * 8) = u32x2{nc[j][0], nc[j][1]};
-          *reinterpret_cast<u32x2*>(row + (ch >> 2) * 64 + (ch & 3) * 8 + 32) = u32x2{nc[j][2], nc[j][3]};
-        }
+      for (int j = 0; j < LC; ++j) {
+        const int x = j * THREADS + tid;
+        if (C * CHC % THREADS == 0 || x < C * CHC) write16(lds + set + L::B + piece<F32, CHC>(x / CHC, x % CHC), nc[j]);
       }
     }
   };
 
   const bool carried = o.z_in && (p.z_in_per_segment || seg == 0);
-  if (begin < live) request(begin);
 
   if (!OUT || wave >= 4) {
-    // ---- the state: rows d = dbase + col_of(mt, .), columns e = col_of(we NT + nt, .) ----
+    // ---- the state: rows d = dbase + 16 mt + .., columns e = 16 (we NT + nt) + .. ----
     const int own = wave & 3, wd = own % WD, we = own / WD;
     const int dbase = wd * (DP / WD);
+
+    // the direct loads: instruction j of this wave fills 64 pieces of b or c
+    constexpr int IB = DIRECT ? C * CHB / 256 : 1, IC = DIRECT ? C * CHC / 256 : 1;
+    uint32_t b_at[IB], c_at[IC];
+    if constexpr (DIRECT) {
+      auto from = [&](int x, int chunks, int r, int c, int64_t stride, int width) -> uint32_t {
+        return c * VEC < width ? static_cast<uint32_t>((rev ? C - 1 - r : r) * static_cast<int>(stride) + c * 16) : OUTSIDE;
+      };
+#pragma unroll
+      for (int j = 0; j < IB; ++j) {
+        const int x = (own * IB + j) * 64 + lane, r = x / CHB;
+        b_at[j] = from(x, CHB, r, (x % CHB) ^ mixed<F32, CHB>(r), sb, dim);
+      }
+#pragma unroll
+      for (int j = 0; j < IC; ++j) {
+        const int x = (own * IC + j) * 64 + lane, r = x / CHC;
+        c_at[j] = from(x, CHC, r, (x % CHC) ^ mixed<F32, CHC>(r), sc, cols);
+      }
+    }
+    auto issue = [&](int r0, int stage) {
+      if constexpr (DIRECT) {
+        const Window wb = window(rows_b, sb, dim, r0), wc = window(rows_c, sc, cols, r0);
+        char* to = lds_all + stage * (L::B + L::CB);
+        const auto fb = make_rsrc(wb.p, wb.bytes), fc = make_rsrc(wc.p, wc.bytes);
+#pragma unroll
+        for (int j = 0; j < IB; ++j) buf_load_lds(fb, to + (own * IB + j) * 1024, b_at[j] + wb.down, 0);
+#pragma unroll
+        for (int j = 0; j < IC; ++j) buf_load_lds(fc, to + L::B + (own * IC + j) * 1024, c_at[j] + wc.down, 0);
+      }
+    };
+    constexpr int AHEAD = L::STAGES - 1;
+    if constexpr (DIRECT) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) issue(begin + k * C, k);
+    } else if (begin < live) {
+      request(begin);
+    }
+
     f32x4 z[MT][NT];
     {
       const float* src = nullptr;
@@ -254,35 +370,31 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT ? 2 : 2) void mix_walk(const M
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int e = col_of<F32>(we * NT + nt, l16);
+          const int e = 16 * (we * NT + nt) + l16;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int d = dbase + col_of<F32>(mt, 4 * g + r);
+            const int d = dbase + 16 * mt + 4 * g + r;
             z[mt][nt][r] = src && d < dim && e < cols ? src[d * o.z_row + (e0 + e) * o.z_col] : 0.0f;
           }
         }
     }
-    // its copy for the outputs, dim_v (by tile) x dim. 16-bit: rounded to bf16, as the operand of q Z, like the
-    // scores as that of the product with v
-    auto show = [&](char* set) {
+    // its copy for the outputs, dim_v x dim. 16-bit: rounded to bf16, as the operand of q Z, like the scores
+    // as that of the product with v
+    const int z_lane = F32 ? piece<true, CHB>(l16, g) : piece<false, CHB>(l16, g >> 1) + (g & 1) * 8;
+    auto show = [&](int copy) {
       if constexpr (OUT) {
+        const int at = (copy + z_lane) ^ dbase * ES;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          char* row = set + C * (PB + PC) + (16 * (we * NT + nt) + l16) * PB + dbase * ES;
-          if constexpr (F32) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              *reinterpret_cast<u32x4*>(row + (16 * mt + 4 * g) * 4) = __builtin_bit_cast(u32x4, z[mt][nt]);
-          } else {
-#pragma unroll
-            for (int mt = 0; mt < MT; mt += 2)
-              *reinterpret_cast<u32x4*>(row + (16 * mt + 8 * g) * 2) =
-                  u32x4{pack(z[mt][nt][0], z[mt][nt][1]), pack(z[mt][nt][2], z[mt][nt][3]),
-                        pack(z[mt + 1][nt][0], z[mt + 1][nt][1]), pack(z[mt + 1][nt][2], z[mt + 1][nt][3])};
+          for (int mt = 0; mt < MT; ++mt) {
+            lds_char* const to = lds + (at ^ 16 * mt * ES) + 16 * (we * NT + nt) * CHB * 16;
+            if constexpr (F32) write16(to, __builtin_bit_cast(u32x4, z[mt][nt]));
+            else write8(to, u32x2{pack(z[mt][nt][0], z[mt][nt][1]), pack(z[mt][nt][2], z[mt][nt][3])});
           }
-        }
       }
     };
+    const int b_lane = columns_lane<F32, CHB>(lane) ^ dbase * ES, c_lane = columns_lane<F32, CHC>(lane) ^ we * NT * 16 * ES;
     // the weights of a chunk's tokens, in the order of `columns`
     float weight[JS][VEC];
     auto weigh = [&](int rows) {
@@ -298,68 +410,77 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT ? 2 : 2) void mix_walk(const M
     float over = __builtin_amdgcn_exp2f(g2 * C);
 
     if (begin < live) {
-      keep(lds);
-      show(lds);
+      keep(stage_of(0));
+      show(copy_of(0));
     }
-    int buf = 0;
+    int stage = 0, copy = 0;
     for (int r0 = begin; r0 < live; r0 += C) {
-      const char* set = lds + buf * SET;
+      if constexpr (DIRECT) wait_vmcnt<(AHEAD - 1) * (IB + IC)>();   // this chunk's are in, the next one's may be on their way
       meet();
+      const int set_b = stage_of(stage) + b_lane, set_c = stage_of(stage) + L::B + c_lane;
       const bool more = r0 + C < live;
-      if (more) request(r0 + C);
+      if constexpr (DIRECT) issue(r0 + AHEAD * C, stage + AHEAD < L::STAGES ? stage + AHEAD : stage + AHEAD - L::STAGES);
+      else if (more) request(r0 + C);
       const int rows = min(live - r0, C);
       if (rows < C) {
         weigh(rows);
         over = __builtin_amdgcn_exp2f(g2 * rows);
       }
-      // weighted b of this wave's rows. 16-bit: as three parts whose sum has the product's 24
-      // bits, so that the state is the sum of unrounded terms
-      constexpr int PARTS = F32 ? 1 : 3;
-      u32x4 kf[PARTS][MT][JS];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int s = 0; s < JS; ++s) {
-          const u32x4 f = columns<F32, PB, false>(set + dbase * ES, mt, s, lane);
-          if constexpr (F32) {
+        for (int nt = 0; nt < NT; ++nt) z[mt][nt] *= over;
+      // Weighted b of this wave's rows, 32 rows and one fragment's tokens at a time. 16-bit: one part, rounded as
+      // the product's operand, or where the state is a result three, whose sum has the product's 24 bits
+      {
+        constexpr int PARTS = EXACT && !F32 ? 3 : 1, PAIR = 2;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) kf[0][mt][s][e] = __float_as_uint(__uint_as_float(f[e]) * weight[s][e]);
-          } else {
+        for (int m0 = 0; m0 < MT; m0 += PAIR)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float lo = __uint_as_float(f[e] << 16) * weight[s][2 * e];
-              float hi = __uint_as_float(f[e] & 0xFFFF0000u) * weight[s][2 * e + 1];
+          for (int s = 0; s < JS; ++s) {
+            u32x4 kf[PARTS][PAIR];
 #pragma unroll
-              for (int q = 0; q < PARTS; ++q) {
-                const unsigned int w = pack(lo, hi);
-                kf[q][mt][s][e] = w;
-                lo -= __uint_as_float(w << 16);
-                hi -= __uint_as_float(w & 0xFFFF0000u);
+            for (int mt = 0; mt < PAIR; ++mt) {
+              const u32x4 f = columns<F32, CHB>(lds, set_b, m0 + mt, s);
+              if constexpr (F32) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) kf[0][mt][e] = __float_as_uint(__uint_as_float(f[e]) * weight[s][e]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float lo = __uint_as_float(f[e] << 16) * weight[s][2 * e];
+                  float hi = __uint_as_float(f[e] & 0xFFFF0000u) * weight[s][2 * e + 1];
+#pragma unroll
+                  for (int q = 0; q < PARTS; ++q) {
+                    const unsigned int w = pack(lo, hi);
+                    kf[q][mt][e] = w;
+                    lo -= __uint_as_float(w << 16);
+                    hi -= __uint_as_float(w & 0xFFFF0000u);
+                  }
+                }
               }
             }
+            constexpr int G = NT < 4 ? NT : 4;
+            stream<NT, G>([&](int i) { return columns<F32, CHC>(lds, set_c, i, s); },
+                          [&](int i0, const u32x4 (&v)[G]) {
+#pragma unroll
+                            for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                              for (int i = 0; i < G; ++i)
+#pragma unroll
+                                for (int mt = 0; mt < PAIR; ++mt) mma<F32>(z[m0 + mt][i0 + i], kf[q][mt], v[i]);
+                          });
           }
-        }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        u32x4 v[JS];
-#pragma unroll
-        for (int s = 0; s < JS; ++s) v[s] = columns<F32, PC, true>(set + C * PB, we * NT + nt, s, lane);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          z[mt][nt] *= over;
-#pragma unroll
-          for (int s = 0; s < JS; ++s)
-#pragma unroll
-            for (int q = 0; q < PARTS; ++q) mma<F32>(z[mt][nt], kf[q][mt][s], v[s]);
-        }
       }
+      stage = stage + 1 < L::STAGES ? stage + 1 : 0;
+      copy = L::COPIES - 1 - copy;
       if (more) {
-        if constexpr (BUFS == 1) meet();
-        buf = BUFS == 2 ? buf ^ 1 : 0;
-        keep(lds + buf * SET);
-        show(lds + buf * SET);
+        if constexpr (L::STAGES == 1) meet();
+        keep(stage_of(stage));
+        show(copy_of(copy));
       }
     }
+    if constexpr (DIRECT) wait_vmcnt<0>();   // none into the LDS of a workgroup that has ended
 
     if (o.z_out && (p.z_out_per_segment || seg == (n > 0 ? (n - 1) / p.segment : 0))) {
       float* dst = o.z_out + (p.z_out_per_segment ? static_cast<int64_t>(bh) * p.segments + seg : bh) * dim * dim_v;
@@ -367,10 +488,10 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT ? 2 : 2) void mix_walk(const M
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int e = col_of<F32>(we * NT + nt, l16);
+          const int e = 16 * (we * NT + nt) + l16;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int d = dbase + col_of<F32>(mt, 4 * g + r);
+            const int d = dbase + 16 * mt + 4 * g + r;
             if (d < dim && e < cols) dst[static_cast<int64_t>(d) * dim_v + e0 + e] = z[mt][nt][r];
           }
         }
@@ -382,13 +503,19 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT ? 2 : 2) void mix_walk(const M
     const int i_tok = 16 * wave + l16;
     const char* rows_a = base(o.a);
     const int64_t sa = o.a.st * ES;
+    constexpr bool AHEAD = DS <= 8;                             // registers for the next chunk's too
     u32x4 na[DS];
+    uint32_t a_at = 0;
+    if constexpr (DIRECT) a_at = static_cast<uint32_t>((rev ? C - 1 - i_tok : i_tok) * static_cast<int>(sa)) + g * 16;
     auto request_a = [&](int r0) {
-      const char* row = rows_a + token(r0 + i_tok) * sa;
-      if (r0 + C <= live && dim == DP) {
+      if constexpr (DIRECT) {
+        const Window w = window(rows_a, sa, dim, r0);
+        const auto f = make_rsrc(w.p, w.bytes);
 #pragma unroll
-        for (int s = 0; s < DS; ++s) na[s] = load_whole<F32>(row, KF * s + VEC * g);
+        for (int s = 0; s < DS; ++s)
+          na[s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(f, KF * s + VEC * g < dim ? a_at + w.down + KF * s * ES : OUTSIDE, 0, 0));
       } else {
+        const char* row = rows_a + token(r0 + i_tok) * sa;
 #pragma unroll
         for (int s = 0; s < DS; ++s) {
           const int c = KF * s + VEC * g;
@@ -397,53 +524,52 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT ? 2 : 2) void mix_walk(const M
         }
       }
     };
-    float within[4][4];                                         // e^{g (i - s)} of the scores' tiles
+    // e^{g (i - s)} of the scores' tiles, 0 above the diagonal. All four tiles are computed by every wave: without
+    // branches their LDS reads and products overlap
+    float within[4][4];
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        within[jt][r] = __builtin_amdgcn_exp2f(g2 * max(i_tok - (16 * jt + 4 * g + r), 0)) * o.p_scale;
+      for (int r = 0; r < 4; ++r) {
+        const int d = i_tok - (16 * jt + 4 * g + r);
+        within[jt][r] = d < 0 ? 0.0f : __builtin_amdgcn_exp2f(g2 * d) * o.p_scale;
+      }
     const float reach = __builtin_amdgcn_exp2f(g2 * (i_tok + off)) * o.o_scale;
     const int64_t o_row = static_cast<int64_t>(p.heads) * dim_v;   // elements from token to token of the output
     const int64_t o_at = (static_cast<int64_t>(batch) * p.tokens * p.heads + head) * dim_v + e0;
 
     if (begin < live) {
-      request_a(begin);
-      keep(lds);
+      if constexpr (AHEAD) request_a(begin);
+      request(begin);
+      keep(stage_of(0));
     }
-    int buf = 0;
+    const int n_lane = rows_lane<F32, CHB>(lane), c_lane = columns_lane<F32, CHC>(lane);
+    int stage = 0, copy = 0;
     for (int r0 = begin; r0 < live; r0 += C) {
-      const char* set = lds + buf * SET;
       meet();
+      const int set_n = stage_of(stage) + n_lane, set_c = stage_of(stage) + L::B + c_lane;
       const bool more = r0 + C < live;
+      if constexpr (!AHEAD) request_a(r0);
       u32x4 a[DS];
 #pragma unroll
       for (int s = 0; s < DS; ++s) a[s] = na[s];
+      if constexpr (AHEAD && DIRECT) request_a(r0 + C);          // past the last chunk: zeros
       if (more) {
         request(r0 + C);
-        request_a(r0 + C);
+        if constexpr (AHEAD && !DIRECT) request_a(r0 + C);
       }
-      // scores, transposed: rows s (the chunk's tokens up to its own), columns this wave's tokens
+      // scores, transposed: rows s, columns this wave's tokens
       u32x4 score[JS];
       {
         f32x4 sc4[4];
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt) {
-          sc4[jt] = f32x4{0, 0, 0, 0};
-          if (jt <= wave) {
+        for (int jt = 0; jt < 4; ++jt) sc4[jt] = f32x4{0, 0, 0, 0};
+        stream<4 * DS, 8>([&](int i) { return rows<CHB>(lds, set_n, i / DS, i % DS); },
+                          [&](int i0, const u32x4 (&k)[8]) { products<F32, DS>(sc4, i0, k, a); });
 #pragma unroll
-            for (int s = 0; s < DS; ++s) {
-              const u32x4 k = *reinterpret_cast<const u32x4*>(set + (16 * jt + l16) * PB + (KF * s + VEC * g) * ES);
-              mma<F32>(sc4[jt], k, a[s]);
-            }
+        for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sc4[jt][r] *= within[jt][r];
-            if (jt == wave) {
-#pragma unroll
-              for (int r = 0; r < 4; ++r) sc4[jt][r] = 4 * g + r <= l16 ? sc4[jt][r] : 0.0f;
-            }
-          }
-        }
+          for (int r = 0; r < 4; ++r) sc4[jt][r] *= within[jt][r];
 #pragma unroll
         for (int s = 0; s < JS; ++s) {
           if constexpr (F32) score[s] = __builtin_bit_cast(u32x4, sc4[s]);
@@ -452,52 +578,51 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT ? 2 : 2) void mix_walk(const M
                              pack(sc4[2 * s + 1][0], sc4[2 * s + 1][1]), pack(sc4[2 * s + 1][2], sc4[2 * s + 1][3])};
         }
       }
-      const bool have = carried || r0 > begin;
-      const bool mine = o.out && r0 + i_tok < live;
+      f32x4 x[TILES];
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) x[t] = f32x4{0, 0, 0, 0};
+      if (carried || r0 > begin) {
+        const int z = copy_of(copy) + n_lane;
+        constexpr int GZ = TILES * DS < 8 ? TILES * DS : 8;
+        stream<TILES * DS, GZ>([&](int i) { return rows<CHB>(lds, z, i / DS, i % DS); },
+                               [&](int i0, const u32x4 (&k)[GZ]) { products<F32, DS>(x, i0, k, a); });
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) x[t] *= reach;
+      }
+      constexpr int G = TILES * JS < 8 ? TILES * JS : 8;
+      stream<TILES * JS, G>([&](int i) { return columns<F32, CHC>(lds, set_c, i / JS, i % JS); },
+                            [&](int i0, const u32x4 (&v)[G]) { products<F32, JS>(x, i0, v, score); });
+      stage = stage + 1 < L::STAGES ? stage + 1 : 0;
+      copy = L::COPIES - 1 - copy;
+      if (more) {
+        if constexpr (L::STAGES == 1) meet();
+        keep(stage_of(stage));
+      }
+      // After the next chunk's loads are in: waiting for those does not wait for these stores. A lane holds
+      // columns 16 t + 4 g .. + 3 of its token.
       const int64_t o_tok = o_at + token(r0 + i_tok) * o_row;
-      f32x4 acc[2];
+      if (o.out && r0 + i_tok < live) {
+        if (F32 || o.out_f32) {
 #pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        f32x4 x{0, 0, 0, 0};
-        if (have) {
-#pragma unroll
-          for (int s = 0; s < DS; ++s) {
-            const u32x4 k = *reinterpret_cast<const u32x4*>(set + C * (PB + PC) + (16 * t + l16) * PB + (KF * s + VEC * g) * ES);
-            mma<F32>(x, k, a[s]);
-          }
-          x *= reach;
-        }
-#pragma unroll
-        for (int s = 0; s < JS; ++s)
-          if (KF * s <= 16 * wave) mma<F32>(x, columns<F32, PC, true>(set + C * PB, t, s, lane), score[s]);
-        acc[t & 1] = x;
-        // lane: token i_tok, columns of the tile (pair) 16 g .. or 32 .. + 8 g ..
-        if constexpr (F32) {
-          if (mine) {
+          for (int t = 0; t < TILES; ++t) {
             float* out = static_cast<float*>(o.out) + o_tok + 16 * t + 4 * g;
             const int left = cols - (16 * t + 4 * g);
-            if (left >= 4) *reinterpret_cast<u32x4_a4*>(out) = __builtin_bit_cast(u32x4, x);
+            if (left >= 4) *reinterpret_cast<u32x4_a4*>(out) = __builtin_bit_cast(u32x4, x[t]);
             else
 #pragma unroll
               for (int r = 0; r < 4; ++r)
-                if (r < left) out[r] = x[r];
+                if (r < left) out[r] = x[t][r];
           }
-        } else if (t & 1) {
-          const int c = 32 * (t >> 1) + 8 * g, left = cols - c;
-          if (mine && o.out_f32) {
-            float* out = static_cast<float*>(o.out) + o_tok + c;
+        } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (left >= 4 * h + 4) *reinterpret_cast<u32x4_a4*>(out + 4 * h) = __builtin_bit_cast(u32x4, acc[h]);
-              else
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  if (4 * h + r < left) out[4 * h + r] = acc[h][r];
-            }
-          } else if (mine) {
+          for (int t = 0; t < TILES; t += 2) {
+            // lane groups 1 and 3 of the even tile change places with 0 and 2 of the odd one: eight columns each
+            const auto lo = __builtin_amdgcn_permlane16_swap(pack(x[t][0], x[t][1]), pack(x[t + 1][0], x[t + 1][1]), false, false);
+            const auto hi = __builtin_amdgcn_permlane16_swap(pack(x[t][2], x[t][3]), pack(x[t + 1][2], x[t + 1][3]), false, false);
+            const int c = 16 * (t + (g & 1)) + 8 * (g >> 1), left = cols - c;
             unsigned short* out = static_cast<unsigned short*>(o.out) + o_tok + c;
-            const u32x4 w{pack(acc[0][0], acc[0][1]), pack(acc[0][2], acc[0][3]), pack(acc[1][0], acc[1][1]),
-                          pack(acc[1][2], acc[1][3])};
+            const u32x4 w{static_cast<unsigned int>(lo[0]), static_cast<unsigned int>(hi[0]), static_cast<unsigned int>(lo[1]),
+                          static_cast<unsigned int>(hi[1])};
             if (left >= 8) *reinterpret_cast<u32x4_a2*>(out) = w;
             else
 #pragma unroll
@@ -505,11 +630,6 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT ? 2 : 2) void mix_walk(const M
                 if (r < left) out[r] = static_cast<unsigned short>(w[r / 2] >> (16 * (r & 1)));
           }
         }
-      }
-      if (more) {
-        if constexpr (BUFS == 1) meet();
-        buf = BUFS == 2 ? buf ^ 1 : 0;
-        keep(lds + buf * SET);
       }
     }
     // rows behind the last token: zeros
@@ -627,19 +747,28 @@ __global__ __launch_bounds__(256) void mix_step(const MixStep p) {
   }
 }
 
-template <bool F32, int DP, int NV>
+template <bool F32, int DP, int NV, bool DIRECT, bool EXACT>
 hipError_t walk(bool out, const MixParams& p, int64_t groups, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(groups));
-  if (out) mix_walk<F32, DP, NV, true><<<grid, 512, 0, st>>>(p);
-  else mix_walk<F32, DP, NV, false><<<grid, 256, 0, st>>>(p);
+  if (out) mix_walk<F32, DP, NV, true, DIRECT, EXACT><<<grid, 512, 0, st>>>(p);
+  else mix_walk<F32, DP, NV, false, DIRECT, EXACT><<<grid, 256, 0, st>>>(p);
   return hipGetLastError();
+}
+template <bool F32, int DP, int NV>
+hipError_t walk(bool out, const MixParams& p, int64_t groups, hipStream_t st) {
+  if constexpr (Layout<F32, DP, NV, true, true>::STAGES > 1 && Layout<F32, DP, NV, false, true>::STAGES > 1)
+    if (p.direct)
+      return F32 || p.exact ? walk<F32, DP, NV, true, true>(out, p, groups, st) : walk<F32, DP, NV, true, F32>(out, p, groups, st);
+  return F32 || p.exact ? walk<F32, DP, NV, false, true>(out, p, groups, st) : walk<F32, DP, NV, false, F32>(out, p, groups, st);
 }
 template <bool F32>
 hipError_t walk(MixTile t, bool out, const MixParams& p, int64_t groups, hipStream_t st) {
   if (t.dim == 64) return t.dim_v == 64 ? walk<F32, 64, 64>(out, p, groups, st) : walk<F32, 64, 32>(out, p, groups, st);
-  if (t.dim == 128)
-    return t.dim_v == 128 ? walk<F32, 128, 128>(out, p, groups, st)
-           : t.dim_v == 64 ? walk<F32, 128, 64>(out, p, groups, st) : walk<F32, 128, 32>(out, p, groups, st);
+  if (t.dim == 128) {
+    if constexpr (!F32)
+      if (t.dim_v == 128) return walk<F32, 128, 128>(out, p, groups, st);
+    return t.dim_v == 64 ? walk<F32, 128, 64>(out, p, groups, st) : walk<F32, 128, 32>(out, p, groups, st);
+  }
   return t.dim_v == 64 ? walk<F32, 256, 64>(out, p, groups, st) : walk<F32, 256, 32>(out, p, groups, st);
 }
 

@@ -70,7 +70,7 @@ def check(X, ins, dtype, scale=None, lengths=None, norm=True):
         inside(x, r, b, name)
     if norm:
         # independent roundings of random values, each about 0.42 of a half step (uniform over the step, averaged over a
-        # binade): the result's and a score's or the state's copy: 0.42 sqrt(2) = 0.6
+        # binade): the result's and a score's or, through the state, two: at most 0.42 sqrt(1 + 2) = 0.73
         for x, r, name in zip((o, *grads[:3]), (want[0], *gwant[:3]), ("o", "dq", "dk", "dv")):
             if dtype == "bf16" and r.size >= 4096:
                 assert rel(to_np(x), r) <= h, name
@@ -133,7 +133,7 @@ def test_strides(X, dtype):
     late.copy_(do)
     for a in ((first(q), first(k), first(v), first(do)), (*joint, late)):
         o, last = X.linear_attention_forward(*a[:3], g, final=True)
-        grads = X.linear_attention_backward(a[3], *a[:3], g)
+        grads = X.linear_attention_backward(a[3], *a[:3], g, need_dstate=True)
         assert torch.equal(o, base[0]) and torch.equal(last, base[1])
         assert all(torch.equal(x, y) for x, y in zip(grads[:3], base[2][:3]))
     # one head of k and v for all, as a broadcast view and as a shared head
@@ -207,7 +207,8 @@ def test_wanted_gradients_alone(X):
             got = X.linear_attention_backward(do, q, k, v, g, state=s, d_final=df, need=need, need_dstate=ds)
             for x, y, n in zip(got, full, (*need, ds)):
                 assert (x is None) == (not n)
-                assert not n or torch.equal(x, y)
+                # a state that leaves is summed unrounded, so the others' last bits differ from those without
+                assert not n or (torch.equal(x, y) if ds else rel(to_np(x), to_np(y)) <= 2.0 ** -8)
 
 
 def test_same_from_run_to_run(X):
