@@ -79,7 +79,7 @@ hipError_t launch_mix_step(bool f32, const MixStep& p, hipStream_t st);
 
 // ---- tokens by expert (experts.hip) ----
 constexpr int kMaxExperts = 1024;
-constexpr int kPlanBlock = 2048;         // choices a workgroup sorts
+constexpr int kPlanBlock = 1024;         // choices a workgroup sorts
 struct PlanParams {
   const void* ids; int32_t ids64;
   int64_t n;                             // choices: tokens x top
@@ -96,6 +96,7 @@ struct RowsParams {
   int64_t ld_in, ld_in2, ld_out;
   int64_t tokens;
   int32_t top, experts, dim;
+  int32_t once;                          // the sorted rows are more than the caches keep: read past them
 };
 enum RowsOp : int { ROWS_DISPATCH = 0, ROWS_COMBINE = 1, ROWS_COMBINE_GRAD = 2 };
 hipError_t launch_expert_rows(RowsOp op, bool f32, const RowsParams& p, hipStream_t st);

@@ -80,30 +80,68 @@ struct MixPlan {
   size_t off_rev = 0, off_dk = 0, off_dv = 0, bytes = 0;  // workspace: states, states of the reversed walk, partial dk, dv
 };
 
+// Times of a walk in us, [fp32][dim 64, 128, 256][slice 32, 64, 128]: a chunk and the start and end of the walk with
+// outputs, then of the one that only sums a segment's state. Measured with one workgroup on every CU (the second:
+// on every other one), 4 to 32 chunks.
+struct MixTime {
+  float chunk, ends, sum_chunk, sum_ends;
+};
+constexpr MixTime kMixTime[2][3][3] = {
+    {{{1.14f, 6.2f, 0.73f, 6.0f}, {1.5f, 6.2f, 0.8f, 6.2f}, {}},
+     {{1.85f, 5.5f, 0.9f, 6.3f}, {2.5f, 6.0f, 1.2f, 8.0f}, {3.9f, 7.0f, 2.3f, 7.5f}},
+     {{4.2f, 8.0f, 2.1f, 6.0f}, {4.7f, 10.0f, 2.8f, 9.0f}, {}}},
+    {{{3.2f, 5.0f, 0.9f, 5.5f}, {5.0f, 7.0f, 1.55f, 4.5f}, {}},
+     {{5.7f, 5.0f, 1.7f, 4.4f}, {8.6f, 6.5f, 3.2f, 5.0f}, {}},
+     {{11.9f, 3.0f, 3.7f, 5.0f}, {16.0f, 8.0f, 5.9f, 8.0f}, {}}}};
+
+// A walk over all tokens with wide slices reads and computes least. More workgroups come from narrower slices
+// (scores and weighted operands are computed once a slice) or from segments (k and v are read twice, two more
+// launches, the states' traffic): the cheapest of both by the measured times. 128 (batch, head)s of 128 x
+// 128, 2048 tokens, forward: slices of 64 82 us, of 128 103 us, two segments 118 us; gradients (three walks): 222, 165
+// and 228 us. 16 of them, 65536 tokens: 16 or 32 segments with slices of 128 380 us, of 64 485 us, 8 segments 650 us.
 MixPlan plan_of(const muon_mix* m, const muon_mix_grads* g, int cus) {
   MixPlan p;
   p.bh = m->batch * m->heads;
-  const int most = std::max(m->dim, m->dim_v);
-  p.tile.dim = (g ? most : m->dim) <= 64 ? 64 : (g ? most : m->dim) <= 128 ? 128 : 256;
-  const int wide = g ? most : m->dim_v;
-  auto per_of = [&](int nv) -> int {
-    if (!g) return static_cast<int>(cdiv(m->dim_v, nv));
-    return static_cast<int>((g->dq ? cdiv(m->dim, nv) : 0) + (g->dk ? cdiv(m->dim, nv) : 0) +
-                            (g->dv || g->d_state ? cdiv(m->dim_v, nv) : 0));
-  };
-  int nv = p.tile.dim == 128 && m->dtype == MUON_BF16 ? 128 : 64;
-  if (wide <= 64) nv = std::min(nv, 64);
-  if (wide <= 32) nv = 32;
-  p.tile.dim_v = nv;
-  p.per = std::max(per_of(nv), 1);
+  const bool f32 = m->dtype == MUON_F32;
+  const int wide = g ? std::max(m->dim, m->dim_v) : m->dim_v, deep = g ? wide : m->dim;
+  const int di = deep <= 64 ? 0 : deep <= 128 ? 1 : 2;
+  p.tile.dim = 64 << di;
   const int64_t chunks = std::max<int64_t>(cdiv(m->tokens, kMixChunk), 1);
-  int64_t want = cdiv(2 * cus, std::max<int64_t>(p.bh * p.per, 1));
-  want = std::min<int64_t>(want, cdiv(chunks, 4));
-  want = std::max<int64_t>(want, 1);
-  const int64_t each = cdiv(chunks, want);
-  p.segment = static_cast<int>(each * kMixChunk);
-  p.segments = static_cast<int>(cdiv(chunks, each));
   const int64_t state = int64_t{4} * m->dim * m->dim_v;
+  const bool back = g && (g->dk || g->dv || g->d_state);
+  const int sums = g ? (g->dq ? 1 : 0) + (back ? 1 : 0) : 1;   // directions whose segments' states are summed
+  double best = 1e300;
+  for (int vi = 0; vi < 3; ++vi) {
+    const MixTime& t = kMixTime[f32][di][vi];
+    const int nv = 32 << vi;
+    if (t.chunk == 0.0f || (vi > 0 && nv >= 2 * wide)) continue;
+    const int64_t v_slices = cdiv(m->dim_v, nv);
+    const int64_t per = !g ? v_slices
+                           : std::max<int64_t>(((g->dq ? 1 : 0) + (g->dk ? 1 : 0)) * cdiv(m->dim, nv) + (g->dv || g->d_state ? v_slices : 0), 1);
+    int64_t last = 0;
+    for (int64_t want = 1; want <= 256 && want <= chunks; want += std::max<int64_t>(1, want / 8)) {
+      const int64_t each = cdiv(chunks, want), segments = cdiv(chunks, each);
+      if (segments == last) continue;
+      last = segments;
+      if (segments > 1 && p.bh * segments * state > (int64_t{1} << 30)) break;
+      // a last round that leaves CUs idle costs less than a whole one
+      auto rounds = [&](int64_t groups, double slots) {
+        const double r = groups / slots, whole = std::floor(r);
+        return r <= 1.0 ? 1.0 : whole + (r > whole ? 0.5 + 0.5 * (r - whole) : 0.0);
+      };
+      double us = rounds(p.bh * per * segments, cus) * (each * static_cast<double>(t.chunk) + t.ends);
+      if (segments > 1)
+        us += rounds(p.bh * sums * v_slices * (segments - 1), 1.3 * cus) * (each * static_cast<double>(t.sum_chunk) + t.sum_ends) + 4.0 +
+              2.0 * sums * p.bh * segments * state / 4e6;
+      if (us < best) {
+        best = us;
+        p.tile.dim_v = nv;
+        p.per = static_cast<int>(per);
+        p.segment = static_cast<int>(each * kMixChunk);
+        p.segments = static_cast<int>(segments);
+      }
+    }
+  }
   if (p.segments > 1) {
     const size_t z = align_up(static_cast<size_t>(p.bh * p.segments * state));
     p.off_rev = z;
@@ -188,7 +226,7 @@ bool rows_ok(const void* p, int64_t ld, int64_t dim, int dtype, bool needed) {
   return ld >= dim && span_ok(int64_t{1} << 25, ld) && aligned(p, size_of(dtype)) && (p || !needed);
 }
 
-RowsParams rows_params(const muon_experts* e, int64_t dim) {
+RowsParams rows_params(const muon_experts* e, int64_t dim, int dtype) {
   RowsParams p;
   std::memset(&p, 0, sizeof(p));
   p.slots = e->slots;
@@ -197,6 +235,7 @@ RowsParams rows_params(const muon_experts* e, int64_t dim) {
   p.top = e->top;
   p.experts = e->experts;
   p.dim = static_cast<int32_t>(dim);
+  p.once = e->tokens * e->top * dim * size_of(dtype) > (int64_t{128} << 20);  // half the 256 MB cache
   return p;
 }
 
@@ -458,7 +497,7 @@ int muon_expert_dispatch(muon_ctx* ctx, const muon_experts* e, const void* token
     if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
     DeviceGuard dg(ctx_device(ctx));
     if (!dg.ok) return MUON_ERR_HIP;
-    RowsParams p = rows_params(e, dim);
+    RowsParams p = rows_params(e, dim, dtype);
     p.in = token; p.ld_in = ld_token;
     p.out = sorted; p.ld_out = ld_sorted;
     MUON_HIP(launch_expert_rows(ROWS_DISPATCH, dtype == MUON_F32, p, static_cast<hipStream_t>(stream)));
@@ -479,7 +518,7 @@ int muon_expert_combine(muon_ctx* ctx, const muon_experts* e, const void* sorted
     if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
     DeviceGuard dg(ctx_device(ctx));
     if (!dg.ok) return MUON_ERR_HIP;
-    RowsParams p = rows_params(e, dim);
+    RowsParams p = rows_params(e, dim, dtype);
     p.weights = weights;
     p.in = sorted; p.ld_in = ld_sorted;
     p.out = token; p.ld_out = ld_token;
@@ -503,7 +542,7 @@ int muon_expert_combine_backward(muon_ctx* ctx, const muon_experts* e, const voi
     if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
     DeviceGuard dg(ctx_device(ctx));
     if (!dg.ok) return MUON_ERR_HIP;
-    RowsParams p = rows_params(e, dim);
+    RowsParams p = rows_params(e, dim, dtype);
     p.weights = weights;
     p.in = d_token; p.ld_in = ld_token;
     p.in2 = sorted; p.ld_in2 = ld_sorted;

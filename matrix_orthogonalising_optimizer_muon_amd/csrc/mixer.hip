@@ -142,21 +142,47 @@ __device__ __forceinline__ u32x4 load_whole(const char* row, int c) {
   if constexpr (F32) return *reinterpret_cast<const u32x4_a4*>(row + c * 4);
   else return *reinterpret_cast<const u32x4_a2*>(row + c * 2);
 }
-// The same with zeros behind its `dim` columns.
+// Rows at any address and of any length, without a branch a load: the 16 bytes from column c on are asked for at the
+// last place where they lie inside the row, and moved down when they are there. Rows of less than
+// 16 bytes element by element.
 template <bool F32>
-__device__ __forceinline__ u32x4 load_row(const char* row, int c, int dim) {
-  constexpr int VEC = Type<F32>::VEC;
-  if (c + VEC <= dim) return load_whole<F32>(row, c);
-  u32x4 v{0, 0, 0, 0};
+struct Piece {
+  static constexpr int ES = F32 ? 4 : 2, VEC = 16 / ES;
+  int c, from;
+  bool in, narrow;
+  __device__ __forceinline__ Piece(int column, int dim)
+      : c(column), from(max(min(column, dim - VEC), 0)), in(column < dim), narrow(dim < VEC) {}
+  __device__ __forceinline__ u32x4 ask(const char* row, int dim) const {
+    if (!narrow) return load_whole<F32>(row, from);
+    u32x4 v{0, 0, 0, 0};
+#pragma unroll 1
+    for (int e = 0; e < dim; ++e) {              // only column 0's piece is used
+      unsigned int x;
+      if constexpr (F32) x = *reinterpret_cast<const unsigned int*>(row + e * 4);
+      else x = static_cast<unsigned int>(*reinterpret_cast<const unsigned short*>(row + e * 2)) << (16 * (e & 1));
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    if (c + e < dim) {
-      if constexpr (F32) v[e] = *reinterpret_cast<const unsigned int*>(row + (c + e) * 4);
-      else v[e / 2] |= static_cast<unsigned int>(*reinterpret_cast<const unsigned short*>(row + (c + e) * 2)) << (16 * (e & 1));
+      for (int w = 0; w < 4; ++w) v[w] |= w == e * ES / 4 ? x : 0u;
     }
+    return v;
   }
-  return v;
-}
+  // there: the row is one of the walk's
+  __device__ __forceinline__ u32x4 take(u32x4 v, bool there) const {
+    const int down = narrow ? 0 : c - from;      // elements
+    if constexpr (!F32) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_alignbit(e < 3 ? v[e + 1] : 0u, v[e], (down & 1) * 16);
+    }
+    const int words = F32 ? down : down >> 1;
+#pragma unroll
+    for (int step = 1; step <= 2; ++step)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = words & step ? (e + step < 4 ? v[e + step] : 0u) : v[e];
+    const bool here = in && there;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = here ? v[e] : 0u;
+    return v;
+  }
+};
 
 // N fragments from LDS in groups of G: a group is read while the one before is used. The compiler
 // alone waits for each read before the product it is for, and asks for the next one after that.
@@ -228,7 +254,6 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
   constexpr int DS = DP / KF;                                  // fragments over dim
   constexpr int TILES = NV / 16;
   static_assert(MT * WD * 16 == DP && NT * WE * 16 == NV, "whole tiles");
-  static_assert(!DIRECT || L::STAGES > 1, "direct loads need a second stage");
   __shared__ __attribute__((aligned(1024))) char lds_all[L::BYTES];
   lds_char* const lds = (lds_char*)lds_all;
   auto stage_of = [&](int i) { return i * (L::B + L::CB); };                       // offsets
@@ -286,34 +311,31 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
 
   // ---- b and c of a chunk through registers ----
   constexpr int LB = DIRECT ? 1 : (C * CHB + THREADS - 1) / THREADS, LC = DIRECT ? 1 : (C * CHC + THREADS - 1) / THREADS;
+  static_assert(THREADS % CHB == 0 && THREADS % CHC == 0, "a thread's pieces are of one column");
   u32x4 nb[LB], nc[LC];
+  const Piece<F32> piece_b(tid % CHB * VEC, dim), piece_c(tid % CHC * VEC, cols);
   auto request = [&](int r0) {
     if constexpr (!DIRECT) {
 #pragma unroll
-      for (int j = 0; j < LB; ++j) {
-        const int x = j * THREADS + tid, row = x / CHB, c = x % CHB * VEC;
-        nb[j] = u32x4{0, 0, 0, 0};
-        if (row < C && r0 + row < live && c < dim) nb[j] = load_row<F32>(rows_b + token(r0 + row) * sb, c, dim);
-      }
+      for (int j = 0; j < LB; ++j)
+        nb[j] = piece_b.ask(rows_b + token(min(r0 + tid / CHB + j * (THREADS / CHB), live - 1)) * sb, dim);
 #pragma unroll
-      for (int j = 0; j < LC; ++j) {
-        const int x = j * THREADS + tid, row = x / CHC, c = x % CHC * VEC;
-        nc[j] = u32x4{0, 0, 0, 0};
-        if (row < C && r0 + row < live && c < cols) nc[j] = load_row<F32>(rows_c + token(r0 + row) * sc, c, cols);
-      }
+      for (int j = 0; j < LC; ++j)
+        nc[j] = piece_c.ask(rows_c + token(min(r0 + tid / CHC + j * (THREADS / CHC), live - 1)) * sc, cols);
     }
   };
-  auto keep = [&](int set) {
+  auto keep = [&](int set, int r0) {
     if constexpr (!DIRECT) {
 #pragma unroll
       for (int j = 0; j < LB; ++j) {
-        const int x = j * THREADS + tid;
-        if (C * CHB % THREADS == 0 || x < C * CHB) write16(lds + set + piece<F32, CHB>(x / CHB, x % CHB), nb[j]);
+        const int r = tid / CHB + j * (THREADS / CHB);
+        if (C * CHB % THREADS == 0 || r < C) write16(lds + set + piece<F32, CHB>(r, tid % CHB), piece_b.take(nb[j], r0 + r < live));
       }
 #pragma unroll
       for (int j = 0; j < LC; ++j) {
-        const int x = j * THREADS + tid;
-        if (C * CHC % THREADS == 0 || x < C * CHC) write16(lds + set + L::B + piece<F32, CHC>(x / CHC, x % CHC), nc[j]);
+        const int r = tid / CHC + j * (THREADS / CHC);
+        if (C * CHC % THREADS == 0 || r < C)
+          write16(lds + set + L::B + piece<F32, CHC>(r, tid % CHC), piece_c.take(nc[j], r0 + r < live));
       }
     }
   };
@@ -354,7 +376,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
         for (int j = 0; j < IC; ++j) buf_load_lds(fc, to + L::B + (own * IC + j) * 1024, c_at[j] + wc.down, 0);
       }
     };
-    constexpr int AHEAD = L::STAGES - 1;
+    constexpr int AHEAD = L::STAGES > 1 ? L::STAGES - 1 : 1;     // with one stage: after everyone has read the last chunk
     if constexpr (DIRECT) {
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) issue(begin + k * C, k);
@@ -410,7 +432,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
     float over = __builtin_amdgcn_exp2f(g2 * C);
 
     if (begin < live) {
-      keep(stage_of(0));
+      keep(stage_of(0), begin);
       show(copy_of(0));
     }
     int stage = 0, copy = 0;
@@ -419,8 +441,8 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
       meet();
       const int set_b = stage_of(stage) + b_lane, set_c = stage_of(stage) + L::B + c_lane;
       const bool more = r0 + C < live;
-      if constexpr (DIRECT) issue(r0 + AHEAD * C, stage + AHEAD < L::STAGES ? stage + AHEAD : stage + AHEAD - L::STAGES);
-      else if (more) request(r0 + C);
+      if constexpr (DIRECT && L::STAGES > 1) issue(r0 + AHEAD * C, stage + AHEAD < L::STAGES ? stage + AHEAD : stage + AHEAD - L::STAGES);
+      else if (!DIRECT && more) request(r0 + C);
       const int rows = min(live - r0, C);
       if (rows < C) {
         weigh(rows);
@@ -430,10 +452,12 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) z[mt][nt] *= over;
-      // Weighted b of this wave's rows, 32 rows and one fragment's tokens at a time. 16-bit: one part, rounded as
-      // the product's operand, or where the state is a result three, whose sum has the product's 24 bits
+      // Weighted b of this wave's rows, 32 rows and one fragment's tokens at a time. 16-bit: in parts, each the rest of
+      // the ones before rounded as the product's operand: three, whose sum has the weighted value's 24 bits, where
+      // the state is a result; else two (one would add a rounding to outputs: 1.65 instead of 1.4 times the error of fp32
+      // throughout, for 12 us of 168 over 8 x 2048 tokens)
       {
-        constexpr int PARTS = EXACT && !F32 ? 3 : 1, PAIR = 2;
+        constexpr int PARTS = F32 ? 1 : EXACT ? 3 : 2, PAIR = 2;
 #pragma unroll
         for (int m0 = 0; m0 < MT; m0 += PAIR)
 #pragma unroll
@@ -475,8 +499,11 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
       stage = stage + 1 < L::STAGES ? stage + 1 : 0;
       copy = L::COPIES - 1 - copy;
       if (more) {
-        if constexpr (L::STAGES == 1) meet();
-        keep(stage_of(stage));
+        if constexpr (L::STAGES == 1) {
+          meet();
+          issue(r0 + C, 0);
+        }
+        keep(stage_of(stage), r0 + C);
         show(copy_of(copy));
       }
     }
@@ -504,6 +531,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
     const char* rows_a = base(o.a);
     const int64_t sa = o.a.st * ES;
     constexpr bool AHEAD = DS <= 8;                             // registers for the next chunk's too
+    constexpr int GN = DS <= 8 ? 8 : 4;                         // fragments in a group
     u32x4 na[DS];
     uint32_t a_at = 0;
     if constexpr (DIRECT) a_at = static_cast<uint32_t>((rev ? C - 1 - i_tok : i_tok) * static_cast<int>(sa)) + g * 16;
@@ -515,13 +543,9 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
         for (int s = 0; s < DS; ++s)
           na[s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(f, KF * s + VEC * g < dim ? a_at + w.down + KF * s * ES : OUTSIDE, 0, 0));
       } else {
-        const char* row = rows_a + token(r0 + i_tok) * sa;
+        const char* row = rows_a + token(min(r0 + i_tok, live - 1)) * sa;
 #pragma unroll
-        for (int s = 0; s < DS; ++s) {
-          const int c = KF * s + VEC * g;
-          na[s] = u32x4{0, 0, 0, 0};
-          if (r0 + i_tok < live && c < dim) na[s] = load_row<F32>(row, c, dim);
-        }
+        for (int s = 0; s < DS; ++s) na[s] = Piece<F32>(KF * s + VEC * g, dim).ask(row, dim);
       }
     };
     // e^{g (i - s)} of the scores' tiles, 0 above the diagonal. All four tiles are computed by every wave: without
@@ -541,7 +565,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
     if (begin < live) {
       if constexpr (AHEAD) request_a(begin);
       request(begin);
-      keep(stage_of(0));
+      keep(stage_of(0), begin);
     }
     const int n_lane = rows_lane<F32, CHB>(lane), c_lane = columns_lane<F32, CHC>(lane);
     int stage = 0, copy = 0;
@@ -552,7 +576,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
       if constexpr (!AHEAD) request_a(r0);
       u32x4 a[DS];
 #pragma unroll
-      for (int s = 0; s < DS; ++s) a[s] = na[s];
+      for (int s = 0; s < DS; ++s) a[s] = DIRECT ? na[s] : Piece<F32>(KF * s + VEC * g, dim).take(na[s], r0 + i_tok < live);
       if constexpr (AHEAD && DIRECT) request_a(r0 + C);          // past the last chunk: zeros
       if (more) {
         request(r0 + C);
@@ -564,8 +588,8 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
         f32x4 sc4[4];
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) sc4[jt] = f32x4{0, 0, 0, 0};
-        stream<4 * DS, 8>([&](int i) { return rows<CHB>(lds, set_n, i / DS, i % DS); },
-                          [&](int i0, const u32x4 (&k)[8]) { products<F32, DS>(sc4, i0, k, a); });
+        stream<4 * DS, GN>([&](int i) { return rows<CHB>(lds, set_n, i / DS, i % DS); },
+                          [&](int i0, const u32x4 (&k)[GN]) { products<F32, DS>(sc4, i0, k, a); });
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
@@ -583,20 +607,20 @@ __global__ __launch_bounds__(OUT ? 512 : 256, OUT || DP <= 128 ? 2 : 1) void mix
       for (int t = 0; t < TILES; ++t) x[t] = f32x4{0, 0, 0, 0};
       if (carried || r0 > begin) {
         const int z = copy_of(copy) + n_lane;
-        constexpr int GZ = TILES * DS < 8 ? TILES * DS : 8;
+        constexpr int GZ = TILES * DS < GN ? TILES * DS : GN;
         stream<TILES * DS, GZ>([&](int i) { return rows<CHB>(lds, z, i / DS, i % DS); },
                                [&](int i0, const u32x4 (&k)[GZ]) { products<F32, DS>(x, i0, k, a); });
 #pragma unroll
         for (int t = 0; t < TILES; ++t) x[t] *= reach;
       }
-      constexpr int G = TILES * JS < 8 ? TILES * JS : 8;
+      constexpr int G = TILES * JS < GN ? TILES * JS : GN;
       stream<TILES * JS, G>([&](int i) { return columns<F32, CHC>(lds, set_c, i / JS, i % JS); },
                             [&](int i0, const u32x4 (&v)[G]) { products<F32, JS>(x, i0, v, score); });
       stage = stage + 1 < L::STAGES ? stage + 1 : 0;
       copy = L::COPIES - 1 - copy;
       if (more) {
         if constexpr (L::STAGES == 1) meet();
-        keep(stage_of(stage));
+        keep(stage_of(stage), r0 + C);
       }
       // After the next chunk's loads are in: waiting for those does not wait for these stores. A lane holds
       // columns 16 t + 4 g .. + 3 of its token.
@@ -756,9 +780,7 @@ hipError_t walk(bool out, const MixParams& p, int64_t groups, hipStream_t st) {
 }
 template <bool F32, int DP, int NV>
 hipError_t walk(bool out, const MixParams& p, int64_t groups, hipStream_t st) {
-  if constexpr (Layout<F32, DP, NV, true, true>::STAGES > 1 && Layout<F32, DP, NV, false, true>::STAGES > 1)
-    if (p.direct)
-      return F32 || p.exact ? walk<F32, DP, NV, true, true>(out, p, groups, st) : walk<F32, DP, NV, true, F32>(out, p, groups, st);
+  if (p.direct) return F32 || p.exact ? walk<F32, DP, NV, true, true>(out, p, groups, st) : walk<F32, DP, NV, true, F32>(out, p, groups, st);
   return F32 || p.exact ? walk<F32, DP, NV, false, true>(out, p, groups, st) : walk<F32, DP, NV, false, F32>(out, p, groups, st);
 }
 template <bool F32>

@@ -35,9 +35,9 @@ class ExpertPlan:
     top: int
     experts: int
 
-    def _c(self):
-        return B.muon_experts(None, self.order.data_ptr(), self.slots.data_ptr(), self.offsets.data_ptr(), self.tokens,
-                              self.top, self.experts, 0, 0)
+    def __post_init__(self):
+        object.__setattr__(self, "_c", B.muon_experts(None, self.order.data_ptr(), self.slots.data_ptr(), self.offsets.data_ptr(),
+                                                      self.tokens, self.top, self.experts, 0, 0))
 
 
 def expert_plan(ids, experts: int) -> ExpertPlan:
@@ -58,7 +58,7 @@ def expert_plan(ids, experts: int) -> ExpertPlan:
     n = tokens * top
     both = torch.empty(2 * n + experts + 1, dtype=torch.int32, device=device)
     plan = ExpertPlan(both[:n], both[n:2 * n].view(ids.shape), both[2 * n:], tokens, top, experts)
-    e = plan._c()
+    e = B.muon_experts.from_buffer_copy(plan._c)
     e.ids = ids.data_ptr()
     e.id_dtype = B.MUON_I64 if ids.dtype == torch.int64 else B.MUON_I32
     ctx = context(device)
@@ -69,12 +69,12 @@ def expert_plan(ids, experts: int) -> ExpertPlan:
 
 
 def _rows(t, name, rows, plan, dim=None, dtype=None):
-    """(t as rows x dim, its row stride) after the checks."""
-    dtype_code(t, name)
+    """(t as rows x dim, its row stride, its type's code) after the checks."""
+    code = dtype_code(t, name)
     if t.dim() < 1 or t.shape[-1] < 1 or (dim is not None and t.shape[-1] != dim):
         raise ValueError(f"{name} has shape {tuple(t.shape)}" + ("" if dim is None else f", expected {dim} columns"))
     t2 = t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
-    return t2, matrix(t2, name, (rows, t.shape[-1]), t.dtype if dtype is None else dtype, plan.slots.device)
+    return t2, matrix(t2, name, (rows, t.shape[-1]), t.dtype if dtype is None else dtype, plan.slots.device), code
 
 
 def _check_plan(plan):
@@ -85,22 +85,22 @@ def _check_plan(plan):
 def dispatch_forward(x, plan: ExpertPlan):
     """The tokens' rows in the plan's order: (tokens x top) x dim."""
     _check_plan(plan)
-    x2, ld = _rows(x, "x", plan.tokens, plan)
+    x2, ld, code = _rows(x, "x", plan.tokens, plan)
     device, dim = x2.device, x2.shape[1]
     xs = torch.empty((plan.tokens * plan.top, dim), dtype=x2.dtype, device=device)
-    B.check(B.muon_expert_dispatch(context(device), plan._c(), x2.data_ptr(), ld, xs.data_ptr(), dim, dim,
-                                   dtype_code(x2, "x"), stream_of(device)), "muon_expert_dispatch")
+    B.check(B.muon_expert_dispatch(context(device), plan._c, x2.data_ptr(), ld, xs.data_ptr(), dim, dim,
+                                   code, stream_of(device)), "muon_expert_dispatch")
     return xs
 
 
 def _combine(rows, name, weights, plan):
     _check_plan(plan)
-    r2, ld = _rows(rows, name, plan.tokens * plan.top, plan)
+    r2, ld, code = _rows(rows, name, plan.tokens * plan.top, plan)
     device, dim = r2.device, r2.shape[1]
     w = None if weights is None else vector(weights, "weights", plan.tokens * plan.top, torch.float32, device)
     y = torch.empty((*plan.slots.shape[:-1], dim), dtype=r2.dtype, device=device)
-    B.check(B.muon_expert_combine(context(device), plan._c(), r2.data_ptr(), ld, w, y.data_ptr(), dim, dim,
-                                  dtype_code(r2, name), stream_of(device)), "muon_expert_combine")
+    B.check(B.muon_expert_combine(context(device), plan._c, r2.data_ptr(), ld, w, y.data_ptr(), dim, dim,
+                                  code, stream_of(device)), "muon_expert_combine")
     return y
 
 
@@ -120,15 +120,15 @@ def combine_backward(dy, ys, weights, plan: ExpertPlan, *, need=(True, True)):
     """(dys, dweights) for the gradient ``dy`` of y; ``need``: which of the two are wanted (None in
     the place of the other; ``ys`` may be None without the second)."""
     _check_plan(plan)
-    dy2, ld = _rows(dy, "dy", plan.tokens, plan)
+    dy2, ld, code = _rows(dy, "dy", plan.tokens, plan)
     device, dim, n = dy2.device, dy2.shape[1], plan.tokens * plan.top
-    ys2, ld_ys = _rows(ys, "ys", n, plan, dim, dy2.dtype) if need[1] else (None, dim)
+    ys2, ld_ys, _ = _rows(ys, "ys", n, plan, dim, dy2.dtype) if need[1] else (None, dim, code)
     w = None if weights is None else vector(weights, "weights", n, torch.float32, device)
     dys = torch.empty((n, dim), dtype=dy2.dtype, device=device) if need[0] else None
     dw = torch.empty(plan.slots.shape, dtype=torch.float32, device=device) if need[1] else None
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    B.check(B.muon_expert_combine_backward(context(device), plan._c(), dy2.data_ptr(), ld, ptr(ys2), ld_ys, w, ptr(dys),
-                                           dim, ptr(dw), dim, dtype_code(dy2, "dy"), stream_of(device)),
+    B.check(B.muon_expert_combine_backward(context(device), plan._c, dy2.data_ptr(), ld, ptr(ys2), ld_ys, w, ptr(dys),
+                                           dim, ptr(dw), dim, code, stream_of(device)),
             "muon_expert_combine_backward")
     return dys, dw
 

@@ -29,7 +29,7 @@ from .context import context, dtype_code, on_gpu, stream_of, vector, written
 
 
 def _strides(t, name, lead, dtype, device, last):
-    """(batch, token, head) strides of a 4-D operand after its checks."""
+    """The strides of an operand but for its last axis, after its checks."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
@@ -58,6 +58,13 @@ def _state(t, name, shape, device):
     return t.data_ptr()
 
 
+def _check_sizes(heads, kv_heads, dim, dim_v):
+    if kv_heads < 1 or heads % kv_heads:
+        raise ValueError(f"{heads} heads of q for {kv_heads} of k and v: not a multiple")
+    if not (1 <= dim <= B.MUON_MIX_MAX_DIM and 1 <= dim_v <= B.MUON_MIX_MAX_DIM):
+        raise ValueError(f"dim and dim_v must be between 1 and {B.MUON_MIX_MAX_DIM}, got {dim} and {dim_v}")
+
+
 def _problem(q, k, v, log_decay, scale, state, lengths):
     """(muon_mix, device, shape of the states, shape of o) after the checks."""
     code = dtype_code(q, "q")
@@ -66,10 +73,7 @@ def _problem(q, k, v, log_decay, scale, state, lengths):
         raise ValueError("q, k and v must be batch x tokens x heads x dim")
     batch, tokens, heads, dim = q.shape
     kv_heads, dim_v = v.shape[2:]
-    if kv_heads < 1 or heads % kv_heads:
-        raise ValueError(f"{heads} heads of q for {kv_heads} of k and v: not a multiple")
-    if not (1 <= dim <= B.MUON_MIX_MAX_DIM and 1 <= dim_v <= B.MUON_MIX_MAX_DIM):
-        raise ValueError(f"dim and dim_v must be between 1 and {B.MUON_MIX_MAX_DIM}, got {dim} and {dim_v}")
+    _check_sizes(heads, kv_heads, dim, dim_v)
     if scale is None:
         scale = 1.0 / math.sqrt(dim)
     shape = (batch, heads, dim, dim_v)
@@ -120,14 +124,26 @@ def linear_attention_backward(do, q, k, v, log_decay, *, scale: float | None = N
 def linear_attention_step(q, k, v, log_decay, state, *, scale: float | None = None, out_state=None):
     """(o, states) of one token: q is batch x heads x dim, k batch x kv_heads x dim, v batch x kv_heads x
     dim_v, o batch x heads x dim_v. The new states go to ``out_state``, or replace ``state``."""
-    if not all(isinstance(t, torch.Tensor) and t.dim() == 3 for t in (q, k, v)):
+    code = dtype_code(q, "q")
+    device = on_gpu(q, "q")
+    if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
         raise ValueError("q, k and v must be batch x heads x dim")
+    batch, heads, dim = q.shape
+    kv_heads, dim_v = v.shape[1:]
+    _check_sizes(heads, kv_heads, dim, dim_v)
     if state is None:
         raise ValueError("a step needs the states")
-    m, device, shape, o_shape = _problem(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), log_decay, scale, state, None)
+    shape = (batch, heads, dim, dim_v)
+    # (batch, head) strides; the token's is not read
+    (qb, qh), (kb, kh), (vb, vh) = (_strides(q, "q", (batch, heads), q.dtype, device, dim),
+                                    _strides(k, "k", (batch, kv_heads), q.dtype, device, dim),
+                                    _strides(v, "v", (batch, kv_heads), q.dtype, device, dim_v))
+    m = B.muon_mix(q.data_ptr(), k.data_ptr(), v.data_ptr(), vector(log_decay, "log_decay", heads, torch.float32, device),
+                   _state(state, "state", shape, device), None, (qb, 0, qh), (kb, 0, kh), (vb, 0, vh), batch, 1, heads,
+                   kv_heads, dim, dim_v, 1.0 / math.sqrt(dim) if scale is None else scale, code)
     new = state if out_state is None else out_state
-    to = _state(new, "out_state", shape, device)
-    o = torch.empty((o_shape[0], *o_shape[2:]), dtype=q.dtype, device=device)
+    to = m.state if out_state is None else _state(new, "out_state", shape, device)
+    o = torch.empty((batch, heads, dim_v), dtype=q.dtype, device=device)
     B.check(B.muon_mix_step(context(device), m, o.data_ptr(), to, stream_of(device)), "muon_mix_step")
     written(new)
     return o, new
