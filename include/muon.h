@@ -518,8 +518,9 @@ int muon_distill_loss(muon_ctx *ctx, const muon_logits *l, const muon_distill *t
  * Computed in chunks of 64 tokens (an infinity or NaN in a token may reach the tokens of its chunk
  * before it). MUON_BF16: products on the bf16 matrix instructions with fp32 sums; scores and the copy of
  * the state that q is multiplied with are rounded to bf16 as their operands. States that leave a
- * call are fp32 sums of unrounded terms. MUON_F32: fp32 throughout.
- * batch up to 2^20, heads to 2^16, batch x heads to 2^20, tokens to 2^24, dim and dim_v in [1, 256]. */
+ * call are fp32 sums of unrounded terms; where none leaves, the terms have 16 bits on the way (so whether
+ * one is wanted can change last bits of the other results). MUON_F32: fp32 throughout.
+ * batch and batch x heads up to 2^18, heads to 2^16, tokens to 2^24, dim and dim_v in [1, 256]. */
 #define MUON_MIX_MAX_DIM 256
 typedef struct muon_mix {
   const void *q, *k, *v;
@@ -612,7 +613,7 @@ int muon_expert_combine_backward(muon_ctx *ctx, const muon_experts *e, const voi
  * there is dropped too). Computed in fp32, rounded once.
  * counter (device memory, two uint64, 8-byte aligned; null: seed and offset as given): seed and offset, read when
  * the call runs, so that a captured graph's replays can differ.
- * rows in [0, 2^31), cols in [1, 2^36], rows x cols up to 2^36, row strides in [cols, 2^36], rows x stride up to 2^60. out may be x or residual
+ * rows in [0, 2^31), cols in [1, 2^34], rows x cols up to 2^34, row strides in [cols, 2^36], rows x stride up to 2^60. out may be x or residual
  * (same stride) and must not overlap them otherwise. */
 typedef struct muon_drop {
   const void *x, *residual;

@@ -48,15 +48,19 @@ __device__ __forceinline__ float get(const Eight<F32>& x, int e) {
   if constexpr (F32) return __uint_as_float(x.v[e >> 2][e & 3]);
   else return __uint_as_float(e & 1 ? x.v[0][e >> 1] & 0xFFFF0000u : x.v[0][e >> 1] << 16);
 }
-template <bool F32>
+template <bool F32, bool ONCE>
 __device__ __forceinline__ Eight<F32> load8(const void* p, int64_t at) {
   Eight<F32> x;
+  auto load = [](auto q) -> u32x4 {
+    if constexpr (ONCE) return __builtin_nontemporal_load(q);
+    else return *q;
+  };
   if constexpr (F32) {
     const float* q = static_cast<const float*>(p) + at;
-    x.v[0] = *reinterpret_cast<const u32x4_a4*>(q);
-    x.v[1] = *reinterpret_cast<const u32x4_a4*>(q + 4);
+    x.v[0] = load(reinterpret_cast<const u32x4_a4*>(q));
+    x.v[1] = load(reinterpret_cast<const u32x4_a4*>(q + 4));
   } else {
-    x.v[0] = *reinterpret_cast<const u32x4_a2*>(static_cast<const unsigned short*>(p) + at);
+    x.v[0] = load(reinterpret_cast<const u32x4_a2*>(static_cast<const unsigned short*>(p) + at));
   }
   return x;
 }
@@ -66,73 +70,62 @@ __device__ __forceinline__ float load1(const void* p, int64_t at) {
   else return __uint_as_float(static_cast<unsigned int>(static_cast<const unsigned short*>(p)[at]) << 16);
 }
 
-constexpr int kBlocks = 4;   // of eight elements a thread: that many loads in flight
-
-template <bool F32, bool ADD>
+// Eight elements a thread. Two, four or eight such blocks a thread were slower: 16384 x 3584 bf16 with a residual 62.4 us
+// with one (5.65 TB/s), 63.4, 66.0 and 69.1 us; without one 38.3 us (6.1 TB/s), 39.1, 43.7, 43.4 us; fp32 118 us (6.0
+// TB/s) and 83 us (5.7 TB/s), 122 to 139 us and 85 to 96 us. ONCE: x and the residual are more than the caches keep and
+// are read past them: 62.4 -> 54.1 us (6.5 TB/s); x alone 37.8 -> 39.8 us, so only with a residual.
+template <bool F32, bool ADD, bool ONCE>
 __global__ __launch_bounds__(256) void drop(const DropParams p) {
+  const int64_t b = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, i = b * 8, n = p.rows * p.cols;
+  if (i >= n) return;
+  int64_t row = 0, col = i;
+  if (p.rows > 1) {
+    row = i / p.cols;
+    col = i - row * p.cols;
+  }
+  const bool whole = col + 8 <= p.cols;
+  Eight<F32> x, r;
+  if (whole) {
+    x = load8<F32, ONCE>(p.x, row * p.ld_x + col);
+    if constexpr (ADD) r = load8<F32, ONCE>(p.residual, row * p.ld_r + col);
+  }
   uint64_t seed = p.seed, offset = p.offset;
   if (p.counter) {
     seed = p.counter[0];
     offset = p.counter[1];
   }
-  const int64_t n = p.rows * p.cols;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kBlocks) + threadIdx.x;
-  Eight<F32> x[kBlocks], r[kBlocks];
-  int64_t row[kBlocks], col[kBlocks];
-  bool whole[kBlocks];
+  const u32x4 bits = philox(static_cast<uint64_t>(b), offset, seed);
+  if (whole) {
+    float y[8];
 #pragma unroll
-  for (int u = 0; u < kBlocks; ++u) {
-    const int64_t i = (first + u * 256) * 8;
-    row[u] = 0;
-    col[u] = i;
-    if (p.rows > 1 && i < n) {
-      row[u] = i / p.cols;
-      col[u] = i - row[u] * p.cols;
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t number = e & 1 ? bits[e >> 1] >> 16 : bits[e >> 1] & 0xFFFFu;
+      y[e] = number >= p.threshold ? get<F32>(x, e) * p.factor : 0.0f;
+      if constexpr (ADD) y[e] += get<F32>(r, e);
     }
-    whole[u] = i < n && col[u] + 8 <= p.cols;
-    if (whole[u]) {
-      x[u] = load8<F32>(p.x, row[u] * p.ld_x + col[u]);
-      if constexpr (ADD) r[u] = load8<F32>(p.residual, row[u] * p.ld_r + col[u]);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < kBlocks; ++u) {
-    const int64_t b = first + u * 256;
-    if (b * 8 >= n) continue;
-    const u32x4 bits = philox(static_cast<uint64_t>(b), offset, seed);
-    if (whole[u]) {
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t number = e & 1 ? bits[e >> 1] >> 16 : bits[e >> 1] & 0xFFFFu;
-        y[e] = number >= p.threshold ? get<F32>(x[u], e) * p.factor : 0.0f;
-        if constexpr (ADD) y[e] += get<F32>(r[u], e);
-      }
-      const int64_t at = row[u] * p.ld_o + col[u];
-      if constexpr (F32) {
-        float* q = static_cast<float*>(p.out) + at;
-        *reinterpret_cast<u32x4_a4*>(q) = u32x4{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])};
-        *reinterpret_cast<u32x4_a4*>(q + 4) = u32x4{__float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7])};
-      } else {
-        u32x4 w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = to_bf16(y[2 * e]) | (static_cast<unsigned int>(to_bf16(y[2 * e + 1])) << 16);
-        *reinterpret_cast<u32x4_a2*>(static_cast<unsigned short*>(p.out) + at) = w;
-      }
+    const int64_t at = row * p.ld_o + col;
+    if constexpr (F32) {
+      float* q = static_cast<float*>(p.out) + at;
+      *reinterpret_cast<u32x4_a4*>(q) = u32x4{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])};
+      *reinterpret_cast<u32x4_a4*>(q + 4) = u32x4{__float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7])};
     } else {
-      // over a row's end, or the last elements
-      int64_t rr = row[u], cc = col[u];
-      for (int e = 0; e < 8 && b * 8 + e < n; ++e) {
-        const uint32_t number = (bits[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-        float y = number >= p.threshold ? load1<F32>(p.x, rr * p.ld_x + cc) * p.factor : 0.0f;
-        if constexpr (ADD) y += load1<F32>(p.residual, rr * p.ld_r + cc);
-        if constexpr (F32) static_cast<float*>(p.out)[rr * p.ld_o + cc] = y;
-        else static_cast<unsigned short*>(p.out)[rr * p.ld_o + cc] = to_bf16(y);
-        if (++cc == p.cols) {
-          cc = 0;
-          ++rr;
-        }
-      }
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = to_bf16(y[2 * e]) | (static_cast<unsigned int>(to_bf16(y[2 * e + 1])) << 16);
+      *reinterpret_cast<u32x4_a2*>(static_cast<unsigned short*>(p.out) + at) = w;
+    }
+    return;
+  }
+  // over a row's end, or the last elements
+  for (int e = 0; e < 8 && i + e < n; ++e) {
+    const uint32_t number = (bits[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+    float y = number >= p.threshold ? load1<F32>(p.x, row * p.ld_x + col) * p.factor : 0.0f;
+    if constexpr (ADD) y += load1<F32>(p.residual, row * p.ld_r + col);
+    if constexpr (F32) static_cast<float*>(p.out)[row * p.ld_o + col] = y;
+    else static_cast<unsigned short*>(p.out)[row * p.ld_o + col] = to_bf16(y);
+    if (++col == p.cols) {
+      col = 0;
+      ++row;
     }
   }
 }
@@ -141,13 +134,16 @@ __global__ __launch_bounds__(256) void drop(const DropParams p) {
 
 hipError_t launch_dropout(bool f32, const DropParams& p, hipStream_t st) {
   const int64_t blocks = (p.rows * p.cols + 7) / 8;
-  const dim3 grid(static_cast<unsigned>((blocks + 256 * kBlocks - 1) / (256 * kBlocks)));
+  const dim3 grid(static_cast<unsigned>((blocks + 255) / 256));
+  const bool once = p.residual && p.rows * p.cols * (f32 ? 8 : 4) > (int64_t{128} << 20);  // half the 256 MB cache
   if (f32) {
-    if (p.residual) drop<true, true><<<grid, 256, 0, st>>>(p);
-    else drop<true, false><<<grid, 256, 0, st>>>(p);
+    if (once) drop<true, true, true><<<grid, 256, 0, st>>>(p);
+    else if (p.residual) drop<true, true, false><<<grid, 256, 0, st>>>(p);
+    else drop<true, false, false><<<grid, 256, 0, st>>>(p);
   } else {
-    if (p.residual) drop<false, true><<<grid, 256, 0, st>>>(p);
-    else drop<false, false><<<grid, 256, 0, st>>>(p);
+    if (once) drop<false, true, true><<<grid, 256, 0, st>>>(p);
+    else if (p.residual) drop<false, true, false><<<grid, 256, 0, st>>>(p);
+    else drop<false, false, false><<<grid, 256, 0, st>>>(p);
   }
   return hipGetLastError();
 }

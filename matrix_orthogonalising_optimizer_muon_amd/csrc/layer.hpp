@@ -79,7 +79,6 @@ hipError_t launch_mix_step(bool f32, const MixStep& p, hipStream_t st);
 
 // ---- tokens by expert (experts.hip) ----
 constexpr int kMaxExperts = 1024;
-constexpr int kPlanBlock = 1024;         // choices a workgroup sorts
 struct PlanParams {
   const void* ids; int32_t ids64;
   int64_t n;                             // choices: tokens x top

@@ -16,7 +16,7 @@ namespace muon {
 namespace {
 
 constexpr size_t kAlign = 256;
-constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;  // of 256 threads: 2^32 threads is past what a launch takes
+constexpr int64_t kMaxTokens = (int64_t{1} << 24) - 1;  // a workgroup of 256 threads each: 2^32 threads is past what a launch takes
 constexpr int64_t kMaxLd = int64_t{1} << 36;
 
 inline int64_t cdiv(int64_t x, int64_t a) { return (x + a - 1) / a; }
@@ -44,7 +44,7 @@ int validate_sizes(const muon_mix* m) {
   if (!m || !dtype_ok(m->dtype)) return MUON_ERR_ARG;
   if (m->batch < 0 || m->batch > (int64_t{1} << 20) || m->tokens < 0 || m->tokens > (int64_t{1} << 24)) return MUON_ERR_ARG;
   if (m->heads < 1 || m->heads > 65536 || m->kv_heads < 1 || m->heads % m->kv_heads != 0) return MUON_ERR_ARG;
-  if (m->batch * m->heads > (int64_t{1} << 20)) return MUON_ERR_ARG;
+  if (m->batch * m->heads > (int64_t{1} << 18)) return MUON_ERR_ARG;
   if (m->dim < 1 || m->dim > MUON_MIX_MAX_DIM || m->dim_v < 1 || m->dim_v > MUON_MIX_MAX_DIM) return MUON_ERR_ARG;
   return MUON_OK;
 }
@@ -123,7 +123,8 @@ MixPlan plan_of(const muon_mix* m, const muon_mix_grads* g, int cus) {
       const int64_t each = cdiv(chunks, want), segments = cdiv(chunks, each);
       if (segments == last) continue;
       last = segments;
-      if (segments > 1 && p.bh * segments * state > (int64_t{1} << 30)) break;
+      // segments are for walks that leave CUs idle
+      if (segments > 1 && (p.bh * segments * state > (int64_t{1} << 30) || p.bh * per > 2 * cus)) break;
       // a last round that leaves CUs idle costs less than a whole one
       auto rounds = [&](int64_t groups, double slots) {
         const double r = groups / slots, whole = std::floor(r);
@@ -201,16 +202,20 @@ hipError_t walk(bool f32, const MixPlan& pl, bool out, const MixParams& p, hipSt
 // ---- tokens by expert ----
 
 int validate_sizes(const muon_experts* e) {
-  if (!e || e->tokens < 0 || e->tokens > kMaxGroups || e->top < 1 || e->top > MUON_MAX_CHOICES) return MUON_ERR_ARG;
+  if (!e || e->tokens < 0 || e->tokens > kMaxTokens || e->top < 1 || e->top > MUON_MAX_CHOICES) return MUON_ERR_ARG;
   if (e->tokens * e->top > (int64_t{1} << 25) || e->experts < 1 || e->experts > MUON_MAX_EXPERTS) return MUON_ERR_ARG;
   if (e->reserved != 0) return MUON_ERR_ARG;
   return MUON_OK;
 }
 
-// One workgroup sorts what it can at once; more choices are dealt to at most 128 workgroups, each of
-// which adds up the counts of all (65536 choices of 64 experts: see plan_place).
+// Workgroups of a plan. One (a launch less) while it is quick; then 512 choices each, at most 128, and at most 32768
+// counters, which every workgroup adds up. Times in us, choices x experts: 1025 x 64: one 6.2, more 7.1; 2048 x 64:
+// one 8.4, more 7.3; 2048 x 1024: one 9.2, more 11.7; 16384 x 64: 512 a workgroup 7.6, 1024 10.9, 2048 13.2; 65536 x
+// 1024: 128 workgroups 30, 64 21, 32 19.
 int plan_blocks(const muon_experts* e) {
-  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(cdiv(e->tokens * e->top, kPlanBlock), 1), 128));
+  const int64_t n = e->tokens * e->top;
+  if (n <= 1536 + 2 * e->experts) return 1;
+  return static_cast<int>(std::min<int64_t>({cdiv(n, 512), 128, 32768 / (e->experts + 1)}));
 }
 size_t plan_bytes(const muon_experts* e) {
   const int blocks = plan_blocks(e);
@@ -280,7 +285,6 @@ int muon_mix_forward(muon_ctx* ctx, const muon_mix* m, void* o, float* final_sta
     if (!aligned(o, size_of(m->dtype)) || !aligned(final_state, 4) || (m->batch * m->tokens > 0 && !o)) return MUON_ERR_ARG;
     if (m->batch == 0 || (m->tokens == 0 && !final_state)) return MUON_OK;
     const MixPlan pl = plan_of(m, nullptr, ctx_cus(ctx));
-    if (pl.bh * pl.per * pl.segments > kMaxGroups) return MUON_ERR_ARG;
     rc = check_workspace(workspace, workspace_bytes, pl.bytes);
     if (rc != MUON_OK) return rc;
     if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
@@ -330,7 +334,6 @@ int muon_mix_backward(muon_ctx* ctx, const muon_mix* m, const muon_mix_grads* g,
     if (rc != MUON_OK) return rc;
     if (m->batch == 0 || (!g->dq && !g->dk && !g->dv && !g->d_state) || (m->tokens == 0 && !g->d_state)) return MUON_OK;
     const MixPlan pl = plan_of(m, g, ctx_cus(ctx));
-    if (pl.bh * pl.per * pl.segments > kMaxGroups) return MUON_ERR_ARG;
     rc = check_workspace(workspace, workspace_bytes, pl.bytes);
     if (rc != MUON_OK) return rc;
     if (ctx_device(ctx) < 0) return MUON_ERR_DEVICE;
@@ -439,9 +442,9 @@ int muon_mix_step(muon_ctx* ctx, const muon_mix* m, void* o, float* new_state, v
     p.scale = m->scale;
     p.batch = static_cast<int32_t>(m->batch); p.heads = m->heads; p.group = m->heads / m->kv_heads;
     p.dim = m->dim; p.dim_v = m->dim_v;
-    // threads across: whole rows of up to 128 columns, fewer (down to 32 columns) while the GPU has idle CUs
-    p.lanes = 32;
-    while (p.lanes > 8 && (p.lanes * 2 >= m->dim_v || m->batch * m->heads * cdiv(m->dim_v, 4 * p.lanes) < ctx_cus(ctx))) p.lanes /= 2;
+    // 64 columns a workgroup, 32 where they are all or leave CUs idle. States of 128 x 128, 32, 64 and 128 columns: 16
+    // of them 4.5, 4.9, 5.9 us; 448: 12.6, 12.3, 12.5 us; 3584: 93.7, 90.7, 94.0 us (5.2 TB/s with 64)
+    p.lanes = m->dim_v <= 32 || m->batch * m->heads * cdiv(m->dim_v, 64) < ctx_cus(ctx) ? 8 : 16;
     MUON_HIP(launch_mix_step(m->dtype == MUON_F32, p, static_cast<hipStream_t>(stream)));
     return MUON_OK;
   } catch (...) {
@@ -558,8 +561,8 @@ int muon_expert_combine_backward(muon_ctx* ctx, const muon_experts* e, const voi
 int muon_dropout(muon_ctx* ctx, const muon_drop* d, void* stream) {
   try {
     if (!ctx || !d || !dtype_ok(d->dtype)) return MUON_ERR_ARG;
-    if (d->rows < 0 || d->rows >= (int64_t{1} << 31) || d->cols < 1 || d->cols > kMaxLd) return MUON_ERR_ARG;
-    if (d->rows > kMaxLd / d->cols || !(d->p >= 0.0f && d->p <= 1.0f)) return MUON_ERR_ARG;
+    if (d->rows < 0 || d->rows >= (int64_t{1} << 31) || d->cols < 1 || d->cols > (int64_t{1} << 34)) return MUON_ERR_ARG;
+    if (d->rows > (int64_t{1} << 34) / d->cols || !(d->p >= 0.0f && d->p <= 1.0f)) return MUON_ERR_ARG;
     const int64_t es = size_of(d->dtype);
     auto ld_ok = [&](int64_t ld) { return ld >= d->cols && span_ok(d->rows, ld); };
     if (!ld_ok(d->ld_x) || !ld_ok(d->ld_out) || (d->residual && !ld_ok(d->ld_residual))) return MUON_ERR_ARG;

@@ -55,8 +55,8 @@ def mix_grads(**kw):
     return B.muon_mix_grads(**d)
 
 
-BAD_SIZES = [dict(batch=-1), dict(batch=(1 << 20) + 1), dict(tokens=-1), dict(tokens=(1 << 24) + 1), dict(heads=0), dict(kv_heads=0),
-             dict(kv_heads=3), dict(kv_heads=-2), dict(heads=65538), dict(batch=1 << 19, heads=4), dict(dim=0), dict(dim=257),
+BAD_SIZES = [dict(batch=-1), dict(batch=(1 << 18) + 1, heads=1, kv_heads=1), dict(tokens=-1), dict(tokens=(1 << 24) + 1), dict(heads=0), dict(kv_heads=0),
+             dict(kv_heads=3), dict(kv_heads=-2), dict(heads=65538), dict(batch=1 << 17, heads=4), dict(dim=0), dict(dim=257),
              dict(dim_v=0), dict(dim_v=257), dict(dtype=2), dict(dtype=-1)]
 BAD_REST = [dict(scale=float("nan")), dict(scale=float("inf")), dict(q_strides=(-1, 64, 16)), dict(k_strides=(0, (1 << 40) + 1, 0)),
             dict(v_strides=(0, 0, -8)), dict(q=None), dict(k=None), dict(v=None), dict(log_decay=None), dict(q=FAKE + 1),
@@ -117,9 +117,9 @@ def test_mix_workspace_size_refuses_what_the_calls_refuse(hctx):
     assert B._lib.muon_mix_workspace_size(hctx, mix(), None, None) == B.MUON_ERR_ARG
     assert B._lib.muon_mix_workspace_size(None, mix(), None, n) == B.MUON_ERR_ARG
     # the largest sizes' arithmetic stays within 64 bits
-    most = mix(batch=1 << 20, tokens=1 << 24, heads=1, kv_heads=1, dim=256, dim_v=256)
+    most = mix(batch=1 << 18, tokens=1 << 24, heads=1, kv_heads=1, dim=256, dim_v=256)
     assert B._lib.muon_mix_workspace_size(hctx, most, mix_grads(), n) == B.MUON_OK
-    assert B._lib.muon_mix_workspace_size(hctx, mix(batch=16, tokens=1 << 24, heads=65536, kv_heads=1, dim=256, dim_v=256),
+    assert B._lib.muon_mix_workspace_size(hctx, mix(batch=4, tokens=1 << 24, heads=65536, kv_heads=1, dim=256, dim_v=256),
                                           mix_grads(), n) == B.MUON_OK
 
 
@@ -159,6 +159,7 @@ def test_expert_plan_validation(hctx):
     for bad in BAD_CHOICES:
         assert B._lib.muon_expert_plan_workspace_size(hctx, choices(**bad), n) == B.MUON_ERR_ARG, bad
     assert B.muon_expert_plan_workspace_size(hctx, choices()) == 0
+    assert B.muon_expert_plan_workspace_size(hctx, choices(tokens=1 << 19)) > 0
     many = choices(tokens=1 << 20, top=32)
     need = B.muon_expert_plan_workspace_size(hctx, many)
     assert need > 0 and need % 256 == 0 and call(many, n=need) == B.MUON_ERR_DEVICE
@@ -203,8 +204,8 @@ def test_dropout_validation(hctx):
                dict(out=FAKE * 2), dict(ld_x=100, out=FAKE + 80, ld_out=100), dict(rows=1, ld_x=50, out=FAKE)]:
         assert call(drop(**ok)) == B.MUON_ERR_DEVICE, ok
     assert call(drop(rows=0, x=None, out=None)) == B.MUON_OK
-    for bad in [dict(rows=-1), dict(rows=1 << 31), dict(cols=0), dict(cols=(1 << 36) + 1, ld_x=1 << 37, ld_out=1 << 37),
-                dict(rows=1 << 30, cols=65, ld_x=65, ld_out=65, ld_residual=65), dict(p=-0.1), dict(p=1.5), dict(p=float("nan")),
+    for bad in [dict(rows=-1), dict(rows=1 << 31), dict(cols=0), dict(cols=(1 << 34) + 1, ld_x=1 << 35, ld_out=1 << 35),
+                dict(rows=1 << 28, cols=65, ld_x=65, ld_out=65, ld_residual=65), dict(p=-0.1), dict(p=1.5), dict(p=float("nan")),
                 dict(ld_x=39), dict(ld_out=39), dict(ld_residual=39), dict(ld_x=(1 << 36) + 1), dict(x=None), dict(out=None),
                 dict(x=FAKE + 1), dict(out=FAKE + 1), dict(residual=FAKE + 1), dict(counter=FAKE + 4), dict(dtype=2),
                 dict(rows=1 << 26, cols=1, ld_x=1 << 35, ld_out=1 << 35, residual=None), dict(out=FAKE + 2), dict(out=FAKE * 2 + 80), dict(out=FAKE, ld_out=80), dict(ld_x=100, out=FAKE + 78, ld_out=100)]:
