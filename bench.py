@@ -62,6 +62,10 @@ def parse():
                          "feed-forward block's forward and backward over this many tokens, the weight "
                          "gradients written into the layer's gate / up / down G arrays, then the Muon step "
                          "of those three matrices (workloads with gate, up and down matrices)")
+    ap.add_argument("--layer-tokens", type=int, default=0,
+                    help="also time the rest of a layer's training pass over this many tokens (one sequence): linear attention "
+                         "with heads of 128 and the width of the primary workload's q matrix, dropout onto the residual "
+                         "stream, and the rows of 8 of 64 experts there and back; forward and gradients each")
     ap.add_argument("--tune-cache", default=None,
                     help="tile-choice file: loaded before the warmup when it exists, written after "
                          "it (so that separate profiling runs use the same kernels)")
@@ -224,6 +228,53 @@ def ffn_bench(B, ctx, torch, args, w):
            "forward_tflops": round(flops / ms["forward"] / 1e9, 1),
            "backward_tflops": round(2 * flops / ms["backward"] / 1e9, 1)}
     print(f"[bench] feed-forward block: {out}", file=sys.stderr, flush=True)
+    return out
+
+
+def layer_bench(torch, args, w):
+    """What a layer's training pass runs beside its feed-forward block: ms of linear attention, dropout and
+    the tokens' way to the experts and back, forward and gradients."""
+    from matrix_orthogonalising_optimizer_muon_amd import dropout, experts, mixers
+    spec = {m.name.split(".")[-1].lower(): m for m in w.matrices[:7]}
+    if not {"q", "k"} <= set(spec) or spec["q"].rows % 128 or spec["k"].rows % 128:
+        raise SystemExit(f"--layer-tokens: {w.name} has no q and k matrices of heads of 128")
+    T, D, H, K = args.layer_tokens, spec["q"].cols, spec["q"].rows // 128, spec["k"].rows // 128
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(12)
+    new = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v, do = new(1, T, H, 128), new(1, T, K, 128), new(1, T, K, 128), new(1, T, H, 128)
+    x, dy, ys = new(T, D), new(T, D), new(8 * T, D)
+    decay = torch.log1p(-torch.exp2(-5.0 - 7.0 * torch.arange(H, device="cuda") / max(H - 1, 1)))
+    ids = torch.rand(T, 64, generator=gen, device="cuda").topk(8, dim=1).indices
+    weights = torch.rand(T, 8, generator=gen, device="cuda")
+    held = {}
+
+    def plan():
+        held["plan"] = experts.expert_plan(ids, 64)
+    stages = {
+        "attention": lambda: mixers.linear_attention_forward(q, k, v, decay),
+        "attention_grad": lambda: mixers.linear_attention_backward(do, q, k, v, decay),
+        "dropout": lambda: dropout.dropout_forward(x, 0.1, 1, residual=dy),
+        "dropout_grad": lambda: dropout.dropout_backward(dy, 0.1, 1),
+        "plan": plan,
+        "dispatch": lambda: experts.dispatch_forward(x, held["plan"]),
+        "combine": lambda: experts.combine_forward(ys, weights, held["plan"]),
+        "combine_grad": lambda: experts.combine_backward(dy, ys, weights, held["plan"]),
+        "dispatch_grad": lambda: experts.dispatch_backward(ys, held["plan"]),
+    }
+    total = dict.fromkeys(stages, 0.0)
+    for t in range(args.warmup + args.steps):
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(len(stages) + 1)]
+        ev[0].record()
+        for n, call in enumerate(stages.values()):
+            call()
+            ev[n + 1].record()
+        torch.cuda.synchronize()
+        if t >= args.warmup:
+            for n, name in enumerate(stages):
+                total[name] += ev[n].elapsed_time(ev[n + 1])
+    out = {"tokens": T, "width": D, "heads": [H, K], **{f"{n}_ms": round(v / args.steps, 4) for n, v in total.items()}}
+    print(f"[bench] layer: {out}", file=sys.stderr, flush=True)
     return out
 
 
@@ -509,6 +560,8 @@ def main():
         out["adamw_companion"] = adamw_bench(B, ctx, torch, args)
     if args.ffn_tokens:
         out["feed_forward"] = ffn_bench(B, ctx, torch, args, w)
+    if args.layer_tokens:
+        out["layer"] = layer_bench(torch, args, w)
     B.muon_destroy(ctx)
     B.muon_destroy(pctx)
     print(json.dumps(out), flush=True)

@@ -87,9 +87,9 @@ struct MixTime {
   float chunk, ends, sum_chunk, sum_ends;
 };
 constexpr MixTime kMixTime[2][3][3] = {
-    {{{1.14f, 6.2f, 0.73f, 6.0f}, {1.5f, 6.2f, 0.8f, 6.2f}, {}},
-     {{1.85f, 5.5f, 0.9f, 6.3f}, {2.5f, 6.0f, 1.2f, 8.0f}, {3.9f, 7.0f, 2.3f, 7.5f}},
-     {{4.2f, 8.0f, 2.1f, 6.0f}, {4.7f, 10.0f, 2.8f, 9.0f}, {}}},
+    {{{1.4f, 5.5f, 0.75f, 6.0f}, {1.7f, 6.5f, 0.8f, 6.2f}, {}},
+     {{2.0f, 5.8f, 0.9f, 6.0f}, {2.6f, 8.0f, 1.15f, 8.0f}, {3.9f, 8.0f, 2.0f, 8.0f}},
+     {{3.9f, 8.0f, 1.9f, 7.0f}, {4.5f, 11.0f, 2.75f, 9.0f}, {}}},
     {{{3.2f, 5.0f, 0.9f, 5.5f}, {5.0f, 7.0f, 1.55f, 4.5f}, {}},
      {{5.7f, 5.0f, 1.7f, 4.4f}, {8.6f, 6.5f, 3.2f, 5.0f}, {}},
      {{11.9f, 3.0f, 3.7f, 5.0f}, {16.0f, 8.0f, 5.9f, 8.0f}, {}}}};
@@ -97,8 +97,9 @@ constexpr MixTime kMixTime[2][3][3] = {
 // A walk over all tokens with wide slices reads and computes least. More workgroups come from narrower slices
 // (scores and weighted operands are computed once a slice) or from segments (k and v are read twice, two more
 // launches, the states' traffic): the cheapest of both by the measured times. 128 (batch, head)s of 128 x
-// 128, 2048 tokens, forward: slices of 64 82 us, of 128 103 us, two segments 118 us; gradients (three walks): 222, 165
-// and 228 us. 16 of them, 65536 tokens: 16 or 32 segments with slices of 128 380 us, of 64 485 us, 8 segments 650 us.
+// 128, 2048 tokens, forward: slices of 64 97 to 107 us, of 128 107 to 110 us, two segments 122 us; gradients (three
+// walks): 290, 190 and 245 us. 16 of them, 65536 tokens: 16 or 32 segments with slices of 128 394 to 404 us, of 64 520
+// us, 8 segments 614 us.
 MixPlan plan_of(const muon_mix* m, const muon_mix_grads* g, int cus) {
   MixPlan p;
   p.bh = m->batch * m->heads;

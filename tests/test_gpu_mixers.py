@@ -103,6 +103,43 @@ def test_segments(X, size, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("size", [(64, 130, 4, 2, 128, 128), (64, 193, 4, 4, 126, 127), (64, 70, 4, 1, 64, 64), (64, 65, 4, 4, 63, 61),
+                                  (32, 129, 4, 2, 256, 256), (32, 100, 2, 1, 250, 255), (64, 66, 4, 4, 128, 64), (64, 66, 4, 4, 64, 128)])
+def test_many_heads(X, size, state, dtype):
+    """Enough (batch, head)s for the wide slices; rows aligned and not; three sequences against the oracle."""
+    q, k, v, do, g, s, df = inputs(*size, dtype, state=state)
+    scale = 0.25
+    lengths = [size[1] - (b % 3 == 2) * (b % size[1]) for b in range(size[0])]
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    kw = dict(scale=scale, state=s, lengths=lens)
+    o, last = X.linear_attention_forward(q, k, v, g, **kw, final=True)
+    plain = X.linear_attention_forward(q, k, v, g, **kw)
+    plain = plain[0] if isinstance(plain, tuple) else plain
+    grads = X.linear_attention_backward(do, q, k, v, g, **kw, d_final=df, need_dstate=True)
+    three = X.linear_attention_backward(do, q, k, v, g, **kw, d_final=df)
+    h = HALF_STEP[dtype]
+    for b in (0, size[0] // 2 + 3, size[0] - 1):
+        n = lengths[b]
+        one = [t[b:b + 1].clone() for t in (q, k, v, do)]
+        for t in one:
+            t[:, n:] = 0
+        a = np_of(*one[:3], g)
+        pick = lambda t: None if t is None else t[b:b + 1]  # noqa: E731
+        ns, ndo, ndf = np_of(pick(s), one[3], pick(df))
+        want, limit = om.forward(*a, scale, ns, [n]), om.bounds(*a, scale, h, ns, [n])
+        for x, r, bound, name in zip((pick(o), pick(last)), want, limit, ("o", "states")):
+            inside(x, r, bound, (name, b))
+        inside(pick(plain), want[0], limit[0], ("o alone", b))
+        want = om.backward(ndo, *a, scale, ns, [n], ndf)
+        limit = om.bounds(*a, scale, h, ns, [n], ndo, ndf)
+        for x, y, r, bound, name in zip(grads, three, want, limit, ("dq", "dk", "dv", "dstate")):
+            inside(pick(x), r, bound, (name, b))
+            if y is not None:
+                inside(pick(y), r, bound, (name, "alone", b))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T", [100, 1200])
 def test_padded_batch(X, T, dtype):
     """Lengths from 0 (and below) to past the end; NaN and infinities behind a sequence are not read."""
