@@ -51,16 +51,13 @@ __device__ __forceinline__ float get(const Eight<F32>& x, int e) {
 template <bool F32, bool ONCE>
 __device__ __forceinline__ Eight<F32> load8(const void* p, int64_t at) {
   Eight<F32> x;
-  auto load = [](auto q) -> u32x4 {
-    if constexpr (ONCE) return __builtin_nontemporal_load(q);
-    else return *q;
-  };
   if constexpr (F32) {
-    const float* q = static_cast<const float*>(p) + at;
-    x.v[0] = load(reinterpret_cast<const u32x4_a4*>(q));
-    x.v[1] = load(reinterpret_cast<const u32x4_a4*>(q + 4));
+    const u32x4_a4* q = reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(p) + at);
+    x.v[0] = ONCE ? __builtin_nontemporal_load(q) : *q;
+    x.v[1] = ONCE ? __builtin_nontemporal_load(q + 1) : q[1];
   } else {
-    x.v[0] = load(reinterpret_cast<const u32x4_a2*>(static_cast<const unsigned short*>(p) + at));
+    const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(static_cast<const unsigned short*>(p) + at);
+    x.v[0] = ONCE ? __builtin_nontemporal_load(q) : *q;
   }
   return x;
 }
