@@ -81,8 +81,8 @@ __device__ __forceinline__ void mma(f32x4& acc, const u32x4& a, const u32x4& b) 
 
 // LDS arrays are rows of CHUNKS 16-byte pieces, a power of two, with the pieces of row r in the order
 // given by XOR with mixed(r), so that reads find different banks. (Padded rows would do, but the direct
-// loads write whole kilobytes.) BY_ROWS (b and the state's copy, read mostly as rows): 16-byte reads of 16 rows, which
-// the hardware serves by lanes 0-3, 12-15, 20-27 and so on, each at one of two neighbouring pieces. Else (c, read as
+// loads write whole kilobytes.) BY_ROWS (b where there are outputs, and the state's copy, read mostly as rows): 16-byte reads of 16 rows, which
+// the hardware serves by lanes 0-3, 12-15, 20-27 and so on, each at one of two neighbouring pieces. Else (c, b of the states' walk, read as
 // columns): 16-bit transpose reads of 32 bytes of 8 neighbouring rows. fp32: 4-byte reads of 64 bytes of the
 // rows r, r + 4, r + 8, r + 12. One order for both kinds left a third of the LDS cycles to conflicts.
 template <bool F32, int CHUNKS, bool BY_ROWS>
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
 #pragma unroll
       for (int j = 0; j < LB; ++j) {
         const int r = tid / CHB + j * (THREADS / CHB);
-        if (C * CHB % THREADS == 0 || r < C) write16(lds + set + piece<F32, CHB, true>(r, tid % CHB), piece_b.take(nb[j], r0 + r < live));
+        if (C * CHB % THREADS == 0 || r < C) write16(lds + set + piece<F32, CHB, OUT>(r, tid % CHB), piece_b.take(nb[j], r0 + r < live));
       }
 #pragma unroll
       for (int j = 0; j < LC; ++j) {
@@ -379,7 +379,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
 #pragma unroll
       for (int j = 0; j < IB; ++j) {
         const int x = (own * IB + j) * 64 + lane, r = x / CHB;
-        b_at[j] = from(x, CHB, r, (x % CHB) ^ mixed<F32, CHB, true>(r), sb, dim);
+        b_at[j] = from(x, CHB, r, (x % CHB) ^ mixed<F32, CHB, OUT>(r), sb, dim);
       }
 #pragma unroll
       for (int j = 0; j < IC; ++j) {
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
           }
       }
     };
-    const int b_lane = columns_lane<F32, CHB, true>(lane) ^ dbase * ES, c_lane = columns_lane<F32, CHC, false>(lane) ^ we * NT * 16 * ES;
+    const int b_lane = columns_lane<F32, CHB, OUT>(lane) ^ dbase * ES, c_lane = columns_lane<F32, CHC, false>(lane) ^ we * NT * 16 * ES;
     // the weights of a chunk's tokens, in the order of `columns`
     float weight[JS][VEC];
     auto weigh = [&](int rows) {
@@ -735,17 +735,54 @@ __global__ __launch_bounds__(256) void mix_scan(const MixScan p) {
   }
 }
 
-// Gradients of shared heads: the group's fp32 partial sums in head order, rounded once.
+// Gradients of shared heads: the group's fp32 partial sums in head order, rounded once. A thread takes four
+// columns and asks for four heads at once. 8 x 2048 tokens, 16 heads of 128 over 4: 56 us for dk and dv (one column a
+// thread, 64-bit divisions 88 us).
 __global__ __launch_bounds__(256) void mix_share(const MixShare p) {
   const auto o = p.one[blockIdx.y];
-  const int64_t n = p.rows * p.kv_heads * o.dim;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t row = i / o.dim, d = i % o.dim;
+  int shift = 0;                                               // 2^shift threads across a row
+  while ((4 << shift) < o.dim) ++shift;
+  const int d = (threadIdx.x & ((1 << shift) - 1)) * 4, live = o.dim - d;
+  if (live <= 0) return;
+  const int64_t n = p.rows * p.kv_heads, each = 256 >> shift;
+  for (int64_t row = blockIdx.x * each + (threadIdx.x >> shift); row < n; row += gridDim.x * each) {
     const float* q = o.part + row * p.group * o.dim + d;
-    float s = q[0];
-    for (int k = 1; k < p.group; ++k) s += q[static_cast<int64_t>(k) * o.dim];
-    if (p.bf16) static_cast<unsigned short*>(o.out)[i] = to_bf16(s);
-    else static_cast<float*>(o.out)[i] = s;
+    auto load = [&](int k) -> f32x4 {
+      const float* x = q + static_cast<int64_t>(k) * o.dim;
+      if (live >= 4) return __builtin_bit_cast(f32x4, static_cast<u32x4>(*reinterpret_cast<const u32x4_a4*>(x)));
+      return f32x4{x[0], live > 1 ? x[1] : 0.0f, live > 2 ? x[2] : 0.0f, 0.0f};
+    };
+    f32x4 s = load(0);
+    for (int k = 1; k < p.group; k += 4) {
+      f32x4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = load(min(k + j, p.group - 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (k + j < p.group) s += x[j];
+      }
+    }
+    if (p.bf16) {
+      unsigned short* out = static_cast<unsigned short*>(o.out) + row * o.dim + d;
+      if (live >= 4) {
+        *reinterpret_cast<u32x2_a2*>(out) = u32x2{pack(s[0], s[1]), pack(s[2], s[3])};
+      } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          if (j < live) out[j] = to_bf16(s[j]);
+        }
+      }
+    } else {
+      float* out = static_cast<float*>(o.out) + row * o.dim + d;
+      if (live >= 4) {
+        *reinterpret_cast<u32x4_a4*>(out) = __builtin_bit_cast(u32x4, s);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          if (j < live) out[j] = s[j];
+        }
+      }
+    }
   }
 }
 
@@ -848,9 +885,11 @@ hipError_t launch_mix_scan(const MixScan& p, hipStream_t st) {
 }
 
 hipError_t launch_mix_share(const MixShare& p, hipStream_t st) {
-  int64_t most = 0;
+  int most = 0;
   for (int i = 0; i < p.count; ++i) most = p.one[i].dim > most ? p.one[i].dim : most;
-  const int64_t want = (p.rows * p.kv_heads * most + 255) / 256;
+  int64_t across = 1;
+  while (4 * across < most) across *= 2;
+  const int64_t want = (p.rows * p.kv_heads * across + 255) / 256;
   mix_share<<<dim3(static_cast<unsigned>(want < 65536 ? want : 65536), p.count), 256, 0, st>>>(p);
   return hipGetLastError();
 }
