@@ -103,6 +103,13 @@ def test_segments(X, size, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [(1, 70, 12, 1, 30, 65), (2, 33, 9, 1, 3, 130), (1, 20, 10, 2, 256, 2), (3, 5, 6, 1, 7, 5)])
+def test_many_query_heads_share_one(X, size, dtype):
+    """Gradients of k and v summed over groups of 5 to 12 heads."""
+    check(X, inputs(*size, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("state", [False, True])
 @pytest.mark.parametrize("size", [(64, 130, 4, 2, 128, 128), (64, 193, 4, 4, 126, 127), (64, 70, 4, 1, 64, 64), (64, 65, 4, 4, 63, 61),
                                   (32, 129, 4, 2, 256, 256), (32, 100, 2, 1, 250, 255), (64, 66, 4, 4, 128, 64), (64, 66, 4, 4, 64, 128)])
