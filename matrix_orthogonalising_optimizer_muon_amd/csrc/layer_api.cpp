@@ -443,9 +443,14 @@ int muon_mix_step(muon_ctx* ctx, const muon_mix* m, void* o, float* new_state, v
     p.scale = m->scale;
     p.batch = static_cast<int32_t>(m->batch); p.heads = m->heads; p.group = m->heads / m->kv_heads;
     p.dim = m->dim; p.dim_v = m->dim_v;
-    // 64 columns a workgroup, 32 where they are all or leave CUs idle. States of 128 x 128, 32, 64 and 128 columns: 16
-    // of them 4.5, 4.9, 5.9 us; 448: 12.6, 12.3, 12.5 us; 3584: 93.7, 90.7, 94.0 us (5.2 TB/s with 64)
-    p.lanes = m->dim_v <= 32 || m->batch * m->heads * cdiv(m->dim_v, 64) < ctx_cus(ctx) ? 8 : 16;
+    // All columns a workgroup where states fill the CUs: rows that are not whole cache lines would share them with another
+    // workgroup's. 4096 states, 64 columns or all, us: 16 x 256: 55.5 or 29.1; 64 x 256: 110 or 104; 128 x 128: 107 or 105;
+    // 40 x 72: 33 or 21; 33 x 129: 56 or 33. Fewer states: 64, or 32 where that leaves CUs idle (16 of 128 x 128, 32, 64 and
+    // 128 columns: 4.5, 4.9, 5.9 us).
+    const int64_t states = m->batch * m->heads;
+    const int all = static_cast<int>(cdiv(m->dim_v, 4));
+    p.lanes = states >= ctx_cus(ctx) ? all : states * cdiv(m->dim_v, 64) < ctx_cus(ctx) ? 8 : 16;
+    p.lanes = std::min(p.lanes, all);
     MUON_HIP(launch_mix_step(m->dtype == MUON_F32, p, static_cast<hipStream_t>(stream)));
     return MUON_OK;
   } catch (...) {

@@ -787,8 +787,10 @@ __global__ __launch_bounds__(256) void mix_share(const MixShare p) {
 }
 
 // One token: S' = e^g S + k^T v, o = scale q S'. Bound by the state's traffic, read and written
-// once: 128 requests of 28 heads of 128 x 128 90.7 us, 5.2 TB/s; 16 heads 4.5 us. A workgroup takes `lanes` threads of four
-// columns across and 256 / lanes rows at a time; their sums are joined in LDS in row order.
+// once: 128 requests of 28 heads of 128 x 128 90 us, 5.2 TB/s; 16 heads 5.0 us; 64 requests of 32 heads of 250 x 250 219 us,
+// 4.7 TB/s (64 columns a workgroup: 437 us). A workgroup takes `lanes` threads of four
+// columns across and as many rows as there are threads at a time, four of them in flight; their sums are joined in LDS in
+// row order. A thread behind the last whole four columns reads the last four of the row and keeps its own.
 template <bool F32>
 __device__ __forceinline__ float load_one(const void* p, int64_t i) {
   if constexpr (F32) return static_cast<const float*>(p)[i];
@@ -806,41 +808,55 @@ __global__ __launch_bounds__(256) void mix_step(const MixStep p) {
   const int across = tid % p.lanes, down = tid / p.lanes, rows = 256 / p.lanes;
   const int e = (blockIdx.y * p.lanes + across) * 4;
   const float decay = __builtin_amdgcn_exp2f(p.log_decay[h] * kLog2e);
-  const int left = p.dim_v - e;
+  const int left = down < rows ? p.dim_v - e : 0;
+  const int skip = left >= 4 ? 0 : 4 - left;                    // of the four columns from e - skip on: a neighbour's
+  const bool four = left > 0 && p.dim_v >= 4;
   f32x4 v{0, 0, 0, 0}, acc{0, 0, 0, 0};
 #pragma unroll
   for (int r = 0; r < 4; ++r)
-    if (r < left) v[r] = load_one<F32>(p.v, b * p.v_sb + (h / p.group) * p.v_sh + e + r);
+    if (left > 0 && (four || r >= skip)) v[r] = load_one<F32>(p.v, b * p.v_sb + (h / p.group) * p.v_sh + e - skip + r);
   __syncthreads();
-  const int64_t at = static_cast<int64_t>(bh) * p.dim * p.dim_v + e;
-  if (left >= 4) {
-#pragma unroll 4
-    for (int d = down; d < p.dim; d += rows) {
-      const int64_t x = at + static_cast<int64_t>(d) * p.dim_v;
-      f32x4 s = __builtin_bit_cast(f32x4, static_cast<u32x4>(*reinterpret_cast<const u32x4_a4*>(p.z_in + x)));
-      s = s * decay + v * qk[1][d];
-      *reinterpret_cast<u32x4_a4*>(p.z_out + x) = __builtin_bit_cast(u32x4, s);
-      acc += s * qk[0][d];
-    }
-  } else {
-    for (int d = down; d < p.dim; d += rows)
+  const int64_t at = static_cast<int64_t>(bh) * p.dim * p.dim_v + e - skip;
+  if (left > 0) {
+    constexpr int U = 4;
+    for (int d0 = down; d0 < p.dim; d0 += U * rows) {
+      f32x4 s[U];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (r < left) {
-          const int64_t x = at + static_cast<int64_t>(d) * p.dim_v + r;
-          const float s = p.z_in[x] * decay + v[r] * qk[1][d];
-          p.z_out[x] = s;
-          acc[r] += s * qk[0][d];
+      for (int u = 0; u < U; ++u) {
+        const int d = min(d0 + u * rows, p.dim - 1);
+        const float* z = p.z_in + at + static_cast<int64_t>(d) * p.dim_v;
+        if (four) {
+          s[u] = __builtin_bit_cast(f32x4, static_cast<u32x4>(*reinterpret_cast<const u32x4_a4*>(z)));
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[u][r] = r >= skip ? z[r] : 0.0f;
         }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int d = d0 + u * rows;
+        if (d >= p.dim) break;
+        s[u] = s[u] * decay + v * qk[1][d];
+        acc += s[u] * qk[0][d];
+        float* z = p.z_out + at + static_cast<int64_t>(d) * p.dim_v;
+        if (skip == 0) {
+          *reinterpret_cast<u32x4_a4*>(z) = __builtin_bit_cast(u32x4, s[u]);
+        } else {
+#pragma unroll
+          for (int r = 1; r < 4; ++r)
+            if (r >= skip) z[r] = s[u][r];
+        }
+      }
+    }
   }
   sums[tid] = acc;
   __syncthreads();
-  if (down == 0) {
+  if (down == 0 && left > 0) {
     for (int k = 1; k < rows; ++k) acc += sums[k * p.lanes + across];
-    const int64_t x = static_cast<int64_t>(bh) * p.dim_v + e;
+    const int64_t x = static_cast<int64_t>(bh) * p.dim_v + e - skip;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (r < left) {
+      if (r >= skip) {
         if constexpr (F32) static_cast<float*>(p.out)[x + r] = acc[r];
         else static_cast<unsigned short*>(p.out)[x + r] = to_bf16(acc[r]);
       }

@@ -207,6 +207,22 @@ def test_step(X, size, dtype):
     assert same is s and s._version > before and torch.equal(s, other) and torch.equal(again, got)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [(64, 4, 4, 33, 129), (64, 4, 2, 5, 3), (64, 4, 4, 16, 256), (64, 4, 1, 200, 1), (43, 6, 3, 57, 191),
+                                  (90, 3, 3, 9, 250), (64, 4, 4, 256, 18)])
+def test_step_of_many_states(X, size, dtype):
+    """Enough states for a workgroup to take all columns; then the same with states at another alignment."""
+    test_step(X, size, dtype)
+    B, H, kv, D, E = size
+    q, k, v, _, g, s, _ = inputs(B, 1, H, kv, D, E, dtype, state=True)
+    held = torch.full((s.numel() + 3,), 7.0, device="cuda")
+    moved = held[1:-2].view(s.shape)
+    moved.copy_(s)
+    a, b = X.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], g, s), X.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], g, moved)
+    assert torch.equal(a[0], b[0]) and torch.equal(s, moved)
+    assert held[0] == 7.0 and bool((held[-2:] == 7.0).all())
+
+
 def test_steps_follow_a_prompt(X):
     """A prompt's states carried on token by token give what the whole sequence gives."""
     q, k, v, _, g, _, _ = inputs(2, 140, 4, 2, 64, 64, "f32")
