@@ -26,8 +26,9 @@
 // Steps (forward / gradients of that case, us; the sizes' first kernel took 225 / 425): state and outputs on waves of
 // their own, one barrier a chunk 135 / 254; stores after the next chunk's loads 120 / 219; direct loads two
 // chunks ahead, XOR-ordered rows, no spills 82 / 165 with one weighted part; then 13 and 20 us for
-// accuracy: two weighted parts, scores and (up to 64 columns) the state's copy in two parts, which take o's error
-// against 64 bits from 1.4 (1.65 in gradients) to 1.0 times that of fp32 throughout (1.37 with 128 columns).
+// accuracy: two weighted parts, scores and the state's copy in two parts, which take the error against 64 bits from 1.4
+// (1.65 in gradients) to 1.0 times that of fp32 throughout. The copy's second part at 128 x 128 and 256 x 64 came later
+// and costs the gradients of that case a fifth.
 #include "layer.hpp"
 #include "mfma_util.hpp"
 
@@ -247,19 +248,25 @@ __device__ __forceinline__ void meet() {
 template <bool F32, int DP, int NV, bool OUT, bool DIRECT>
 struct Layout {
   static constexpr int ES = F32 ? 4 : 2;
-  // 16-bit: the state's copy in two parts where they fit
-  static constexpr int COPY = NV * DP * ES, ZPARTS = !F32 && COPY <= 16384 ? 2 : 1;
+  // 16-bit: the state's copy in two parts
+  static constexpr int COPY = NV * DP * ES, ZPARTS = F32 ? 1 : 2;
   static constexpr int B = C * DP * ES, CB = C * NV * ES, Z = OUT ? COPY * ZPARTS : 0;
   static constexpr int MOST = 160 * 1024;
   // copies of the operands: the next chunk's arrive (direct loads: the next two) while one is read
-  static constexpr int STAGES = DIRECT && OUT && 3 * (B + CB) + 2 * Z <= MOST ? 3 : 2 * (B + CB) + 2 * Z <= MOST ? 2 : 1;
-  static constexpr int COPIES = STAGES > 1 ? 2 : 1;              // of the state's copy
+  static constexpr int stages(int copies) {
+    return DIRECT && OUT && 3 * (B + CB) + copies * Z <= MOST ? 3 : 2 * (B + CB) + copies * Z <= MOST ? 2 : 1;
+  }
+  // of the state's copy: two, or one (bf16: 128 x 128 and 256 x 64) that is written again when the outputs' waves have read it
+  static constexpr int COPIES = stages(2) > 1 ? 2 : 1, STAGES = stages(COPIES);
+  static constexpr bool TURNS = OUT && COPIES == 1 && STAGES > 1;   // with one stage the operands' meeting does
   static constexpr int BYTES = STAGES * (B + CB) + COPIES * Z;
+  static_assert(BYTES <= MOST, "LDS of a workgroup");
 };
 
 // Four waves keep the state (each dim / 4 of its rows, or half of rows and columns), with OUT four
 // more make the outputs (16 of a chunk's tokens each): a SIMD then has one of either, whose matrix
-// instructions, conversions and LDS reads fill each other's gaps. They meet once a chunk.
+// instructions, conversions and LDS reads fill each other's gaps. They meet once a chunk, and once more where the state's
+// copy has one place: the outputs' waves read it first, the state's waves meet them halfway through their own products.
 // DIRECT: operands whose rows are 16-byte aligned and not more than 2^31 bytes apart in a chunk go global -> LDS
 // by the direct loads, issued by the state's waves up to two chunks ahead, zeros past the last row and
 // column by the buffer's bounds; else all waves bring the next chunk's through registers.
@@ -437,7 +444,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
             else {
               const u32x2 w{pack(z[mt][nt][0], z[mt][nt][1]), pack(z[mt][nt][2], z[mt][nt][3])};
               write8(to, w);
-              if constexpr (L::ZPARTS == 2) write8(to + L::COPY, u32x2{rest(w[0], z[mt][nt][0], z[mt][nt][1]), rest(w[1], z[mt][nt][2], z[mt][nt][3])});
+              write8(to + L::COPY, u32x2{rest(w[0], z[mt][nt][0], z[mt][nt][1]), rest(w[1], z[mt][nt][2], z[mt][nt][3])});
             }
           }
       }
@@ -487,6 +494,9 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
         for (int m0 = 0; m0 < MT; m0 += PAIR)
 #pragma unroll
           for (int s = 0; s < JS; ++s) {
+            if constexpr (L::TURNS) {
+              if (more && m0 / PAIR * JS + s == MT / PAIR * JS / 2) meet();
+            }
             u32x4 kf[PARTS][PAIR];
 #pragma unroll
             for (int mt = 0; mt < PAIR; ++mt) {
@@ -607,6 +617,23 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
         request(r0 + C);
         if constexpr (AHEAD && !DIRECT) request_a(r0 + C);
       }
+      f32x4 x[TILES];
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) x[t] = f32x4{0, 0, 0, 0};
+      if (carried || r0 > begin) {
+        const int z = copy_of(copy) + n_lane;
+        constexpr int GZ = TILES * DS < GN ? TILES * DS : GN;
+        stream<TILES * DS, GZ>([&](int i) { return rows<CHB>(lds, z, i / DS, i % DS); },
+                               [&](int i0, const u32x4 (&k)[GZ]) { products<F32, DS>(x, i0, k, a); });
+        if constexpr (!F32)
+          stream<TILES * DS, GZ>([&](int i) { return rows<CHB>(lds, z + L::COPY, i / DS, i % DS); },
+                                 [&](int i0, const u32x4 (&k)[GZ]) { products<F32, DS>(x, i0, k, a); });
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) x[t] *= reach;
+      }
+      if constexpr (L::TURNS) {
+        if (more) meet();
+      }
       // scores, transposed: rows s, columns this wave's tokens
       // 16-bit: rounded as the operand of the product with v, in two parts
       constexpr int PARTS = F32 ? 1 : 2;
@@ -634,20 +661,6 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
             }
           }
         }
-      }
-      f32x4 x[TILES];
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) x[t] = f32x4{0, 0, 0, 0};
-      if (carried || r0 > begin) {
-        const int z = copy_of(copy) + n_lane;
-        constexpr int GZ = TILES * DS < GN ? TILES * DS : GN;
-        stream<TILES * DS, GZ>([&](int i) { return rows<CHB>(lds, z, i / DS, i % DS); },
-                               [&](int i0, const u32x4 (&k)[GZ]) { products<F32, DS>(x, i0, k, a); });
-        if constexpr (L::ZPARTS == 2)
-          stream<TILES * DS, GZ>([&](int i) { return rows<CHB>(lds, z + L::COPY, i / DS, i % DS); },
-                                 [&](int i0, const u32x4 (&k)[GZ]) { products<F32, DS>(x, i0, k, a); });
-#pragma unroll
-        for (int t = 0; t < TILES; ++t) x[t] *= reach;
       }
       constexpr int G = TILES * JS < GN ? TILES * JS : GN;
       stream<TILES * JS, G>([&](int i) { return columns<F32, CHC>(lds, set_c, i / JS, i % JS); },
