@@ -104,7 +104,9 @@ def dropout(x, p: float, seed, offset: int = 0, *, residual=None):
 
 class Dropout(torch.nn.Module):
     """``dropout`` with a seed and a count of calls, held on the GPU (``counter``): also the replays of a
-    captured graph go on counting. In evaluation x passes through (plus the residual)."""
+    captured graph go on counting. In evaluation x passes through (plus the residual). A call inside a
+    backward is refused: a forward that activation checkpointing runs again there would have the next count's
+    mask; ``dropout`` with the call's own offset runs again as it was."""
 
     def __init__(self, p: float, seed: int = 0, *, device=None):
         super().__init__()
@@ -117,6 +119,9 @@ class Dropout(torch.nn.Module):
     def forward(self, x, residual=None):
         if not self.training or self.p == 0.0:
             return x if residual is None else x + residual
+        if torch._C._current_graph_task_id() != -1:      # a backward is running on this thread
+            raise RuntimeError("Dropout counts its calls, so its forward cannot be run again in a backward (activation "
+                               "checkpointing): call dropout(x, p, seed, offset) there")
         now = self.counter.clone()
         self.counter[1:].add_(1)
         return dropout(x, self.p, now, residual=residual)
