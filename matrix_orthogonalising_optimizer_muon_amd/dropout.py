@@ -6,8 +6,8 @@ offset and an element's number, so nothing of it is stored and the gradient draw
 ``seed`` is an integer and ``offset`` another (a call's number, so that each call has a mask of its
 own), or ``seed`` is a tensor of the two on the GPU (int64), read when the work runs: a captured
 graph's replays then differ as the tensor does. ``dropout_forward`` / ``dropout_backward`` are the
-calls, ``dropout`` the same for torch's automatic differentiation, ``Dropout`` a module that counts
-its calls. x may have any leading dimensions and row stride. Work is enqueued on the current
+calls, ``dropout`` the same for torch's automatic differentiation, ``Dropout`` a module that takes
+its numbers from torch's generator or counts its calls. x may have any leading dimensions and row stride. Work is enqueued on the current
 stream of the operands' device.
 """
 
@@ -103,25 +103,36 @@ def dropout(x, p: float, seed, offset: int = 0, *, residual=None):
 
 
 class Dropout(torch.nn.Module):
-    """``dropout`` with a seed and a count of calls, held on the GPU (``counter``): also the replays of a
-    captured graph go on counting. In evaluation x passes through (plus the residual). A call inside a
-    backward is refused: a forward that activation checkpointing runs again there would have the next count's
-    mask; ``dropout`` with the call's own offset runs again as it was."""
+    """``dropout`` with numbers of its own for each call; in evaluation x passes through (plus the residual).
 
-    def __init__(self, p: float, seed: int = 0, *, device=None):
+    Without a seed every call draws both numbers from torch's generator of x's device: modules, their copies and
+    differently seeded ranks have masks of their own, ``torch.manual_seed`` repeats them, replays of a captured
+    graph differ, and activation checkpointing, which sets the generator back, draws a call's mask again.
+
+    With a seed the numbers are it and a count of the module's calls, held on the GPU (``counter``): also the replays
+    of a captured graph go on counting. Modules of one seed (copies too, and ranks, whose buffers
+    DistributedDataParallel makes alike) draw the same masks. A call inside a backward is refused: a forward that
+    activation checkpointing runs again there would have the next count's mask; ``dropout`` with the call's
+    own offset runs again as it was."""
+
+    def __init__(self, p: float, seed: int | None = None, *, device=None):
         super().__init__()
         if not 0.0 <= p <= 1.0:
             raise ValueError(f"p must be between 0 and 1, got {p}")
         self.p = p
-        seed = _number(seed, "seed")
-        self.register_buffer("counter", torch.tensor([seed - (1 << 64) if seed >> 63 else seed, 0], dtype=torch.int64, device=device))
+        if seed is not None:
+            seed = _number(seed, "seed")
+            seed = torch.tensor([seed - (1 << 64) if seed >> 63 else seed, 0], dtype=torch.int64, device=device)
+        self.register_buffer("counter", seed)
 
     def forward(self, x, residual=None):
         if not self.training or self.p == 0.0:
             return x if residual is None else x + residual
+        if self.counter is None:
+            return dropout(x, self.p, torch.empty(2, dtype=torch.int64, device=x.device).random_(), residual=residual)
         if torch._C._current_graph_task_id() != -1:      # a backward is running on this thread
-            raise RuntimeError("Dropout counts its calls, so its forward cannot be run again in a backward (activation "
-                               "checkpointing): call dropout(x, p, seed, offset) there")
+            raise RuntimeError("Dropout with a seed counts its calls, so its forward cannot be run again in a backward "
+                               "(activation checkpointing): give it no seed, or call dropout(x, p, seed, offset) there")
         now = self.counter.clone()
         self.counter[1:].add_(1)
         return dropout(x, self.p, now, residual=residual)

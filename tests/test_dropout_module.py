@@ -41,3 +41,40 @@ def test_counted_calls_are_not_run_again(reentrant):
     # the call with numbers of its own runs again as it was
     a, b = run(lambda t: R.dropout(t, 0.5, 3, 7), x, reentrant)
     assert torch.equal(a, b)
+
+
+def test_modules_draw_masks_of_their_own():
+    """Built alike, copied, called again: another mask each, and the same ones after torch.manual_seed."""
+    import copy
+    x = torch.ones(50, 20)
+
+    def masks():
+        torch.manual_seed(5)
+        first, second = R.Dropout(0.5), R.Dropout(0.5)
+        return [m(x) != 0 for m in (first, second, copy.deepcopy(first), first)]
+    one, two = masks(), masks()
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+    for i in range(4):
+        for j in range(i):
+            # 1000 coins of 1/2: six deviations
+            assert abs(float((one[i] == one[j]).float().mean()) - 0.5) <= 6 * 0.5 / np.sqrt(1000), (i, j)
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_a_checkpointed_call_draws_its_mask_again(reentrant):
+    m, x = R.Dropout(0.5), torch.ones(40, 10)
+    torch.manual_seed(6)
+    a, b = run(m, x, None)
+    torch.manual_seed(6)
+    c, d = run(m, x, reentrant)
+    assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(a, d)
+
+
+def test_seed_and_state():
+    assert R.Dropout(0.1).counter is None and list(R.Dropout(0.1).state_dict()) == []
+    m = R.Dropout(0.1, seed=-2)
+    m(torch.ones(3))
+    other = R.Dropout(0.1, seed=9)
+    other.load_state_dict(m.state_dict())
+    assert other.counter.tolist() == [-2, 1]
+    assert torch.equal(R.Dropout(0.0)(x := torch.ones(3)), x) and torch.equal(R.Dropout(0.5).eval()(x, x), 2 * x)
