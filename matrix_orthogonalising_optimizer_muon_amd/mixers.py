@@ -181,7 +181,8 @@ def linear_attention(q, k, v, log_decay, *, scale: float | None = None, state=No
 class DecayAttention(torch.nn.Module):
     """A layer's mixer: the ``query``, ``key``, ``value`` and ``out`` matrices, which ``MuonWithAdamW``
     routes to the Muon update, around ``linear_attention``. Head h of n forgets with
-    exp(log_decay[h]) = 1 - 2^-(5 + 7 h / (n - 1)) unless ``log_decay`` is given."""
+    exp(log_decay[h]) = 1 - 2^-(5 + 7 h / (n - 1)) unless ``log_decay`` is given. ``log_decay`` stays
+    float32 when the module is cast."""
 
     def __init__(self, dim: int, heads: int, head_dim: int, *, kv_heads: int | None = None, head_dim_v: int | None = None,
                  log_decay=None, device=None, dtype=torch.bfloat16):
@@ -200,6 +201,13 @@ class DecayAttention(torch.nn.Module):
         if log_decay is None:
             log_decay = torch.log1p(-torch.exp2(-5.0 - 7.0 * torch.arange(heads, dtype=torch.float32) / max(heads - 1, 1)))
         self.register_buffer("log_decay", torch.as_tensor(log_decay, dtype=torch.float32).detach().to(device).clone())
+
+    def _apply(self, fn, recurse=True):
+        kept = self.log_decay
+        super()._apply(fn, recurse)
+        # moved as the module is, but not cast: 8 bits would leave 1 - 2^-12 at 1
+        self.log_decay = self.log_decay.float() if kept.is_meta else kept.to(self.log_decay.device)
+        return self
 
     def _project(self, x):
         heads = lambda w, d: torch.nn.functional.linear(x, w).unflatten(-1, (-1, d))  # noqa: E731
