@@ -236,6 +236,18 @@ __device__ __forceinline__ void products(f32x4 (&acc)[T], int i0, const u32x4 (&
       if ((i0 + i) % INNER == s) mma<F32>(acc[(i0 + i) / INNER], f[i], b[s]);
 }
 
+// e^{g n}, n > 0, the same for a wave, as a sum of two: a state is multiplied with the same power chunk after chunk, so that one fp32 number's
+// rounding would add up over them (by 24 chunks to as much as all other roundings of the state).
+struct Power {
+  float whole, rest;
+};
+__device__ __forceinline__ Power power(float g, int n) {
+  const double p = exp(static_cast<double>(g) * n);
+  const float whole = static_cast<float>(p), rest = whole <= 3.4e38f ? static_cast<float>(p - whole) : 0.0f;
+  auto uniform = [](float f) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(f))); };
+  return {uniform(whole), uniform(rest)};
+}
+
 // Waits for this workgroup's LDS traffic and its waves. The two kinds of waves below meet here from
 // loops of their own, with the same number of turns.
 __device__ __forceinline__ void meet() {
@@ -373,6 +385,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
 
   if (!OUT || wave >= 4) {
     // ---- the state: rows d = dbase + 16 mt + .., columns e = 16 (we NT + nt) + .. ----
+    const Power whole_chunk = power(p.log_decay[head], C), last_chunk = power(p.log_decay[head], max(live - begin, 0) % C);
     const int own = wave & 3, wd = own % WD, we = own / WD;
     const int dbase = wd * (DP / WD);
 
@@ -462,7 +475,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
         }
     };
     weigh(C);
-    float over = __builtin_amdgcn_exp2f(g2 * C);
+    Power over = whole_chunk;
 
     if (begin < live) {
       keep(stage_of(0), begin);
@@ -479,31 +492,30 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
       const int rows = min(live - r0, C);
       if (rows < C) {
         weigh(rows);
-        over = __builtin_amdgcn_exp2f(g2 * rows);
+        over = last_chunk;
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) z[mt][nt] *= over;
-      // Weighted b of this wave's rows, 32 rows and one fragment's tokens at a time. 16-bit: in parts, each the rest of
+      // Weighted b of this wave's rows, 32 rows at a time. 16-bit: in parts, each the rest of
       // the ones before rounded as the product's operand: three, whose sum has the weighted value's 24 bits, where
-      // the state is a result; else two (one adds a rounding to the outputs, for 12 us of 168 over 8 x 2048 tokens)
+      // the state is a result; else two (one adds a rounding to the outputs, for 12 us of 168 over 8 x 2048 tokens).
+      // A tile's sum over the chunk stands apart and is added once: products summed onto the state itself each round at
+      // its size (error of fp32 states against 64 bits over 24 chunks 6.9e-7 instead of 1.7e-7, with the power's rest)
       {
-        constexpr int PARTS = F32 ? 1 : EXACT ? 3 : 2, PAIR = 2;
+        // Rows of a state of 16 tiles a wave 16 at a time where the next chunk's operands wait in registers too: 32 would
+        // spill (32768 tokens, 16 heads of 251 x 250: 1190 instead of 1550 us)
+        constexpr int PARTS = F32 ? 1 : EXACT ? 3 : 2, PAIR = !OUT && !DIRECT && MT * NT >= 16 ? 1 : 2;
+        constexpr int N = NT * JS, G = N < 4 ? N : 4, GROUPS = MT / PAIR * (N / G);   // fragments of c, in groups of whole tiles
+        static_assert(G % JS == 0, "whole tiles");
 #pragma unroll
-        for (int m0 = 0; m0 < MT; m0 += PAIR)
+        for (int m0 = 0; m0 < MT; m0 += PAIR) {
+          u32x4 kf[JS][PARTS][PAIR];
 #pragma unroll
-          for (int s = 0; s < JS; ++s) {
-            if constexpr (L::TURNS) {
-              if (more && m0 / PAIR * JS + s == MT / PAIR * JS / 2) meet();
-            }
-            u32x4 kf[PARTS][PAIR];
+          for (int s = 0; s < JS; ++s)
 #pragma unroll
             for (int mt = 0; mt < PAIR; ++mt) {
               const u32x4 f = columns<F32, CHB>(lds, set_b, m0 + mt, s);
               if constexpr (F32) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) kf[0][mt][e] = __float_as_uint(__uint_as_float(f[e]) * weight[s][e]);
+                for (int e = 0; e < 4; ++e) kf[s][0][mt][e] = __float_as_uint(__uint_as_float(f[e]) * weight[s][e]);
               } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -512,24 +524,37 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
 #pragma unroll
                   for (int q = 0; q < PARTS; ++q) {
                     const unsigned int w = pack(lo, hi);
-                    kf[q][mt][e] = w;
+                    kf[s][q][mt][e] = w;
                     lo -= __uint_as_float(w << 16);
                     hi -= __uint_as_float(w & 0xFFFF0000u);
                   }
                 }
               }
             }
-            constexpr int G = NT < 4 ? NT : 4;
-            stream<NT, G>([&](int i) { return columns<F32, CHC>(lds, set_c, i, s); },
-                          [&](int i0, const u32x4 (&v)[G]) {
+          stream<N, G>([&](int i) { return columns<F32, CHC>(lds, set_c, i / JS, i % JS); },
+                       [&](int i0, const u32x4 (&v)[G]) {
+                         if constexpr (L::TURNS) {
+                           if (more && m0 / PAIR * (N / G) + i0 / G == GROUPS / 2) meet();
+                         }
+                         f32x4 u[PAIR][G / JS];
 #pragma unroll
-                            for (int q = 0; q < PARTS; ++q)
+                         for (int mt = 0; mt < PAIR; ++mt)
 #pragma unroll
-                              for (int i = 0; i < G; ++i)
+                           for (int i = 0; i < G / JS; ++i) u[mt][i] = z[m0 + mt][i0 / JS + i] * over.rest;
 #pragma unroll
-                                for (int mt = 0; mt < PAIR; ++mt) mma<F32>(z[m0 + mt][i0 + i], kf[q][mt], v[i]);
-                          });
-          }
+                         for (int s = 0; s < JS; ++s)
+#pragma unroll
+                           for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                             for (int i = 0; i < G / JS; ++i)
+#pragma unroll
+                               for (int mt = 0; mt < PAIR; ++mt) mma<F32>(u[mt][i], kf[s][q][mt], v[i * JS + s]);
+#pragma unroll
+                         for (int mt = 0; mt < PAIR; ++mt)
+#pragma unroll
+                           for (int i = 0; i < G / JS; ++i) z[m0 + mt][i0 / JS + i] = z[m0 + mt][i0 / JS + i] * over.whole + u[mt][i];
+                       });
+        }
       }
       stage = stage + 1 < L::STAGES ? stage + 1 : 0;
       copy = L::COPIES - 1 - copy;
@@ -628,8 +653,6 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
         if constexpr (!F32)
           stream<TILES * DS, GZ>([&](int i) { return rows<CHB>(lds, z + L::COPY, i / DS, i % DS); },
                                  [&](int i0, const u32x4 (&k)[GZ]) { products<F32, DS>(x, i0, k, a); });
-#pragma unroll
-        for (int t = 0; t < TILES; ++t) x[t] *= reach;
       }
       if constexpr (L::TURNS) {
         if (more) meet();
@@ -662,12 +685,17 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
           }
         }
       }
+      f32x4 y[TILES];                                            // apart, as the state's sums are
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) y[t] = f32x4{0, 0, 0, 0};
       constexpr int G = TILES * JS < GN ? TILES * JS : GN;
       stream<TILES * JS, G>([&](int i) { return columns<F32, CHC>(lds, set_c, i / JS, i % JS); },
                             [&](int i0, const u32x4 (&v)[G]) {
 #pragma unroll
-                              for (int q = 0; q < PARTS; ++q) products<F32, JS>(x, i0, v, score[q]);
+                              for (int q = 0; q < PARTS; ++q) products<F32, JS>(y, i0, v, score[q]);
                             });
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) x[t] = x[t] * reach + y[t];
       stage = stage + 1 < L::STAGES ? stage + 1 : 0;
       copy = L::COPIES - 1 - copy;
       if (more) {
@@ -728,8 +756,8 @@ __global__ __launch_bounds__(256) void mix_scan(const MixScan p) {
   for (int bh = blockIdx.y; bh < p.batch * p.heads; bh += gridDim.y) {
     int n = p.tokens;
     if (p.lengths) n = min(max(p.lengths[bh / p.heads], 0), n);
-    float g2 = p.log_decay[bh % p.heads] * kLog2e;
-    g2 = g2 < -1e30f ? -1e30f : g2;
+    const float g = p.log_decay[bh % p.heads];
+    const Power full = power(g, p.segment);
     float* z = o.z + static_cast<int64_t>(bh) * p.segments * o.n + i;
     float s = o.z0 ? o.z0[static_cast<int64_t>(bh) * o.n + i] : 0.0f;
     constexpr int U = 8;
@@ -742,7 +770,10 @@ __global__ __launch_bounds__(256) void mix_scan(const MixScan p) {
         if (k0 + k >= p.segments) break;
         const int len = min(max(n - (k0 + k) * p.segment, 0), p.segment);
         z[static_cast<int64_t>(k0 + k) * o.n] = s;
-        s = __builtin_amdgcn_exp2f(g2 * len) * s + u[k];
+        if (len > 0) {                                           // behind the last token u is 0
+          const Power over = len == p.segment ? full : power(g, len);
+          s = over.whole * s + (over.rest * s + u[k]);
+        }
       }
     }
   }

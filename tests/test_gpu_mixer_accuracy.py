@@ -79,3 +79,34 @@ def test_bf16_results_are_as_exact_as_one_rounding(X, size, with_states):
                 ratios[name, b, j] = rel(pick(got[name], name), want) / rel(once, want)
     print(size, with_states, {k: round(v, 4) for k, v in ratios.items()})
     assert max(ratios.values()) <= 1.01, ratios
+
+
+def steps32(size, name):
+    """A bound of the fp32 error's norm, relative to the result's, in steps of 2^-24: a sum of n random terms whose running
+    sum is rounded after each has sqrt(n / 2) roundings' worth, each 0.42 of a half step (uniform over the step, averaged over a
+    binade). How often a matrix instruction rounds is not documented; after each of its products at most: dim for a score
+    and for a row through the state, 64 for a chunk's tokens in a score row's sum, 64 in the state's. The state
+    takes one rounding for each chunk before it; eight more for powers, scales and joins. With products summed onto the state
+    itself, each of its chunks' roundings would be of its size (and a power in one fp32 number would be wrong by up to a step,
+    chunk after chunk the same way)."""
+    B, T, H, kv, D, E = size
+    dim = {"o": D, "dq": E, "dk": E, "dv": D}.get(name, 0)
+    chunks, sums = -(-T // 64), 2 if dim else 1
+    return 0.42 * np.sqrt(2 * dim / 2 + sums * 64 / 2 + chunks / 2 + (H // kv) / 2 + 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", SIZES + [(8, 1540, 16, 8, 128, 128), (8, 1541, 16, 16, 63, 62), (4, 1100, 16, 8, 256, 256)])
+def test_fp32_results_are_as_exact_as_sums_by_chunks(X, size, dtype):
+    """fp32 results, and the states of bf16 operands, within the bound."""
+    ins = inputs(*size, dtype)
+    got = results(X, ins, True)
+    B, kv = size[0], size[3]
+    ratios = {}
+    for b, j in {(0, 0), (B - 1, kv - 1)}:
+        a, do, s, df, pick = group_of(ins, b, j)
+        for name, want in exact(a, do, s, df, True).items():
+            if dtype == "f32" or name in ("states", "dstate"):
+                ratios[name, b, j] = rel(pick(got[name], name), want) / (steps32(size, name) * 2.0 ** -24)
+    print(size, dtype, {k: round(float(v), 2) for k, v in ratios.items()})
+    assert max(ratios.values()) <= 1.0, ratios
