@@ -517,8 +517,7 @@ int muon_distill_loss(muon_ctx *ctx, const muon_logits *l, const muon_distill *t
  * are not read, their o and gradients are zeros, the state passes them by.
  * Computed in chunks of 64 tokens (an infinity or NaN in a token may reach the tokens of its chunk
  * before it). MUON_BF16: products on the bf16 matrix instructions with fp32 sums; scores and the copy of the
- * state that q is multiplied with are operands of 16 bits. States that leave a call are fp32 sums of unrounded terms; where none leaves, the terms
- * have 16 bits on the way (so whether one is wanted can change last bits of the other results). MUON_F32: fp32
+ * state that q is multiplied with are operands of 16 bits, states fp32 sums of unrounded terms. MUON_F32: fp32
  * throughout.
  * batch and batch x heads up to 2^18, heads to 2^16, tokens to 2^24, dim and dim_v in [1, 256]. */
 #define MUON_MIX_MAX_DIM 256

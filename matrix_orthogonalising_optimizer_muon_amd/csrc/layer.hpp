@@ -42,7 +42,6 @@ struct MixParams {
   int32_t batch, heads, tokens;
   int32_t segments, segment;  // number, tokens of one (a multiple of the chunk)
   int32_t direct;             // every operand's rows are 16-byte aligned, apart, and a chunk's span 31 bits of bytes
-  int32_t exact;              // a state is a result: its terms are not rounded to the operands' type
   int32_t walked;             // segments walked: all, or without the last one
   int32_t z_in_per_segment;   // z_in has an array for each segment, else one for the first
   int32_t z_out_per_segment;  // z_out too (a segment's own sum), else one from the last token's segment

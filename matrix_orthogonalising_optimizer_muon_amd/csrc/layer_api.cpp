@@ -297,7 +297,6 @@ int muon_mix_forward(muon_ctx* ctx, const muon_mix* m, void* o, float* final_sta
     const MixArray q = array(m->q, m->q_strides, 1), k = array(m->k, m->k_strides, group), v = array(m->v, m->v_strides, group);
     float* z = static_cast<float*>(workspace);
     MixParams p = params(m, pl);
-    p.exact = final_state != nullptr;
     const int64_t es = size_of(m->dtype);
     p.direct = direct(q, m->dim, es) && direct(k, m->dim, es) && direct(v, m->dim_v, es);
     if (pl.segments > 1) {
@@ -349,7 +348,6 @@ int muon_mix_backward(muon_ctx* ctx, const muon_mix* m, const muon_mix_grads* g,
     float *z = reinterpret_cast<float*>(ws), *zr = reinterpret_cast<float*>(ws + pl.off_rev);
     const bool back = g->dk || g->dv || g->d_state;
     MixParams p = params(m, pl);
-    p.exact = g->d_state != nullptr;
     const int64_t es = size_of(m->dtype);
     p.direct = direct(q, m->dim, es) && direct(k, m->dim, es) && direct(v, m->dim_v, es) && direct(d_o, m->dim_v, es);
     if (pl.segments > 1) {

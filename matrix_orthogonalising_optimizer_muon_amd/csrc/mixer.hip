@@ -26,7 +26,7 @@
 // Steps (forward / gradients of that case, us; the sizes' first kernel took 225 / 425): state and outputs on waves of
 // their own, one barrier a chunk 135 / 254; stores after the next chunk's loads 120 / 219; direct loads two
 // chunks ahead, XOR-ordered rows, no spills 82 / 165 with one weighted part; then 13 and 20 us for
-// accuracy: two weighted parts, scores and the state's copy in two parts, which take the error against 64 bits from 1.4
+// accuracy: two weighted parts (now three), scores and the state's copy in two parts, which take the error against 64 bits from 1.4
 // (1.65 in gradients) to 1.0 times that of fp32 throughout. The copy's second part at 128 x 128 and 256 x 64 came later
 // and costs the gradients of that case a fifth.
 #include "layer.hpp"
@@ -282,8 +282,7 @@ struct Layout {
 // DIRECT: operands whose rows are 16-byte aligned and not more than 2^31 bytes apart in a chunk go global -> LDS
 // by the direct loads, issued by the state's waves up to two chunks ahead, zeros past the last row and
 // column by the buffer's bounds; else all waves bring the next chunk's through registers.
-// EXACT: the state is a result, so its terms are not rounded to the operands' type.
-template <bool F32, int DP, int NV, bool OUT, bool DIRECT, bool EXACT>
+template <bool F32, int DP, int NV, bool OUT, bool DIRECT>
 __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, DIRECT>::BYTES <= 81920 ? 2 : 1)) void mix_walk(const MixParams p) {
   constexpr int ES = Type<F32>::ES, VEC = Type<F32>::VEC, KF = Type<F32>::KF;
   constexpr int THREADS = OUT ? 512 : 256;
@@ -494,15 +493,15 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
         weigh(rows);
         over = last_chunk;
       }
-      // Weighted b of this wave's rows, 32 rows at a time. 16-bit: in parts, each the rest of
-      // the ones before rounded as the product's operand: three, whose sum has the weighted value's 24 bits, where
-      // the state is a result; else two (one adds a rounding to the outputs, for 12 us of 168 over 8 x 2048 tokens).
+      // Weighted b of this wave's rows, 32 rows at a time. 16-bit: in three parts, each the rest of
+      // the ones before rounded as the product's operand: their sum has the weighted value's 24 bits, so that the state is
+      // one of fp32 terms (two parts, where no state leaves: 230 instead of 242 us for the gradients of 8 x 2048 tokens)
       // A tile's sum over the chunk stands apart and is added once: products summed onto the state itself each round at
       // its size (error of fp32 states against 64 bits over 24 chunks 6.9e-7 instead of 1.7e-7, with the power's rest)
       {
         // Rows of a state of 16 tiles a wave 16 at a time where the next chunk's operands wait in registers too: 32 would
         // spill (32768 tokens, 16 heads of 251 x 250: 1190 instead of 1550 us)
-        constexpr int PARTS = F32 ? 1 : EXACT ? 3 : 2, PAIR = !OUT && !DIRECT && MT * NT >= 16 ? 1 : 2;
+        constexpr int PARTS = F32 ? 1 : 3, PAIR = !OUT && !DIRECT && MT * NT >= 16 ? 1 : 2;
         constexpr int N = NT * JS, G = N < 4 ? N : 4, GROUPS = MT / PAIR * (N / G);   // fragments of c, in groups of whole tiles
         static_assert(G % JS == 0, "whole tiles");
 #pragma unroll
@@ -907,17 +906,16 @@ __global__ __launch_bounds__(256) void mix_step(const MixStep p) {
   }
 }
 
-template <bool F32, int DP, int NV, bool DIRECT, bool EXACT>
+template <bool F32, int DP, int NV, bool DIRECT>
 hipError_t walk(bool out, const MixParams& p, int64_t groups, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(groups));
-  if (out) mix_walk<F32, DP, NV, true, DIRECT, EXACT><<<grid, 512, 0, st>>>(p);
-  else mix_walk<F32, DP, NV, false, DIRECT, EXACT><<<grid, 256, 0, st>>>(p);
+  if (out) mix_walk<F32, DP, NV, true, DIRECT><<<grid, 512, 0, st>>>(p);
+  else mix_walk<F32, DP, NV, false, DIRECT><<<grid, 256, 0, st>>>(p);
   return hipGetLastError();
 }
 template <bool F32, int DP, int NV>
 hipError_t walk(bool out, const MixParams& p, int64_t groups, hipStream_t st) {
-  if (p.direct) return F32 || p.exact ? walk<F32, DP, NV, true, true>(out, p, groups, st) : walk<F32, DP, NV, true, F32>(out, p, groups, st);
-  return F32 || p.exact ? walk<F32, DP, NV, false, true>(out, p, groups, st) : walk<F32, DP, NV, false, F32>(out, p, groups, st);
+  return p.direct ? walk<F32, DP, NV, true>(out, p, groups, st) : walk<F32, DP, NV, false>(out, p, groups, st);
 }
 template <bool F32>
 hipError_t walk(MixTile t, bool out, const MixParams& p, int64_t groups, hipStream_t st) {

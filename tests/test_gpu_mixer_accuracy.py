@@ -110,3 +110,14 @@ def test_fp32_results_are_as_exact_as_sums_by_chunks(X, size, dtype):
                 ratios[name, b, j] = rel(pick(got[name], name), want) / (steps32(size, name) * 2.0 ** -24)
     print(size, dtype, {k: round(float(v), 2) for k, v in ratios.items()})
     assert max(ratios.values()) <= 1.0, ratios
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [(2, 330, 4, 2, 128, 128), (1, 1500, 2, 1, 126, 127), (1, 700, 2, 2, 64, 40), (8, 330, 8, 8, 200, 256)])
+def test_a_state_that_leaves_changes_no_other_result(X, size, dtype):
+    q, k, v, do, g, s, df = inputs(*size, dtype)
+    for kw in ({}, dict(state=s)):
+        assert torch.equal(X.linear_attention_forward(q, k, v, g, **kw)[0], X.linear_attention_forward(q, k, v, g, **kw, final=True)[0])
+        a = X.linear_attention_backward(do, q, k, v, g, **kw, d_final=df)
+        b = X.linear_attention_backward(do, q, k, v, g, **kw, d_final=df, need_dstate=True)
+        assert all(torch.equal(x, y) for x, y in zip(a[:3], b[:3]))
