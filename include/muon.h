@@ -515,8 +515,8 @@ int muon_distill_loss(muon_ctx *ctx, const muon_logits *l, const muon_distill *t
  * 2^36. heads is a multiple of kv_heads; head h reads k, v head h / (heads / kv_heads).
  * lengths (batch, or null): entry b has the first lengths[b] tokens (clamped to [0, tokens]); the others
  * are not read, their o and gradients are zeros, the state passes them by.
- * Computed in chunks of 64 tokens (an infinity or NaN in a token may reach the tokens of its chunk
- * before it). MUON_BF16: products on the bf16 matrix instructions with fp32 sums; scores and the copy of the
+ * An infinity or NaN reaches what the formulas say, an infinity possibly as NaN. Computed in chunks of 64 tokens.
+ * MUON_BF16: products on the bf16 matrix instructions with fp32 sums; scores and the copy of the
  * state that q is multiplied with are operands of 16 bits, states fp32 sums of unrounded terms. MUON_F32: fp32
  * throughout.
  * batch and batch x heads up to 2^18, heads to 2^16, tokens to 2^24, dim and dim_v in [1, 256]. */

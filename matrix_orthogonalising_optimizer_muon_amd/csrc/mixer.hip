@@ -500,8 +500,8 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
       // its size (error of fp32 states against 64 bits over 24 chunks 6.9e-7 instead of 1.7e-7, with the power's rest)
       {
         // Rows of a state of 16 tiles a wave 16 at a time where the next chunk's operands wait in registers too: 32 would
-        // spill (32768 tokens, 16 heads of 251 x 250: 1190 instead of 1550 us)
-        constexpr int PARTS = F32 ? 1 : 3, PAIR = !OUT && !DIRECT && MT * NT >= 16 ? 1 : 2;
+        // spill (32768 tokens, 16 heads of 251 x 250: 1550 instead of 1190 us)
+        constexpr int PARTS = F32 ? 1 : 3, PAIR = !DIRECT && MT * NT >= 16 ? 1 : 2;
         constexpr int N = NT * JS, G = N < 4 ? N : 4, GROUPS = MT / PAIR * (N / G);   // fragments of c, in groups of whole tiles
         static_assert(G % JS == 0, "whole tiles");
 #pragma unroll
@@ -590,7 +590,8 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
     const char* rows_a = base(o.a);
     const int64_t sa = o.a.st * ES;
     constexpr bool AHEAD = DS <= 8;                             // registers for the next chunk's too
-    constexpr int GN = DS <= 8 ? 8 : 4;                         // fragments in a group
+    // Fragments in a group; four where eight would spill (4 x 2309 tokens, 16 heads of 227 x 224: 253 instead of 308 us)
+    constexpr int GN = DS <= (DIRECT ? 8 : 4) ? 8 : 4;
     u32x4 na[DS];
     uint32_t a_at = 0;
     if constexpr (DIRECT) a_at = static_cast<uint32_t>((rev ? C - 1 - i_tok : i_tok) * static_cast<int>(sa)) + g * 16;
@@ -626,6 +627,50 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
       request(begin);
       keep(stage_of(0), begin);
     }
+    constexpr int PARTS = F32 ? 1 : 2;                          // of the scores
+    auto causal = [&](f32x4 (&y)[TILES], const u32x4 (&score)[PARTS][JS], int set_c, int here) {
+      asm volatile("" : "+v"(set_c));                           // addresses of its own: those of the products would stay in registers
+      u32x4 ones[JS];                                           // a token's own and those before it, as `columns` orders them
+#pragma unroll
+      for (int s = 0; s < JS; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (F32) ones[s][e] = here < 16 * s + 4 * g + e ? 0u : 0x3F800000u;
+          else {
+            const int j = 32 * s + 16 * (e >> 1) + 4 * g + 2 * (e & 1);
+            ones[s][e] = (here < j ? 0u : 0x3F80u) | (here < j + 1 ? 0u : 0x3F800000u);
+          }
+        }
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        f32x4 sum{0, 0, 0, 0}, count{0, 0, 0, 0};
+        u32x4 v[JS];
+#pragma unroll
+        for (int s = 0; s < JS; ++s) {
+          v[s] = columns<F32, CHC>(lds, set_c, t, s);
+          u32x4 odd;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (F32) {
+              const bool finite = (v[s][e] & 0x7F800000u) != 0x7F800000u;
+              odd[e] = finite ? 0u : 0x3F800000u;
+              v[s][e] = finite ? v[s][e] : 0u;
+            } else {
+              const bool lo = (v[s][e] & 0x7F80u) != 0x7F80u, hi = (v[s][e] & 0x7F800000u) != 0x7F800000u;
+              odd[e] = (lo ? 0u : 0x3F80u) | (hi ? 0u : 0x3F800000u);
+              v[s][e] &= (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+            }
+          }
+          mma<F32>(count, odd, ones[s]);
+        }
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)                           // in the order of the sums without it
+#pragma unroll
+          for (int s = 0; s < JS; ++s) mma<F32>(sum, v[s], score[q][s]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[t][r] = count[r] > 0.0f ? __builtin_nanf("") : sum[r];
+      }
+    };
     const int n_lane = rows_lane<F32, CHB>(lane), c_lane = columns_lane<F32, CHC, false>(lane);
     int stage = 0, copy = 0;
     for (int r0 = begin; r0 < live; r0 += C) {
@@ -658,10 +703,11 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
       }
       // scores, transposed: rows s, columns this wave's tokens
       // 16-bit: rounded as the operand of the product with v, in two parts
-      constexpr int PARTS = F32 ? 1 : 2;
       u32x4 score[PARTS][JS];
+      int here = i_tok;
       {
         f32x4 sc4[4];
+        asm volatile("" : "+v"(here));                             // compared here: 16 masks kept over the loop would spill
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt) sc4[jt] = f32x4{0, 0, 0, 0};
         stream<4 * DS, GN>([&](int i) { return rows<CHB>(lds, set_n, i / DS, i % DS); },
@@ -669,7 +715,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
 #pragma unroll
         for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sc4[jt][r] *= within[jt][r];
+          for (int r = 0; r < 4; ++r) sc4[jt][r] = here < 16 * jt + 4 * g + r ? 0.0f : sc4[jt][r] * within[jt][r];
 #pragma unroll
         for (int s = 0; s < JS; ++s) {
           if constexpr (F32) {
@@ -693,6 +739,15 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
 #pragma unroll
                               for (int q = 0; q < PARTS; ++q) products<F32, JS>(y, i0, v, score[q]);
                             });
+      // A row of c that is not finite belongs to its token and those after it, but 0 times it is NaN in the sums of the
+      // tokens before. Where a sum is not finite, all are made again without such elements, which are counted up to each
+      // token by products of ones instead.
+      float odd = 0.0f;
+#pragma unroll
+      for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) odd = __builtin_fmaf(y[t][r], 0.0f, odd);
+      if (__any(!(odd == 0.0f))) causal(y, score, set_c, here);
 #pragma unroll
       for (int t = 0; t < TILES; ++t) x[t] = x[t] * reach + y[t];
       stage = stage + 1 < L::STAGES ? stage + 1 : 0;

@@ -13,8 +13,7 @@ h // (heads // kv_heads). The decay is a constant: it has no gradient.
 ``linear_attention`` the same for torch's automatic differentiation, ``linear_attention_step``
 one token of every sequence. ``state`` (batch x heads x dim x dim_v, float32, contiguous) carries a
 sequence on; ``lengths`` (int32, on the GPU) gives each sequence of a padded batch its tokens:
-what lies behind is not read, its outputs and gradients are zeros. An infinity or NaN in a token may
-reach the outputs of up to 63 tokens before it (chunks of 64). Work is enqueued on the
+what lies behind is not read, its outputs and gradients are zeros. Work is enqueued on the
 current stream of the operands' device; workspaces come from torch's allocator for the
 length of the call.
 """
