@@ -87,19 +87,19 @@ struct MixTime {
   float chunk, ends, sum_chunk, sum_ends;
 };
 constexpr MixTime kMixTime[2][3][3] = {
-    {{{1.4f, 5.5f, 0.75f, 6.0f}, {1.7f, 6.5f, 0.8f, 6.2f}, {}},
-     {{2.0f, 5.8f, 0.9f, 6.0f}, {2.6f, 8.0f, 1.15f, 8.0f}, {3.9f, 8.0f, 2.0f, 8.0f}},
-     {{3.9f, 8.0f, 1.9f, 7.0f}, {4.5f, 11.0f, 2.75f, 9.0f}, {}}},
-    {{{3.2f, 5.0f, 0.9f, 5.5f}, {5.0f, 7.0f, 1.55f, 4.5f}, {}},
-     {{5.7f, 5.0f, 1.7f, 4.4f}, {8.6f, 6.5f, 3.2f, 5.0f}, {}},
-     {{11.9f, 3.0f, 3.7f, 5.0f}, {16.0f, 8.0f, 5.9f, 8.0f}, {}}}};
+    {{{1.5f, 5.4f, 0.8f, 5.8f}, {2.0f, 5.5f, 1.0f, 7.0f}, {}},
+     {{2.0f, 5.6f, 1.0f, 6.5f}, {2.75f, 7.2f, 1.35f, 6.1f}, {4.3f, 9.4f, 2.0f, 8.9f}},
+     {{4.0f, 6.1f, 1.8f, 7.1f}, {5.0f, 9.0f, 2.4f, 9.5f}, {}}},
+    {{{3.2f, 6.0f, 0.9f, 6.0f}, {4.8f, 7.7f, 1.5f, 6.0f}, {}},
+     {{5.2f, 8.7f, 1.6f, 5.6f}, {8.0f, 9.9f, 3.0f, 7.0f}, {}},
+     {{11.2f, 9.1f, 3.6f, 7.6f}, {16.0f, 8.0f, 6.0f, 8.0f}, {}}}};
 
 // A walk over all tokens with wide slices reads and computes least. More workgroups come from narrower slices
 // (scores and weighted operands are computed once a slice) or from segments (k and v are read twice, two more
 // launches, the states' traffic): the cheapest of both by the measured times. 128 (batch, head)s of 128 x
-// 128, 2048 tokens, forward: slices of 64 97 to 107 us, of 128 107 to 110 us, two segments 122 us; gradients (three
-// walks): 290, 190 and 245 us. 16 of them, 65536 tokens: 16 or 32 segments with slices of 128 394 to 404 us, of 64 520
-// us, 8 segments 614 us.
+// 128, 2048 tokens, forward: slices of 64 109 us, of 128 132 us, two segments of those 139 us; gradients (three
+// walks): 329, 252 and 304 us. 16 of them, 65536 tokens: 32 segments with slices of 128 460 us, 16 486 us, 8 758 us; slices of 64
+// with 32 segments 552 us.
 MixPlan plan_of(const muon_mix* m, const muon_mix_grads* g, int cus) {
   MixPlan p;
   p.bh = m->batch * m->heads;
