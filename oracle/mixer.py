@@ -76,16 +76,17 @@ def sums32(tokens, dim, group=1):
     return (dim + 64 + 2 * (tokens // 64 + 1) + 262 + group + 32) * 2.0 ** -24
 
 
-def bounds(q, k, v, log_decay, scale, half_step, state=None, lengths=None, do=None, d_final=None):
+def bounds(q, k, v, log_decay, scale, half_step, state=None, lengths=None, do=None, d_final=None, operands=None):
     """Element-wise error bounds of (o, states), or with ``do`` of (dq, dk, dv, dstate). Every result
     is a sum of products; with 16-bit operands (half_step 2^-8) the terms inside a chunk may carry the rounding
-    of a score, those through the state the roundings of a weighted operand and of the state's
-    copy (all of 8 bits at worst: kernels that keep 16 of some stay well inside), and the result is rounded
-    once. States leave as sums of unrounded terms."""
+    of a score, those through the state that of the state's copy: ``operands`` bounds it, relative to the
+    term (None: two roundings of 8 bits). The result is rounded once. States leave as sums of unrounded terms."""
     a = lambda x: None if x is None else np.abs(np.asarray(x, np.float64))  # noqa: E731
     T, D = q.shape[1], max(q.shape[3], v.shape[3])
     c32 = sums32(T, D, q.shape[2] // k.shape[2])
-    rounded = c32 + (2.02 * half_step if half_step > 2.0 ** -24 else 0.0)
+    if operands is None:
+        operands = 2.02 * half_step
+    rounded = c32 + (operands if half_step > 2.0 ** -24 else 0.0)
     tiny = 1e-37
     if do is None:
         o, S = forward(q, k, v, log_decay, scale, state, lengths)

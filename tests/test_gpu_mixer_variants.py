@@ -1,0 +1,53 @@
+"""Every kernel of linear attention's walk against the float64 oracle, element by element, with the bounds of what
+the kernels round: scores and the state's copy to 16 bits, results once."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+from oracle import mixer as om  # noqa: E402
+from tests.gpu_util import TORCH_DT, to_np  # noqa: E402
+from tests.mixer_cases import CASES  # noqa: E402
+
+HALF_STEP = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def X():
+    from matrix_orthogonalising_optimizer_muon_amd import mixers
+    return mixers
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", CASES)
+def test_against_the_oracle(X, size, dtype):
+    B, T, H, kv, D, E = size
+    rng = np.random.default_rng([9, *size])
+    new = lambda *s: torch.from_numpy(rng.standard_normal(s, dtype=np.float32)).cuda()  # noqa: E731
+    q, k, v, do = (new(B, T, h, d).to(TORCH_DT[dtype]) for h, d in ((H, D), (kv, D), (kv, E), (H, E)))
+    g = torch.from_numpy(-np.geomspace(1.0, 3e-4, H).astype(np.float32)).cuda()
+    s, df = new(B, H, D, E) * 4.0, new(B, H, D, E) * 4.0
+    lens = torch.tensor([T - (7 * b) % 130 for b in range(B)], dtype=torch.int32, device="cuda")
+    f, h = float(np.float32(1.0 / np.sqrt(D))), HALF_STEP[dtype]
+    kw = dict(state=s, lengths=lens)
+    o, last = X.linear_attention_forward(q, k, v, g, **kw, final=True)
+    dq, dk, dv, ds = X.linear_attention_backward(do, q, k, v, g, **kw, d_final=df, need_dstate=True)
+    group = H // kv
+    for b, j in {(0, 0), (B // 2, kv // 2), (B - 1, kv - 1)}:
+        n, at = int(lens[b]), slice(j * group, (j + 1) * group)
+        mine = lambda t, heads: to_np(t[b:b + 1, :n, heads])  # noqa: E731
+        a = (mine(q, at), mine(k, slice(j, j + 1)), mine(v, slice(j, j + 1)), to_np(g[at]), f)
+        ndo, ns, ndf = mine(do, at), to_np(s[b:b + 1, at]), to_np(df[b:b + 1, at])
+        # two parts of 8 bits: wrong by at most 2^-17 of itself, and as much again for the product of two such
+        kw = dict(state=ns, operands=2.0 ** -16)
+        want = (*om.forward(*a, ns), *om.backward(ndo, *a, ns, None, ndf))
+        limit = (*om.bounds(*a, h, **kw), *om.bounds(*a, h, do=ndo, d_final=ndf, **kw))
+        got = (mine(o, at), to_np(last[b:b + 1, at]), mine(dq, at), mine(dk, slice(j, j + 1)), mine(dv, slice(j, j + 1)),
+               to_np(ds[b:b + 1, at]))
+        for x, r, e, name in zip(got, want, limit, ("o", "states", "dq", "dk", "dv", "dstate")):
+            bad = ~(np.abs(x - r) <= e)
+            assert not bad.any(), (name, b, j, int(bad.sum()), np.argwhere(bad)[:3].tolist(), x[bad][:3], r[bad][:3], e[bad][:3])
+    for b in range(B):
+        assert all(bool((t[b, int(lens[b]):] == 0).all()) for t in (o, dq, dk, dv))
