@@ -22,7 +22,7 @@ struct MixArray {
 };
 struct MixRole {
   MixArray a, b, c;
-  void* out;              // contiguous batch x tokens x heads x dim_v; null: the last state alone is wanted
+  void* out;              // contiguous batch x tokens x heads x dim_v (walks with outputs)
   int32_t out_f32;        // fp32 whatever the operands' type (one of several partial sums)
   int32_t dim, dim_v;
   int32_t reversed;

@@ -389,15 +389,18 @@ int muon_mix_backward(muon_ctx* ctx, const muon_mix* m, const muon_mix_grads* g,
       r.z_row = 1;
       r.z_col = m->dim_v;
     }
+    MixParams alone = p;                         // d_state without dv: the walk that makes no outputs
+    alone.roles = alone.per = 0;
     if (g->dv || g->d_state) {
-      MixRole& r = add(p, pl, k, q, d_o, !g->dv ? nullptr : group > 1 ? static_cast<void*>(ws + pl.off_dv) : g->dv, m->dim, m->dim_v);
+      MixRole& r = add(g->dv ? p : alone, pl, k, q, d_o, !g->dv ? nullptr : group > 1 ? static_cast<void*>(ws + pl.off_dv) : g->dv, m->dim, m->dim_v);
       r.out_f32 = group > 1;
       r.reversed = 1;
       r.p_scale = r.u_scale = m->scale;
       r.z_in = pl.segments > 1 ? zr : g->d_final;
       r.z_out = g->d_state;
     }
-    MUON_HIP(walk(f32, pl, true, p, st));
+    if (p.roles > 0) MUON_HIP(walk(f32, pl, true, p, st));
+    if (alone.roles > 0) MUON_HIP(walk(f32, pl, false, alone, st));
     if (group > 1 && m->tokens > 0 && (g->dk || g->dv)) {
       MixShare s;
       std::memset(&s, 0, sizeof(s));

@@ -759,7 +759,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
       // After the next chunk's loads are in: waiting for those does not wait for these stores. A lane holds
       // columns 16 t + 4 g .. + 3 of its token.
       const int64_t o_tok = o_at + token(r0 + i_tok) * o_row;
-      if (o.out && r0 + i_tok < live) {
+      if (r0 + i_tok < live) {
         if (F32 || o.out_f32) {
 #pragma unroll
           for (int t = 0; t < TILES; ++t) {
@@ -792,7 +792,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (OUT || Layout<F32, DP, NV, OUT, D
     }
     // rows behind the last token: zeros
     const int first = max(live, begin);
-    const int64_t count = o.out ? static_cast<int64_t>(end - first) * cols : 0;
+    const int64_t count = static_cast<int64_t>(end - first) * cols;
     for (int64_t x = tid; x < count; x += 256) {
       const int64_t w = o_at + (first + x / cols) * o_row + x % cols;
       if (F32 || o.out_f32) static_cast<float*>(o.out)[w] = 0.0f;

@@ -51,3 +51,21 @@ def test_against_the_oracle(X, size, dtype):
             assert not bad.any(), (name, b, j, int(bad.sum()), np.argwhere(bad)[:3].tolist(), x[bad][:3], r[bad][:3], e[bad][:3])
     for b in range(B):
         assert all(bool((t[b, int(lens[b]):] == 0).all()) for t in (o, dq, dk, dv))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [(1, 1, 2, 1, 16, 16), (3, 150, 4, 2, 64, 40), (1, 1500, 4, 2, 126, 127), (1, 1500, 4, 2, 128, 128), (16, 330, 4, 4, 250, 256)])
+def test_the_states_gradient_without_that_of_v(X, size, dtype):
+    """Made by a walk without outputs: the same sums."""
+    B, T, H, kv, D, E = size
+    q, k, v, do = (torch.randn(B, T, h, d, device="cuda").to(TORCH_DT[dtype]) for h, d in ((H, D), (kv, D), (kv, E), (H, E)))
+    g = torch.linspace(-0.5, -0.001, H, device="cuda")
+    s, df = torch.randn(B, H, D, E, device="cuda"), torch.randn(B, H, D, E, device="cuda")
+    lens = torch.tensor([max(T - 70 * b, 0) for b in range(B)], dtype=torch.int32, device="cuda")
+    a, ns = [to_np(t) for t in (q, k, v, g)], lens.tolist()
+    f = float(np.float32(1.0 / np.sqrt(D)))
+    want = om.backward(to_np(do), *a, f, to_np(s), ns, to_np(df))[3]
+    limit = om.bounds(*a, f, HALF_STEP[dtype], to_np(s), ns, to_np(do), to_np(df))[3]
+    for need in ((False, False, False), (True, False, False), (False, True, False), (True, True, False)):
+        got = X.linear_attention_backward(do, q, k, v, g, state=s, lengths=lens, d_final=df, need=need, need_dstate=True)
+        assert np.all(np.abs(to_np(got[3]) - want) <= limit), need
