@@ -236,8 +236,9 @@ __device__ __forceinline__ void products(f32x4 (&acc)[T], int i0, const u32x4 (&
       if ((i0 + i) % INNER == s) mma<F32>(acc[(i0 + i) / INNER], f[i], b[s]);
 }
 
-// e^{g n}, n > 0, the same for a wave, as a sum of two: a state is multiplied with the same power chunk after chunk, so that one fp32 number's
-// rounding would add up over them (by 24 chunks to as much as all other roundings of the state).
+// e^{g n}, n > 0, the same for a wave, as a sum of two: a state is multiplied with the same power chunk after chunk or
+// token after token, so that one fp32 number's rounding would add up over them (by 24 chunks to as much as all other roundings
+// of the state).
 struct Power {
   float whole, rest;
 };
@@ -905,7 +906,7 @@ __global__ __launch_bounds__(256) void mix_step(const MixStep p) {
   }
   const int across = tid % p.lanes, down = tid / p.lanes, rows = 256 / p.lanes;
   const int e = (blockIdx.y * p.lanes + across) * 4;
-  const float decay = __builtin_amdgcn_exp2f(p.log_decay[h] * kLog2e);
+  const Power decay = power(p.log_decay[h], 1);                 // token after token the same
   const int left = down < rows ? p.dim_v - e : 0;
   const int skip = left >= 4 ? 0 : 4 - left;                    // of the four columns from e - skip on: a neighbour's
   const bool four = left > 0 && p.dim_v >= 4;
@@ -934,7 +935,7 @@ __global__ __launch_bounds__(256) void mix_step(const MixStep p) {
       for (int u = 0; u < U; ++u) {
         const int d = d0 + u * rows;
         if (d >= p.dim) break;
-        s[u] = s[u] * decay + v * qk[1][d];
+        s[u] = s[u] * decay.whole + (s[u] * decay.rest + v * qk[1][d]);
         acc += s[u] * qk[0][d];
         float* z = p.z_out + at + static_cast<int64_t>(d) * p.dim_v;
         if (skip == 0) {

@@ -121,3 +121,19 @@ def test_a_state_that_leaves_changes_no_other_result(X, size, dtype):
         a = X.linear_attention_backward(do, q, k, v, g, **kw, d_final=df)
         b = X.linear_attention_backward(do, q, k, v, g, **kw, d_final=df, need_dstate=True)
         assert all(torch.equal(x, y) for x, y in zip(a[:3], b[:3]))
+
+
+def test_decay_does_not_drift_over_many_steps(X):
+    """2048 tokens of zeros leave e^{2048 g} of a state. A rounding a step, as likely up as down: 0.42 sqrt(2048) = 19 steps of
+    2^-24 in the norm, and 1.5 times that for the powers' rests; a decay of one fp32 number is wrong by up to a
+    half step the same way every time, 1024 steps in the end."""
+    n = 2048
+    g = torch.tensor([-1e-4, -3e-4, -7e-4, -1.1e-3], device="cuda")
+    q, k, v = torch.zeros(1, 4, 32, device="cuda"), torch.zeros(1, 4, 32, device="cuda"), torch.zeros(1, 4, 64, device="cuda")
+    s0 = torch.randn(1, 4, 32, 64, device="cuda")
+    s = s0.clone()
+    for _ in range(n):
+        X.linear_attention_step(q, k, v, g, s)
+    for h in range(4):
+        want = to_np(s0[0, h]) * np.exp(float(g[h]) * n)
+        assert rel(to_np(s[0, h]), want) <= 1.5 * 0.42 * np.sqrt(n) * 2.0 ** -24, h
