@@ -201,7 +201,7 @@ __device__ __forceinline__ int pieces_of(int dim, int vec, int most) {
 }
 
 // xs[slots[f]] = x[t]: a token's row is read once and written for each choice; a row behind the
-// last expert's is written as zeros by the choice of its number. The same sizes: 50 us, 6.0 TB/s.
+// last expert's is written as zeros by the choice of its number. The sizes below: 52 to 58 us, 5.2 to 5.8 TB/s.
 template <bool F32>
 __global__ __launch_bounds__(256) void rows_dispatch(const RowsParams p) {
   using R = Row<F32>;

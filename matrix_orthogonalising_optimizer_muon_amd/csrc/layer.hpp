@@ -30,7 +30,6 @@ struct MixRole {
   const float* z_in;      // null: zeros. One dim x dim_v array per (batch, head) and segment
   int64_t z_row, z_col;   // its strides
   float* z_out;           // null: not wanted. Contiguous rows
-  int32_t slices;         // parts of dim_v
   int32_t first;          // index of its first workgroup among a (batch, head, segment)'s
 };
 struct MixParams {
@@ -41,7 +40,7 @@ struct MixParams {
   const int32_t* lengths; // null: tokens
   int32_t batch, heads, tokens;
   int32_t segments, segment;  // number, tokens of one (a multiple of the chunk)
-  int32_t direct;             // every operand's rows are 16-byte aligned, apart, and a chunk's span 31 bits of bytes
+  int32_t direct;             // every operand's rows are 16-byte aligned, apart, and a chunk spans at most 2^29 bytes
   int32_t walked;             // segments walked: all, or without the last one
   int32_t z_in_per_segment;   // z_in has an array for each segment, else one for the first
   int32_t z_out_per_segment;  // z_out too (a segment's own sum), else one from the last token's segment
@@ -83,7 +82,7 @@ struct PlanParams {
   int64_t n;                             // choices: tokens x top
   int32_t experts, blocks;
   int32_t *order, *slots, *offsets;
-  int32_t* counts;                       // blocks x (experts + 1): a block's choices by expert, then their first place
+  int32_t* counts;                       // blocks x (experts + 1): a block's choices by expert
 };
 hipError_t launch_expert_plan(const PlanParams& p, hipStream_t st);
 struct RowsParams {

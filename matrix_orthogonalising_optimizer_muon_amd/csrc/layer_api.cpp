@@ -75,7 +75,6 @@ int validate(const muon_mix* m, const muon_mix_grads* g) {
 struct MixPlan {
   MixTile tile{64, 64};
   int64_t bh = 0;
-  int per = 1;                  // workgroups of a (batch, head, segment)
   int segments = 1, segment = kMixChunk;
   size_t off_rev = 0, off_dk = 0, off_dv = 0, bytes = 0;  // workspace: states, states of the reversed walk, partial dk, dv
 };
@@ -138,7 +137,6 @@ MixPlan plan_of(const muon_mix* m, const muon_mix_grads* g, int cus) {
       if (us < best) {
         best = us;
         p.tile.dim_v = nv;
-        p.per = static_cast<int>(per);
         p.segment = static_cast<int>(each * kMixChunk);
         p.segments = static_cast<int>(segments);
       }
@@ -162,7 +160,7 @@ MixPlan plan_of(const muon_mix* m, const muon_mix_grads* g, int cus) {
 MixArray array(const void* p, const int64_t (&s)[3], int group) { return {p, s[0], s[1], s[2], group}; }
 
 // Whether the direct loads can take an array: rows of whole 16-byte pieces at 16-byte addresses that do not
-// overlap, a chunk of them within 2^29 bytes.
+// overlap, a chunk of them within 2^29 bytes (the kernels' offsets and their marker of what lies outside need that).
 bool direct(const MixArray& a, int dim, int64_t es) {
   const int64_t tok = a.st * es;
   return aligned(a.p, 16) && a.sb * es % 16 == 0 && tok % 16 == 0 && a.sh * es % 16 == 0 && dim * es % 16 == 0 &&
@@ -190,9 +188,8 @@ MixRole& add(MixParams& p, const MixPlan& pl, const MixArray& a, const MixArray&
   r.dim = dim; r.dim_v = dim_v;
   r.p_scale = r.o_scale = r.u_scale = 1.0f;
   r.z_row = dim_v; r.z_col = 1;
-  r.slices = static_cast<int32_t>(cdiv(dim_v, pl.tile.dim_v));
   r.first = p.per;
-  p.per += r.slices;
+  p.per += static_cast<int32_t>(cdiv(dim_v, pl.tile.dim_v));   // its slices
   return r;
 }
 

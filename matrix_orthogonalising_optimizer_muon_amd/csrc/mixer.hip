@@ -280,7 +280,8 @@ struct Layout {
 // more make the outputs (16 of a chunk's tokens each): a SIMD then has one of either, whose matrix
 // instructions, conversions and LDS reads fill each other's gaps. They meet once a chunk, and once more where the state's
 // copy has one place: the outputs' waves read it first, the state's waves meet them halfway through their own products.
-// DIRECT: operands whose rows are 16-byte aligned and not more than 2^31 bytes apart in a chunk go global -> LDS
+// DIRECT: operands whose rows are 16-byte aligned and not more than 2^29 bytes apart in a chunk (OUTSIDE below, less a reversed
+// chunk's span, has to stay behind the buffer's end) go global -> LDS
 // by the direct loads, issued by the state's waves up to two chunks ahead, zeros past the last row and
 // column by the buffer's bounds; else all waves bring the next chunk's through registers.
 template <bool F32, int DP, int NV, bool OUT, bool DIRECT>

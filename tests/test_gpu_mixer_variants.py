@@ -69,3 +69,21 @@ def test_the_states_gradient_without_that_of_v(X, size, dtype):
     for need in ((False, False, False), (True, False, False), (False, True, False), (True, True, False)):
         got = X.linear_attention_backward(do, q, k, v, g, state=s, lengths=lens, d_final=df, need=need, need_dstate=True)
         assert np.all(np.abs(to_np(got[3]) - want) <= limit), need
+
+
+@pytest.mark.parametrize("apart", [1 << 22, (1 << 22) + 8])
+def test_rows_as_far_apart_as_direct_loads_go(X, apart):
+    """Chunks that span 2^29 bytes, the most that goes through buffers, and a little more, which does not."""
+    if torch.cuda.mem_get_info()[0] < (8 << 30):
+        pytest.skip("needs 8 GB")
+    T, D = 100, 40
+    q, k, v, do = (torch.randn(1, T, 1, D, device="cuda").bfloat16() for _ in range(4))
+    g, lens = torch.tensor([-0.05], device="cuda"), torch.tensor([T - 7], dtype=torch.int32, device="cuda")
+    far = torch.full(((T - 1) * apart + D,), float("nan"), dtype=torch.bfloat16, device="cuda").as_strided((1, T, 1, D), (0, apart, 0, 1))
+
+    def results(k):
+        o, s = X.linear_attention_forward(q, k, v, g, lengths=lens, final=True)
+        return (o, s, *X.linear_attention_backward(do, q, k, v, g, lengths=lens, need_dstate=True))
+    want = results(k)
+    far[:, :T - 7].copy_(k[:, :T - 7])
+    assert all(torch.equal(a, b) for a, b in zip(results(far), want))
