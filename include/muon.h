@@ -518,7 +518,7 @@ int muon_distill_loss(muon_ctx *ctx, const muon_logits *l, const muon_distill *t
  * An infinity or NaN reaches what the formulas say, an infinity possibly as NaN. Computed in chunks of 64 tokens.
  * MUON_BF16: products on the bf16 matrix instructions with fp32 sums; scores and the copy of the
  * state that q is multiplied with are operands of 16 bits, states fp32 sums of unrounded terms. MUON_F32: fp32
- * throughout.
+ * throughout. How a call is divided goes by its sizes and the wanted gradients, which can change fp32 sums' last bits.
  * batch and batch x heads up to 2^18, heads to 2^16, tokens to 2^24, dim and dim_v in [1, 256]. */
 #define MUON_MIX_MAX_DIM 256
 typedef struct muon_mix {

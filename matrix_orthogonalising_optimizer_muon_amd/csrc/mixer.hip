@@ -16,19 +16,20 @@
 // the operand of the product with v without leaving the lane.
 //
 // Bound by HBM in bf16 with enough workgroups, by the latency of a chunk's chain with few, by the fp32
-// matrix instructions in fp32. MI355X, 8 x 2048 tokens, 16 heads of 128, bf16: forward 84 to 101 us for 268 MB (2.7 to 3.2 TB/s;
-// loads and stores alone 65 us, the products alone 72 us), the three gradients 170 to 190 us: 444 MB read, 197 MB
-// written (3.4 to 3.8 TB/s), 384 workgroups of 32 chunks on 256 CUs. A 65536-token prompt of 16 heads: 120 to 140 us for
-// the segments' states, 230 to 290 us for the outputs.
-// In these kernels the matrix units are busy for 30 to 41% of the cycles, vector instructions run in 40 to 48%, and
-// 17 to 19% of the LDS cycles are lost to bank conflicts.
+// matrix instructions in fp32. MI355X, 8 x 2048 tokens, 16 heads of 128, bf16: forward 100 us for 268 MB (2.7 TB/s;
+// loads and stores alone 65 us), the three gradients 240 to 255 us: 443 MB read, 197 MB
+// written (2.6 TB/s), 384 workgroups of 32 chunks on 256 CUs. A 65536-token prompt of 16 heads: 156 to 195 us for
+// the segments' states, 293 to 354 us for the outputs.
+// In these kernels the matrix units are busy for 30 to 38% of the cycles, vector instructions run in 44 to 53%, and
+// 19 to 20% of the LDS cycles are lost to bank conflicts (none in the states' walk).
 //
 // Steps (forward / gradients of that case, us; the sizes' first kernel took 225 / 425): state and outputs on waves of
 // their own, one barrier a chunk 135 / 254; stores after the next chunk's loads 120 / 219; direct loads two
 // chunks ahead, XOR-ordered rows, no spills 82 / 165 with one weighted part; then 13 and 20 us for
-// accuracy: two weighted parts (now three), scores and the state's copy in two parts, which take the error against 64 bits from 1.4
-// (1.65 in gradients) to 1.0 times that of fp32 throughout. The copy's second part at 128 x 128 and 256 x 64 came later
-// and costs the gradients of that case a fifth.
+// accuracy: two weighted parts, scores and the state's copy in two parts, which take the error against 64 bits from 1.4
+// (1.65 in gradients) to 1.0 times that of fp32 throughout. Then the copy's second part at 128 x 128 and 256 x 64
+// as well (gradients 173 -> 226), three weighted parts (-> 243), a chunk's sum apart from the state (+ 3), infinities
+// and NaN kept to their tokens (+ 6; forward 98 -> 103).
 #include "layer.hpp"
 #include "mfma_util.hpp"
 

@@ -178,7 +178,8 @@ class RoutedFeedForward(torch.nn.Module):
     """A layer's feed-forward blocks behind a router: each token goes to the ``top`` experts of the
     largest scores x router^T, weighted by the softmax over those. ``router`` and the experts'
     ``gate``, ``up`` and ``down`` are matrices that ``MuonWithAdamW`` routes to the Muon update.
-    A call waits for the number of each expert's tokens, which sizes the blocks' products."""
+    A call waits for the number of each expert's tokens, which sizes the blocks' products, so it cannot be captured
+    into a graph."""
 
     def __init__(self, dim: int, hidden: int, experts: int, top: int, *, activation: str = "silu", device=None,
                  dtype=torch.bfloat16):
